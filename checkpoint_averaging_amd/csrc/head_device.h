@@ -26,15 +26,27 @@ template <> __device__ __forceinline__ bf16 from_f32<bf16>(float v) {
 
 // kVec elements of one row in one 128-bit access.  Rows start at any element
 // (odd leading dimensions), so the access is declared aligned to an element
-// only: the hardware takes global accesses at any such address.
+// only: the hardware takes global accesses at any such address.  NT: without
+// a stay in the caches.
 template <typename T> struct Vec;
 
 template <> struct Vec<float> {
     static constexpr int n = 4;
     typedef float raw __attribute__((ext_vector_type(4), aligned(4)));
+    template <bool NT = false> static __device__ __forceinline__ raw load(const float* p) {
+        const raw* q = reinterpret_cast<const raw*>(p);
+        if constexpr (NT) return __builtin_nontemporal_load(q);
+        else return *q;
+    }
+    template <bool NT = false> static __device__ __forceinline__ void store(float* p, raw v) {
+        raw* q = reinterpret_cast<raw*>(p);
+        if constexpr (NT) __builtin_nontemporal_store(v, q);
+        else *q = v;
+    }
     static __device__ __forceinline__ void unpack(const raw& r, float* v) {
         for (int i = 0; i < n; ++i) v[i] = r[i];
     }
+    static __device__ __forceinline__ void unpack4(const raw& r, int, float* v) { unpack(r, v); }
     static __device__ __forceinline__ raw pack(const float* v) {
         raw r;
         for (int i = 0; i < n; ++i) r[i] = v[i];
@@ -45,11 +57,29 @@ template <> struct Vec<float> {
 template <> struct Vec<bf16> {
     static constexpr int n = 8;
     typedef uint32_t raw __attribute__((ext_vector_type(4), aligned(2)));
+    template <bool NT = false> static __device__ __forceinline__ raw load(const bf16* p) {
+        const raw* q = reinterpret_cast<const raw*>(p);
+        if constexpr (NT) return __builtin_nontemporal_load(q);
+        else return *q;
+    }
+    template <bool NT = false> static __device__ __forceinline__ void store(bf16* p, raw v) {
+        raw* q = reinterpret_cast<raw*>(p);
+        if constexpr (NT) __builtin_nontemporal_store(v, q);
+        else *q = v;
+    }
     static __device__ __forceinline__ void unpack(const raw& r, float* v) {
         for (int i = 0; i < 4; ++i) {
             v[2 * i] = __uint_as_float(r[i] << 16);
             v[2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
         }
+    }
+    // the four from 4h on
+    static __device__ __forceinline__ void unpack4(const raw& r, int h, float* v) {
+        const uint32_t a = h == 0 ? r[0] : r[2], b = h == 0 ? r[1] : r[3];
+        v[0] = __uint_as_float(a << 16);
+        v[1] = __uint_as_float(a & 0xFFFF0000u);
+        v[2] = __uint_as_float(b << 16);
+        v[3] = __uint_as_float(b & 0xFFFF0000u);
     }
     static __device__ __forceinline__ raw pack(const float* v) {
         raw r;
@@ -60,20 +90,59 @@ template <> struct Vec<bf16> {
     }
 };
 
-// Reductions over a wavefront: every lane gets the result (the same pairing,
-// so the same bits, in every lane).
-template <typename T> __device__ __forceinline__ T wave_sum(T v) {
-    for (int o = kWave / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
-    return v;
+// Reductions over a wavefront; every lane gets the result.  Within rows of 16
+// lanes values move by DPP (no LDS), in a fixed pairing that gives every lane
+// of a row the same bits; the four rows' are read as scalars.
+template <int CTRL> __device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return static_cast<uint32_t>(
+        __builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xF, 0xF, true));
+}
+template <int CTRL> __device__ __forceinline__ float dpp(float v) {
+    return __uint_as_float(dpp<CTRL>(__float_as_uint(v)));
+}
+template <int CTRL> __device__ __forceinline__ double dpp(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint64_t lo = dpp<CTRL>(static_cast<uint32_t>(u));
+    const uint64_t hi = dpp<CTRL>(static_cast<uint32_t>(u >> 32));
+    return __builtin_bit_cast(double, lo | (hi << 32));
+}
+__device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) {
+    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), lane));
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {
+    return __uint_as_float(lane_value(__float_as_uint(v), lane));
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint64_t lo = lane_value(static_cast<uint32_t>(u), lane);
+    const uint64_t hi = lane_value(static_cast<uint32_t>(u >> 32), lane);
+    return __builtin_bit_cast(double, lo | (hi << 32));
 }
 
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-    for (int o = kWave / 2; o > 0; o >>= 1) {
-        const uint32_t u = __shfl_xor(v, o);
-        v = u > v ? u : v;
+struct Sum {
+    template <typename T> __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
+};
+struct Max {
+    __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const {
+        return a > b ? a : b;
     }
+    __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+
+// over 2, 4, 8 or 16 neighbouring lanes
+template <int N, typename T, typename Op> __device__ __forceinline__ T lanes_reduce(T v, Op op) {
+    if constexpr (N >= 2) v = op(v, dpp<0xB1>(v));     // lanes 1 0 3 2
+    if constexpr (N >= 4) v = op(v, dpp<0x4E>(v));     // lanes 2 3 0 1
+    if constexpr (N >= 8) v = op(v, dpp<0x141>(v));    // halves of a row mirrored
+    if constexpr (N >= 16) v = op(v, dpp<0x140>(v));   // rows mirrored
     return v;
 }
+template <typename T, typename Op> __device__ __forceinline__ T wave_reduce(T v, Op op) {
+    v = lanes_reduce<16>(v, op);
+    return op(op(lane_value(v, 0), lane_value(v, 16)), op(lane_value(v, 32), lane_value(v, 48)));
+}
+template <typename T> __device__ __forceinline__ T wave_sum(T v) { return wave_reduce(v, Sum{}); }
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) { return wave_reduce(v, Max{}); }
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 

@@ -3,10 +3,11 @@
 //
 // With m the row's largest element, d = l - m and e = exp(d):
 //   log p = d - log S, S = sum e ;  H = log S - sum(e d) / S
-// One pass keeps, against a running maximum, S, the sum R of every e below 1
-// and t = sum(e d).  Where S is below 1.5 there is one maximum and S = 1 + R, so
-// log S = log1p(R): a nearly certain token's log probability and entropy keep
-// their digits, which log(1 + R) would lose.
+// One pass keeps S and t = sum(e d) against a running maximum.  Where S is below
+// 1.5 there is one maximum and S = 1 + R; log S is then log1p(R), so that a
+// nearly certain token's log probability and entropy keep their digits.  R
+// comes from the threads' sums but for the one that the maximum's own 1 went
+// through: its elements (one 256th of the row) are read once more.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -23,12 +24,27 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kUnroll = 4;          // 16-byte loads a thread has under way
+constexpr int kTogether = 2;        // of these, vectors whose maximum is taken together
 constexpr int64_t kMaxGrid = 1 << 20;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLowest = -3.40282347e38f;
 constexpr float kFar = -1e4f;       // exp of this and of anything below is 0
-constexpr int kMaxParts = 32;
-constexpr int kList = kThreads * 8 + kThreads;   // candidates held at once (see choose)
+constexpr int kMaxParts = 16;
+constexpr int kAdded = 1024;        // most candidates added between two looks at the list
+constexpr int kList = kAdded + 256; // candidates held at once (see choose)
+constexpr int kKeys = 256;          // maxima that bound the alternatives
+
+// Logits of more than this stream past the 256 MB Infinity Cache without a
+// stay in it (2048 x 73760 bf16, 302 MB: 57 us, 61 us with ordinary loads);
+// fewer may be there still, or be wanted again by the backward pass (180 x
+// 73760 fp32, 53 MB: 15 us, 20 us non-temporally).  Alternatives are read
+// again, so their rows are loaded in the ordinary way.
+constexpr int64_t kNontemporalMin = int64_t(192) << 20;
+
+template <int N> struct Count {
+    static constexpr int value = N;
+    __device__ constexpr operator int() const { return N; }
+};
 
 // exp(d) for d <= 0; NaN stays NaN.
 __device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
@@ -38,7 +54,8 @@ __device__ __forceinline__ float minus_inf() { return __uint_as_float(0xFF800000
 
 // Running statistics of the elements seen so far.  The first maximum is the
 // lowest finite value: an element of -infinity then adds exp(-infinity) = 0,
-// one of +infinity or NaN turns S into NaN.
+// one of +infinity or NaN turns S into NaN.  r is the sum without the (single)
+// maximum, where S is below 1.5.
 struct Stats {
     float m, s, r, t;
 
@@ -51,35 +68,33 @@ struct Stats {
         const float d = fmaxf(m - m2, kFar), a = exp_of(d);
         t = a * (t + d * s);
         s *= a;
-        r = s;
         m = m2;
     }
     // Adds an element that is not above the maximum.
     template <bool ENTROPY> __device__ __forceinline__ void add(float l) {
         const float d = l - m, e = exp_of(d);
         s += e;
-        r += __builtin_amdgcn_fractf(e);      // e if below 1, 0 at the maximum itself
         if constexpr (ENTROPY) t = __builtin_fmaf(e, fmaxf(d, kFar), t);
     }
-    __device__ __forceinline__ void merge(Stats o) {
-        if (o.m > m) raise(o.m);
-        else if (m > o.m) o.raise(m);
-        s += o.s;
-        r += o.r;
-        t += o.t;
+    // The same elements against a maximum m2 >= m.
+    __device__ __forceinline__ Stats at(float m2) const {
+        const float d = fmaxf(m - m2, kFar), a = exp_of(d);
+        return m == m2 ? *this : Stats{m2, a * s, a * s, a * (t + d * s)};
     }
-    __device__ __forceinline__ Stats shuffled(int o) const {
-        Stats q;
-        q.m = __shfl_xor(m, o);
-        q.s = __shfl_xor(s, o);
-        q.r = __shfl_xor(r, o);
-        q.t = __shfl_xor(t, o);
-        return q;
+    // The statistics of 16 neighbouring lanes, or of the wave (without r), in one.
+    __device__ __forceinline__ Stats of_lanes() const {
+        const Stats q = at(lanes_reduce<16>(m, Max{}));
+        return Stats{q.m, lanes_reduce<16>(q.s, Sum{}), lanes_reduce<16>(q.r, Sum{}),
+                     lanes_reduce<16>(q.t, Sum{})};
+    }
+    __device__ __forceinline__ Stats of_wave() const {
+        const Stats q = at(wave_reduce(m, Max{}));
+        return Stats{q.m, wave_sum(q.s), 0.0f, wave_sum(q.t)};
     }
     __device__ __forceinline__ bool nothing() const { return s == 0.0f; }
+    __device__ __forceinline__ bool nearly_certain() const { return s < 1.5f && s > 0.0f; }
     __device__ __forceinline__ float log_sum() const {
-        if (nothing()) return 0.0f;
-        return s < 1.5f ? log1pf(r) : logf(s);
+        return nothing() ? 0.0f : nearly_certain() ? log1pf(r) : logf(s);
     }
 };
 
@@ -91,8 +106,8 @@ __device__ __forceinline__ uint32_t order_of(float l) {
     const uint32_t b = __float_as_uint(v);
     return v != v ? 0xFFFFFFFFu : (b >> 31) != 0 ? ~b : b | 0x80000000u;
 }
-__device__ __forceinline__ uint64_t key_of(uint32_t order, int64_t i) {
-    return (static_cast<uint64_t>(order) << 32) | (0x7FFFFFFFu - static_cast<uint32_t>(i));
+__device__ __forceinline__ uint64_t key_of(uint32_t order, uint32_t i) {
+    return (static_cast<uint64_t>(order) << 32) | (0x7FFFFFFFu - i);
 }
 __device__ __forceinline__ int64_t index_of(uint64_t key) {
     return 0x7FFFFFFFu - static_cast<uint32_t>(key);
@@ -110,25 +125,53 @@ __device__ __forceinline__ float logprob_of(float l, const Stats& st, float log_
 struct TopLds {
     uint64_t list[kList];
     uint64_t best[DL_MAX_TOP];
-    uint32_t key[kThreads];
-    int cand[kThreads];
+    uint32_t key[kKeys];
+    int cand[kKeys];
     int count, cands;
     uint32_t least;
 };
 
 // best[0..k) = the k largest of the `count` distinct keys of list[], largest
 // first; 0 where there are fewer.  An element's place is the number of larger
-// ones.
+// ones, counted four keys at a time (list[count..] is filled up with 0).
 __device__ __forceinline__ void rank_select(TopLds& s, int count, int k) {
+    const int padded = (count + 3) / 4 * 4;
+    if (threadIdx.x < static_cast<unsigned>(padded - count)) s.list[count + threadIdx.x] = 0;
     if (threadIdx.x < static_cast<unsigned>(k)) s.best[threadIdx.x] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < count; i += kThreads) {
         const uint64_t q = s.list[i];
         int rank = 0;
-        for (int j = 0; j < count; ++j) rank += s.list[j] > q;
+        for (int j = 0; j < padded; j += 4) {
+            ulonglong2 o[2];
+            for (int u = 0; u < 2; ++u)
+                o[u] = *reinterpret_cast<const ulonglong2*>(&s.list[j + 2 * u]);
+            for (int u = 0; u < 2; ++u) rank += (o[u].x > q) + (o[u].y > q);
+        }
         if (rank < k) s.best[rank] = q;
     }
     __syncthreads();
+}
+
+// A lower bound of the k-th largest of the 256 numbers key[]: its upper BITS
+// bits, from the highest down.  A bit belongs to it if k numbers reach it; the
+// scalar unit counts them from a compare's mask.  The first wave finds it for
+// all (the others' vector units are left to other workgroups).
+template <int BITS> __device__ __forceinline__ uint32_t kth_bound(TopLds& s, int k) {
+    static_assert(kKeys == 4 * kWave, "four numbers a lane");
+    if (threadIdx.x < kWave) {
+        const uint4 q = reinterpret_cast<const uint4*>(s.key)[threadIdx.x];
+        uint32_t t = 0;
+        for (int bit = 31; bit >= 32 - BITS; --bit) {
+            const uint32_t u = t | (1u << bit);
+            const int c = __popcll(__ballot(q.x >= u)) + __popcll(__ballot(q.y >= u)) +
+                          __popcll(__ballot(q.z >= u)) + __popcll(__ballot(q.w >= u));
+            if (c >= k) t = u;
+        }
+        if (threadIdx.x == 0) s.least = t;
+    }
+    __syncthreads();
+    return s.least;
 }
 
 // best[0..k) of the elements [0, n) of l, whose index in the row is `first`
@@ -138,85 +181,93 @@ __device__ __forceinline__ void rank_select(TopLds& s, int count, int k) {
 // The k-th largest of the threads' maxima is a lower bound of the k-th largest
 // element, and only threads whose maximum reaches it hold elements that do:
 // about k threads' vectors are read once more (out of a cache), spread over
-// all threads.  Elements that reach the bound go to a list; when a round may
+// all threads.  Elements that reach the bound go to a list; where more might
 // overflow it, the list is cut to its k largest, whose last then is a bound
 // too (rows of many equal or ordered elements).
 template <typename T>
-__device__ __forceinline__ void choose(TopLds& s, const T* l, int64_t n, int64_t first, int k,
+__device__ __forceinline__ void choose(TopLds& s, const T* l, uint32_t n, uint32_t first, int k,
                                        const Stats& mine) {
     constexpr int NV = Vec<T>::n;
+    static_assert(kThreads == kKeys && kThreads * 4 == kAdded, "");
     const int tid = threadIdx.x;
-    // The thread's maximum, rounded down to make room for its number: distinct keys.
     uint32_t key = 0;                         // no elements
-    if (static_cast<int64_t>(tid) * NV < n)
+    if (static_cast<uint32_t>(tid * NV) < n)
         key = mine.s != mine.s ? 0xFF800000u  // NaN or +infinity: at least +infinity
               : mine.nothing() ? 0x007FFFFFu  // -infinity
                                : order_of(mine.m);
-    key = (key & ~0xFFu) | static_cast<uint32_t>(tid);
     s.key[tid] = key;
     if (tid == 0) s.count = s.cands = 0;
     __syncthreads();
-    int rank = 0;
-    for (int j = 0; j < kThreads; j += 4) {
-        const uint4 q = *reinterpret_cast<const uint4*>(&s.key[j]);
-        rank += (q.x > key) + (q.y > key) + (q.z > key) + (q.w > key);
-    }
-    if (rank == k - 1) s.least = key & ~0xFFu;
-    __syncthreads();
-    const uint32_t least = s.least;
-    if ((key & ~0xFFu) >= least) s.cand[atomicAdd(&s.cands, 1)] = tid;
+    const uint32_t least = kth_bound<sizeof(T) == 2 ? 16 : 20>(s, k);
+    if (key >= least) s.cand[atomicAdd(&s.cands, 1)] = tid;
     __syncthreads();
     const uint32_t cands = s.cands;
-    // (fewer than 2^31 / NV vectors, so whole numbers of 32 bits hold these)
-    const uint32_t vectors = static_cast<uint32_t>((n + NV - 1) / NV);
+    const uint32_t vectors = (n + NV - 1) / NV;
     const uint32_t steps = (vectors + kThreads - 1) / kThreads;
+    const uint32_t total = steps * cands;
+    auto load = [&](uint32_t p, uint32_t& at) {
+        typename Vec<T>::raw r{};
+        at = n;
+        if (p < total) at = (p / cands * kThreads + s.cand[p % cands]) * NV;
+        if (at + NV <= n) {
+            r = Vec<T>::load(l + at);
+        } else if (at < n) {                              // the row's last, partial vector
+            float x[NV];
+            for (int i = 0; i < NV; ++i) x[i] = at + i < n ? to_f32(l[at + i]) : 0.0f;
+            r = Vec<T>::pack(x);
+        }
+        return r;
+    };
+    uint32_t at;
+    typename Vec<T>::raw r = load(tid, at);
     uint64_t bound = 0;
-    for (uint32_t p0 = 0; p0 < steps * cands; p0 += kThreads) {
-        const uint32_t p = p0 + tid;
-        if (p < steps * cands) {
-            const int64_t at = static_cast<int64_t>(p / cands * kThreads + s.cand[p % cands]) * NV;
-            if (at < n) {
-                float x[NV];
-                if (at + NV <= n) {
-                    Vec<T>::unpack(*reinterpret_cast<const typename Vec<T>::raw*>(l + at), x);
-                } else {
-                    for (int i = 0; i < NV; ++i) x[i] = at + i < n ? to_f32(l[at + i]) : 0.0f;
-                }
-                for (int i = 0; i < NV; ++i) {
-                    const uint32_t o = order_of(x[i]);
-                    const uint64_t q = key_of(o, first + at + i);
-                    if (at + i < n && o >= least && q > bound) s.list[atomicAdd(&s.count, 1)] = q;
+#pragma unroll 1
+    for (uint32_t p0 = 0; p0 < total; p0 += kThreads) {
+        uint32_t next_at;
+        const typename Vec<T>::raw next = load(p0 + kThreads + tid, next_at);
+#pragma unroll 1
+        for (int h = 0; h < NV / 4; ++h) {                  // kAdded elements between two looks
+            float x[4];
+            Vec<T>::unpack4(r, h, x);
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t o = order_of(x[i]), e = at + 4 * h + i;
+                if (e < n && o >= least) {
+                    const uint64_t q = key_of(o, first + e);
+                    if (q > bound) s.list[atomicAdd(&s.count, 1)] = q;
                 }
             }
-        }
-        __syncthreads();
-        const int count = s.count;
-        __syncthreads();                      // read by all before the next round adds to it
-        if (count > kList - kThreads * NV) {
-            rank_select(s, count, k);
-            if (tid < k) s.list[tid] = s.best[tid];
-            bound = s.best[k - 1];
-            if (tid == 0) s.count = k;
             __syncthreads();
+            const int count = s.count;
+            __syncthreads();                                // read by all before more is added
+            if (count > kList - kAdded) {
+                rank_select(s, count, k);
+                if (tid < k) s.list[tid] = s.best[tid];
+                bound = s.best[k - 1];
+                if (tid == 0) s.count = k;
+                __syncthreads();
+            }
         }
+        r = next;
+        at = next_at;
     }
     rank_select(s, s.count, k);
 }
 
 // What a row is split into: `parts` workgroups of `chunk` elements each.
+//
+// A workgroup a row fills the GPU from about 300 rows on; fewer are split, as
+// long as a part has 4096 elements, and a second kernel joins the parts.
 struct Split {
-    int parts;
-    int64_t chunk;
+    uint32_t parts, chunk;
 };
 
 Split split_of(int64_t rows, int64_t vocab) {
-    const int64_t least = 4096;
-    int64_t parts = (1024 + rows - 1) / rows;
+    int64_t parts = rows < 512 ? 512 / rows : 1;
     parts = parts < kMaxParts ? parts : kMaxParts;
-    const int64_t most = (vocab + least - 1) / least;
+    const int64_t most = (vocab + 4095) / 4096;
     parts = parts < most ? parts : most;
     const int64_t chunk = ((vocab + parts - 1) / parts + 7) / 8 * 8;
-    return Split{static_cast<int>((vocab + chunk - 1) / chunk), chunk};
+    return Split{static_cast<uint32_t>((vocab + chunk - 1) / chunk), static_cast<uint32_t>(chunk)};
 }
 
 // A part's results in the workspace: its statistics, then its best keys.
@@ -248,19 +299,52 @@ __device__ __forceinline__ void write_row(const LogprobsArgs& a, int64_t row, co
     }
 }
 
+// R of a nearly certain row (or part), from the threads' own statistics
+// `mine`: the single maximum's thread counts by its elements, read again.
+template <typename T>
+__device__ __forceinline__ float rest_of(float* lds, int* owner, const T* l, uint32_t n,
+                                         const Stats& mine, const Stats& row) {
+    constexpr int NV = Vec<T>::n;
+    const int tid = threadIdx.x;
+    if (mine.m == row.m) *owner = tid;        // one thread: two would make S 2
+    __syncthreads();
+    float r = mine.m == row.m ? 0.0f : mine.s * exp_of(fmaxf(mine.m - row.m, kFar));
+    const uint32_t steps = (n + kThreads * NV - 1) / (kThreads * NV);
+    for (uint32_t j = tid; j < steps; j += kThreads) {
+        const uint32_t at = (j * kThreads + *owner) * NV;
+        for (uint32_t i = at; i < at + NV && i < n; ++i) {
+            const float x = to_f32(l[i]);
+            if (x != row.m) r += exp_of(x - row.m);
+        }
+    }
+    r = wave_sum(r);
+    if (tid % kWave == 0) lds[tid / kWave] = r;
+    __syncthreads();
+    return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+}
+
 // One workgroup a part of a row; with one part a row, the results themselves.
-template <typename T, bool ENTROPY, bool TOP>
-__global__ __launch_bounds__(kThreads) void k_logprobs(LogprobsArgs a, int parts, int64_t chunk) {
+// Eight workgroups a CU (64 vector registers, 80 scalar ones): 2048 rows are
+// then under way at once (2048 x 73760 bf16 with 20 alternatives: 78 us, 86 us
+// with six).
+template <typename T, bool ENTROPY, bool TOP, bool NT>
+__global__ __launch_bounds__(kThreads, 8) void k_logprobs(LogprobsArgs a, uint32_t parts, uint32_t chunk) {
     constexpr int NV = Vec<T>::n;
     typedef typename Vec<T>::raw raw;
     __shared__ Stats lds[kWaves];
+    __shared__ float lds_r[kWaves];
+    __shared__ int owner;
     __shared__ char top_lds[TOP ? sizeof(TopLds) : 1] __attribute__((aligned(16)));
     const int tid = threadIdx.x;
-    for (int64_t job = blockIdx.x; job < a.rows * parts; job += gridDim.x) {
-        const int64_t row = job / parts;
-        const int part = static_cast<int>(job - row * parts);
-        const int64_t first = part * chunk;
-        const int64_t n = a.vocab - first < chunk ? a.vocab - first : chunk;
+    // Fewer than 512 rows are in parts, so jobs, and all indices within a row
+    // (below 2^31), are whole numbers of 32 bits.
+    const uint32_t jobs = static_cast<uint32_t>(a.rows) * parts;
+    for (uint32_t job = blockIdx.x; job < jobs; job += gridDim.x) {
+        const uint32_t r0 = job / parts;
+        const int64_t row = r0;
+        const uint32_t first = (job - r0 * parts) * chunk;
+        const uint32_t left = static_cast<uint32_t>(a.vocab) - first;
+        const uint32_t n = left < chunk ? left : chunk;
         const T* whole = static_cast<const T*>(a.logits) + row * a.ld;
         const T* l = whole + first;
         int64_t target = -1;
@@ -270,36 +354,47 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobsArgs a, int parts
             if (target >= 0 && target < a.vocab) target_logit = to_f32(whole[target]);
         }
         Stats st = Stats::none();
-        const int64_t full = n / NV;              // whole vectors
-        int64_t v = tid;
-        auto take = [&](const raw& r) {
-            float x[NV];
-            Vec<T>::unpack(r, x);
-            float mx = x[0];
-            for (int i = 1; i < NV; ++i) mx = fmaxf(mx, x[i]);
+        const uint32_t full = n / NV;             // whole vectors
+        uint32_t v = tid;
+        // The maximum is looked at once for kTogether vectors.
+        auto take = [&](const raw* r, auto count) {
+            float x[decltype(count)::value][NV];
+            float mx = kLowest;
+            for (int u = 0; u < count; ++u) {
+                Vec<T>::unpack(r[u], x[u]);
+                for (int i = 0; i < NV; ++i) mx = fmaxf(mx, x[u][i]);
+            }
             if (mx > st.m) st.raise(mx);
-            for (int i = 0; i < NV; ++i) st.template add<ENTROPY>(x[i]);
+            for (int u = 0; u < count; ++u)
+                for (int i = 0; i < NV; ++i) st.template add<ENTROPY>(x[u][i]);
         };
         for (; v + (kUnroll - 1) * kThreads < full; v += kUnroll * kThreads) {
             raw r[kUnroll];
             for (int u = 0; u < kUnroll; ++u)
-                r[u] = *reinterpret_cast<const raw*>(l + (v + u * kThreads) * NV);
-            for (int u = 0; u < kUnroll; ++u) take(r[u]);
+                r[u] = Vec<T>::template load<NT>(l + static_cast<size_t>(v + u * kThreads) * NV);
+            for (int u = 0; u < kUnroll; u += kTogether) take(r + u, Count<kTogether>{});
         }
-        for (; v < full; v += kThreads) take(*reinterpret_cast<const raw*>(l + v * NV));
+        for (; v < full; v += kThreads) {
+            const raw r = Vec<T>::load(l + static_cast<size_t>(v) * NV);
+            take(&r, Count<1>{});
+        }
         if (v == full) {                          // the row's last, partial vector
-            for (int64_t i = full * NV; i < n; ++i) {
+            for (uint32_t i = full * NV; i < n; ++i) {
                 const float x = to_f32(l[i]);
                 if (x > st.m) st.raise(x);
                 st.template add<ENTROPY>(x);
             }
         }
         const Stats mine = st;
-        for (int o = kWave / 2; o > 0; o >>= 1) st.merge(st.shuffled(o));
+        st = st.of_wave();
         if (tid % kWave == 0) lds[tid / kWave] = st;
         __syncthreads();
-        st = lds[0];
-        for (int w = 1; w < kWaves; ++w) st.merge(lds[w]);
+        {
+            const float m = fmaxf(fmaxf(lds[0].m, lds[1].m), fmaxf(lds[2].m, lds[3].m));
+            const Stats q0 = lds[0].at(m), q1 = lds[1].at(m), q2 = lds[2].at(m), q3 = lds[3].at(m);
+            st = Stats{m, (q0.s + q1.s) + (q2.s + q3.s), 0.0f, (q0.t + q1.t) + (q2.t + q3.t)};
+        }
+        if (st.nearly_certain()) st.r = rest_of<T>(lds_r, &owner, l, n, mine, st);
         const uint64_t* best = nullptr;
         if constexpr (TOP) {
             TopLds& s = *reinterpret_cast<TopLds*>(top_lds);
@@ -309,7 +404,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobsArgs a, int parts
         if (parts == 1) {
             write_row<TOP>(a, row, st, target_logit, target, best);
         } else {
-            char* w = static_cast<char*>(a.workspace) + job * part_bytes(a.top_k);
+            char* w = static_cast<char*>(a.workspace) + static_cast<int64_t>(job) * part_bytes(a.top_k);
             if (tid == 0) *reinterpret_cast<Stats*>(w) = st;
             if constexpr (TOP)
                 if (tid < a.top_k) reinterpret_cast<uint64_t*>(w + 16)[tid] = best[tid];
@@ -318,36 +413,58 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobsArgs a, int parts
     }
 }
 
-// Joins the parts of a row.
+// Joins the parts of a row.  Every part's best keys are sorted; the first
+// ceil(k / parts) of each are at least k keys, so the k-th largest of them
+// bounds the row's k-th from below and few keys are left to be ranked.  All
+// loads are under way before the first is used: a chain of them is what this
+// kernel's time is made of.
 template <typename T, bool TOP>
 __global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobsArgs a, int parts) {
+    constexpr int kHeld = kMaxParts * DL_MAX_TOP / kThreads;
     __shared__ char top_lds[TOP ? sizeof(TopLds) : 1] __attribute__((aligned(16)));
-    const int tid = threadIdx.x;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const char* w = static_cast<const char*>(a.workspace) + row * parts * part_bytes(a.top_k);
-        int64_t target = -1;
-        float target_logit = 0;
-        if (a.targets != nullptr) {
-            target = a.targets[row];
-            if (target >= 0 && target < a.vocab)
-                target_logit = to_f32((static_cast<const T*>(a.logits) + row * a.ld)[target]);
+    const int tid = threadIdx.x, held = tid % kMaxParts, k = a.top_k;
+    const int64_t bytes = part_bytes(k);
+    const int64_t row = blockIdx.x;
+    const char* w = static_cast<const char*>(a.workspace) + row * parts * bytes;
+    int64_t target = -1;
+    float target_logit = 0;
+    if (a.targets != nullptr) target = a.targets[row];
+    Stats st = Stats::none();
+    if (held < parts) st = *reinterpret_cast<const Stats*>(w + held * bytes);
+    uint64_t key[kHeld];
+    uint32_t head = 0;
+    if constexpr (TOP) {
+        const int heads = (k + parts - 1) / parts;       // parts * heads < parts + k
+        if (tid < parts * heads)
+            head = static_cast<uint32_t>(
+                reinterpret_cast<const uint64_t*>(w + tid / heads * bytes + 16)[tid % heads] >>
+                32);
+        for (int u = 0; u < kHeld; ++u) {
+            const int i = tid + u * kThreads;
+            key[u] = i < parts * k
+                         ? reinterpret_cast<const uint64_t*>(w + i / k * bytes + 16)[i % k]
+                         : 0;
         }
-        Stats st = *reinterpret_cast<const Stats*>(w);
-        for (int p = 1; p < parts; ++p)
-            st.merge(*reinterpret_cast<const Stats*>(w + p * part_bytes(a.top_k)));
-        const uint64_t* best = nullptr;
-        if constexpr (TOP) {
-            TopLds& s = *reinterpret_cast<TopLds*>(top_lds);
-            const int k = a.top_k;
-            for (int i = tid; i < parts * k; i += kThreads)
-                s.list[i] = reinterpret_cast<const uint64_t*>(w + i / k * part_bytes(k) + 16)[i % k];
-            __syncthreads();
-            rank_select(s, parts * k, k);
-            best = s.best;
-        }
-        write_row<TOP>(a, row, st, target_logit, target, best);
-        __syncthreads();
     }
+    if (target >= 0 && target < a.vocab)
+        target_logit = to_f32((static_cast<const T*>(a.logits) + row * a.ld)[target]);
+    static_assert(kMaxParts == 16, "");
+    st = st.of_lanes();
+    const uint64_t* best = nullptr;
+    if constexpr (TOP) {
+        TopLds& s = *reinterpret_cast<TopLds*>(top_lds);
+        s.key[tid] = head;
+        if (tid == 0) s.count = 0;
+        __syncthreads();
+        const uint32_t least = kth_bound<sizeof(T) == 2 ? 16 : 20>(s, k);
+        for (int u = 0; u < kHeld; ++u)
+            if (key[u] != 0 && static_cast<uint32_t>(key[u] >> 32) >= least)
+                s.list[atomicAdd(&s.count, 1)] = key[u];
+        __syncthreads();
+        rank_select(s, s.count, k);
+        best = s.best;
+    }
+    write_row<TOP>(a, row, st, target_logit, target, best);
 }
 
 // Elements of a row in chunks of kThreads * kBackUnroll vectors.
@@ -384,7 +501,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_backward(LogprobsBackward
         raw r[kBackUnroll];
         for (int u = 0; u < kBackUnroll; ++u)
             if (v0 + u * kThreads < full)
-                r[u] = *reinterpret_cast<const raw*>(l + (v0 + u * kThreads) * NV);
+                r[u] = Vec<T>::load(l + (v0 + u * kThreads) * NV);
         for (int u = 0; u < kBackUnroll; ++u) {
             const int64_t v = v0 + u * kThreads, at = v * NV;
             if (v < full) {
@@ -394,7 +511,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_backward(LogprobsBackward
                 if (t >= at && t < at + NV)
                     for (int i = 0; i < NV; ++i)
                         if (at + i == t) d[i] = of_target(x[i]);
-                *reinterpret_cast<raw*>(dl + at) = Vec<T>::pack(d);
+                Vec<T>::store(dl + at, Vec<T>::pack(d));
             } else if (v == full) {
                 for (int64_t i = at; i < a.vocab; ++i) {
                     const float x = to_f32(l[i]);
@@ -409,14 +526,15 @@ template <typename T, bool ENTROPY, bool TOP>
 hipError_t launch(const LogprobsArgs& a, hipStream_t s) {
     const Split sp = split_of(a.rows, a.vocab);
     const int64_t jobs = a.rows * sp.parts;
-    const dim3 block(kThreads);
-    k_logprobs<T, ENTROPY, TOP><<<dim3(static_cast<unsigned>(jobs < kMaxGrid ? jobs : kMaxGrid)),
-                                  block, 0, s>>>(a, sp.parts, sp.chunk);
-    if (sp.parts > 1) {
-        if (hipError_t e = hipGetLastError()) return e;
-        k_logprobs_join<T, TOP><<<dim3(static_cast<unsigned>(a.rows < kMaxGrid ? a.rows : kMaxGrid)),
-                                  block, 0, s>>>(a, sp.parts);
-    }
+    const dim3 grid(static_cast<unsigned>(jobs < kMaxGrid ? jobs : kMaxGrid)), block(kThreads);
+    if (!TOP && a.rows * a.vocab * static_cast<int64_t>(sizeof(T)) >= kNontemporalMin)
+        k_logprobs<T, ENTROPY, TOP, !TOP><<<grid, block, 0, s>>>(a, sp.parts, sp.chunk);
+    else
+        k_logprobs<T, ENTROPY, TOP, false><<<grid, block, 0, s>>>(a, sp.parts, sp.chunk);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || sp.parts == 1) return e;
+    k_logprobs_join<T, TOP>
+        <<<dim3(static_cast<unsigned>(a.rows)), dim3(kThreads), 0, s>>>(a, static_cast<int>(sp.parts));
     return hipGetLastError();
 }
 
