@@ -69,39 +69,187 @@ __global__ __launch_bounds__(kThreads) void k_w4_quantize(const T* w, int64_t ld
     }
 }
 
-__device__ __forceinline__ float e4m3(uint32_t c) {
-    const uint32_t e = (c >> 3) & 15u, m = c & 7u;
-    float v = e == 0 ? static_cast<float>(m) * 0x1p-9f
-                     : __uint_as_float(((e + 120u) << 23) | (m << 20));
-    if ((c & 127u) == 127u) v = __uint_as_float(0x7FC00000u);
-    return (c & 128u) != 0 ? -v : v;
+// ---- the product -------------------------------------------------------------
+//
+// y[v][r] = sum_k x[v][k] W[r][k] as 16 x 16 tiles of v_mfma_f32_16x16x32_bf16:
+// rows of W against (up to 16) vectors.  A code times its block's power of two
+// is a bfloat16 number, and so is an e4m3 value times its own: products are
+// exact and sums binary32.
+//
+// Bound by the weights' bytes (17 for 32 weights) once there are enough of
+// them.  A lane's 16 bytes are the 32 codes of one row's block, all with one
+// scale, and the four lanes of a row take four neighbouring blocks (a span of
+// 128 columns): the four products of a span take eight codes each of every
+// lane, whatever columns these are, as x is laid out the same.  The vectors
+// stay in registers: a wave has kSpans spans of them and passes rows by, so
+// x is read once a workgroup, not once a tile.  The waves of a workgroup take
+// different spans of the same rows, and their sums meet in LDS.
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+
+constexpr int kMatThreads = 512;
+constexpr int kMatWaves = kMatThreads / kWave;
+constexpr int kSpans = 2;
+
+template <typename F> __device__ __forceinline__ uint32_t bits_of(F v) {
+    static_assert(sizeof(F) == 4, "");
+    return __builtin_bit_cast(uint32_t, v);
 }
 
-// One wave an element of y.
-template <typename Y>
-__global__ __launch_bounds__(kThreads) void k_w4_matvec(MatvecArgs a, int x_scale_kind) {
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / kWave) +
-                        threadIdx.x / kWave;
-    if (row >= a.rows) return;
-    const int v = blockIdx.y;
-    const int64_t kb = (a.cols + 31) / 32;
-    float t = 0;
-    for (int64_t k = threadIdx.x % kWave; k < a.cols; k += kWave) {
-        const uint32_t byte = a.packed[row * kb * 16 + k / 2];
-        const float w = e2m1((byte >> (4 * (k & 1))) & 15u) * scale_of(a.scales[row * kb + k / 32]);
-        float x;
-        if (x_scale_kind == DL_SCALE_NONE) {
-            x = to_f32(static_cast<const bf16*>(a.x)[v * a.ldx + k]);
-        } else {
-            x = e4m3(static_cast<const uint8_t*>(a.x)[v * a.ldx + k]);
-            if (x_scale_kind == DL_SCALE_BLOCK32)
-                x *= scale_of(static_cast<const uint8_t*>(a.x_scales)[v * kb + k / 32]);
-        }
-        t += w * x;
+// 32 codes (four words) as 4 x 8 bf16 values, the block's scale applied.
+__device__ __forceinline__ void decode(u32x4 w, uint32_t byte, bf16x8* out) {
+    // The conversion takes a scale's exponent from a binary32 number's: all
+    // ones is NaN there, all zeros 2^-127.
+    const float b = __uint_as_float(byte << 23);
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t c = w[i];
+        const u32x4 v = {bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, b, 0)),
+                         bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, b, 1)),
+                         bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, b, 2)),
+                         bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, b, 3))};
+        out[i] = __builtin_bit_cast(bf16x8, v);
     }
-    t = wave_sum(t);
-    if (x_scale_kind == DL_SCALE_ROW) t *= static_cast<const float*>(a.x_scales)[v];
-    if (threadIdx.x % kWave == 0) static_cast<Y*>(a.y)[v * a.ldy + row] = from_f32<Y>(t);
+}
+
+// 32 elements of one vector from column k0 on, 0 past the end, in the order in
+// which decode() has the weights.
+template <int KIND>
+__device__ __forceinline__ void load_vector(const MatvecArgs& a, int v, int64_t k0, bf16x8* out) {
+    const int64_t kb = (a.cols + 31) / 32;
+    u32x4 q[4] = {};
+    if (KIND == DL_SCALE_NONE) {
+        if (v < a.count && k0 < a.cols) {
+            const uint16_t* p = static_cast<const uint16_t*>(a.x) + v * a.ldx + k0;
+            if (k0 + 32 <= a.cols) {
+                for (int i = 0; i < 4; ++i) q[i] = reinterpret_cast<const u32x4_any*>(p)[i];
+            } else {
+                const int n = static_cast<int>(a.cols - k0);
+                for (int i = 0; i < 16; ++i) {
+                    const uint32_t lo = 2 * i < n ? p[2 * i] : 0, hi = 2 * i + 1 < n ? p[2 * i + 1] : 0;
+                    q[i / 4][i % 4] = lo | (hi << 16);
+                }
+            }
+        }
+        for (int i = 0; i < 4; ++i) out[i] = __builtin_bit_cast(bf16x8, q[i]);
+        return;
+    }
+    uint32_t byte = 127;
+    if (v < a.count && k0 < a.cols) {
+        const uint8_t* p = static_cast<const uint8_t*>(a.x) + v * a.ldx + k0;
+        if (KIND == DL_SCALE_BLOCK32) byte = static_cast<const uint8_t*>(a.x_scales)[v * kb + k0 / 32];
+        if (k0 + 32 <= a.cols) {
+            for (int i = 0; i < 2; ++i) q[i] = reinterpret_cast<const u32x4_any*>(p)[i];
+        } else {
+            const int n = static_cast<int>(a.cols - k0);
+            for (int i = 0; i < 32; ++i)
+                q[i / 16][i / 4 % 4] |= (i < n ? static_cast<uint32_t>(p[i]) : 0) << (8 * (i % 4));
+        }
+    }
+    const float b = __uint_as_float(byte << 23);
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t c = q[i / 2][i % 2 * 2], d = q[i / 2][i % 2 * 2 + 1];
+        const u32x4 r = {bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, b, false)),
+                         bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, b, true)),
+                         bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, b, false)),
+                         bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, b, true))};
+        out[i] = __builtin_bit_cast(bf16x8, r);
+    }
+}
+
+// MT tiles of 16 vectors, RT tiles of 16 rows a wave; kw of the workgroup's
+// waves (2, 4 or 8) share rows and split the columns, the others take other
+// rows.
+template <int KIND, int MT, int RT, typename Y>
+__global__ __launch_bounds__(kMatThreads) void k_w4_matvec(MatvecArgs a, int kw) {
+    __shared__ f32x4 part[kMatWaves][RT][MT][16][4];
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    const int l16 = lane % 16, j = lane / 16;
+    const int k_of = wave % kw, tw = kMatWaves / kw, t_of = wave / kw;
+    const int64_t kb = (a.cols + 31) / 32;
+    const int64_t chunk = static_cast<int64_t>(kw) * kSpans * 4;          // blocks of all waves
+    const int64_t groups = (a.rows + 16 * RT - 1) / (16 * RT);
+    bf16x8 x[MT][kSpans][4];
+    for (int64_t g0 = static_cast<int64_t>(blockIdx.x) * tw; g0 < groups;
+         g0 += static_cast<int64_t>(gridDim.x) * tw) {
+        const int64_t row0 = (g0 + t_of) * 16 * RT;
+        f32x4 acc[RT][MT] = {};
+        for (int64_t c0 = 0; c0 < kb; c0 += chunk) {
+            const int64_t b0 = c0 + (static_cast<int64_t>(k_of) * kSpans) * 4 + j;
+            u32x4 w[RT][kSpans];
+            uint32_t e[RT][kSpans];
+            for (int t = 0; t < RT; ++t) {
+                int64_t row = row0 + t * 16 + l16;
+                row = row < a.rows ? row : a.rows - 1;
+                for (int s = 0; s < kSpans; ++s) {
+                    const int64_t b = b0 + s * 4;
+                    w[t][s] = u32x4{};
+                    e[t][s] = 0;
+                    if (b < kb) {
+                        w[t][s] = *reinterpret_cast<const u32x4*>(a.packed + (row * kb + b) * 16);
+                        e[t][s] = a.scales[row * kb + b];
+                    }
+                }
+            }
+            if (chunk < kb || g0 == static_cast<int64_t>(blockIdx.x) * tw)
+                for (int m = 0; m < MT; ++m)
+                    for (int s = 0; s < kSpans; ++s)
+                        load_vector<KIND>(a, m * 16 + l16, (b0 + s * 4) * 32, x[m][s]);
+            for (int s = 0; s < kSpans; ++s)
+                for (int t = 0; t < RT; ++t) {
+                    bf16x8 v[4];
+                    decode(w[t][s], e[t][s], v);
+                    for (int m = 0; m < MT; ++m)
+                        for (int i = 0; i < 4; ++i)
+                            acc[t][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                v[i], x[m][s][i], acc[t][m], 0, 0, 0);
+                }
+        }
+        // Lane (j, l16) has rows 4j .. 4j+3 of vector l16 of each tile.
+        __syncthreads();                      // the last rows' sums have been read
+        for (int t = 0; t < RT; ++t)
+            for (int m = 0; m < MT; ++m) part[wave][t][m][l16][j] = acc[t][m];
+        __syncthreads();
+        constexpr int kOut = RT * MT * 64;    // four rows of a vector each
+        for (int o = k_of * kWave + lane; o < kOut; o += kw * kWave) {
+            const int jj = o % 4, t = o / 4 % RT, v = o / (4 * RT);
+            f32x4 r = part[wave - k_of][t][v / 16][v % 16][jj];
+            for (int q = 1; q < kw; ++q) r += part[wave - k_of + q][t][v / 16][v % 16][jj];
+            const int64_t row = row0 + t * 16 + jj * 4;
+            if (v < a.count) {
+                if (KIND == DL_SCALE_ROW) r *= static_cast<const float*>(a.x_scales)[v];
+                Y* y = static_cast<Y*>(a.y) + v * a.ldy + row;
+                for (int i = 0; i < 4; ++i)
+                    if (row + i < a.rows) y[i] = from_f32<Y>(r[i]);
+            }
+        }
+    }
+}
+
+template <int KIND, int MT, int RT>
+hipError_t matvec(const MatvecArgs& a, int y_dtype, hipStream_t s) {
+    const int64_t spans = ((a.cols + 31) / 32 + 3) / 4;
+    int kw = 2;
+    while (kw < kMatWaves && kw * kSpans < spans) kw *= 2;
+    const int64_t groups = (a.rows + 16 * RT - 1) / (16 * RT);
+    const int64_t tw = kMatWaves / kw;
+    int64_t blocks = (groups + tw - 1) / tw;
+    blocks = blocks < 512 ? blocks : 512;
+    const dim3 grid(static_cast<unsigned>(blocks)), block(kMatThreads);
+    if (y_dtype == DL_F32) k_w4_matvec<KIND, MT, RT, float><<<grid, block, 0, s>>>(a, kw);
+    else k_w4_matvec<KIND, MT, RT, bf16><<<grid, block, 0, s>>>(a, kw);
+    return hipGetLastError();
+}
+
+template <int KIND> hipError_t matvec_of(const MatvecArgs& a, int y_dtype, hipStream_t s) {
+    // Four row tiles a wave keep more bytes under way; few rows are spread
+    // over more workgroups instead.
+    const bool many = a.rows >= 16 * 1024;
+    if (a.count <= 16)
+        return many ? matvec<KIND, 1, 4>(a, y_dtype, s) : matvec<KIND, 1, 1>(a, y_dtype, s);
+    return many ? matvec<KIND, 2, 4>(a, y_dtype, s) : matvec<KIND, 2, 1>(a, y_dtype, s);
 }
 
 }  // namespace
@@ -121,13 +269,9 @@ hipError_t w4_quantize(const void* w, int64_t ldw, int dtype, int64_t rows, int6
 }
 
 hipError_t w4_matvec(const MatvecArgs& a, int, int x_scale_kind, int y_dtype, hipStream_t s) {
-    const int per = kThreads / kWave;
-    const dim3 grid(static_cast<unsigned>((a.rows + per - 1) / per),
-                    static_cast<unsigned>(a.count)),
-        block(kThreads);
-    if (y_dtype == DL_F32) k_w4_matvec<float><<<grid, block, 0, s>>>(a, x_scale_kind);
-    else k_w4_matvec<bf16><<<grid, block, 0, s>>>(a, x_scale_kind);
-    return hipGetLastError();
+    if (x_scale_kind == DL_SCALE_NONE) return matvec_of<DL_SCALE_NONE>(a, y_dtype, s);
+    if (x_scale_kind == DL_SCALE_ROW) return matvec_of<DL_SCALE_ROW>(a, y_dtype, s);
+    return matvec_of<DL_SCALE_BLOCK32>(a, y_dtype, s);
 }
 
 }  // namespace dlk
