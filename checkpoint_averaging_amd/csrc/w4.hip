@@ -89,6 +89,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
 
 constexpr int kMatThreads = 512;
 constexpr int kMatWaves = kMatThreads / kWave;
@@ -172,41 +173,80 @@ __global__ __launch_bounds__(kMatThreads) void k_w4_matvec(MatvecArgs a, int kw)
     const int64_t chunk = static_cast<int64_t>(kw) * kSpans * 4;          // blocks of all waves
     const int64_t groups = (a.rows + 16 * RT - 1) / (16 * RT);
     bf16x8 x[MT][kSpans][4];
-    for (int64_t g0 = static_cast<int64_t>(blockIdx.x) * tw; g0 < groups;
-         g0 += static_cast<int64_t>(gridDim.x) * tw) {
-        const int64_t row0 = (g0 + t_of) * 16 * RT;
-        f32x4 acc[RT][MT] = {};
-        for (int64_t c0 = 0; c0 < kb; c0 += chunk) {
-            const int64_t b0 = c0 + (static_cast<int64_t>(k_of) * kSpans) * 4 + j;
-            u32x4 w[RT][kSpans];
-            uint32_t e[RT][kSpans];
-            for (int t = 0; t < RT; ++t) {
-                int64_t row = row0 + t * 16 + l16;
-                row = row < a.rows ? row : a.rows - 1;
+    // The weights of one chunk of columns of one group of rows, a step.  Four
+    // neighbouring lanes load 64 bytes of a row; the lane that the product
+    // wants them in gets them at use.  A row's eight scale bytes come in one
+    // load where it has as many.
+    auto load = [&](int64_t g, int64_t c, u32x4 (&w)[RT][kSpans], uint32_t (&e)[RT][kSpans]) {
+        const int64_t b0 = c + static_cast<int64_t>(k_of) * (kSpans * 4);
+        const int64_t r0 = (g + t_of) * (16 * RT);
+        for (int t = 0; t < RT; ++t) {
+            int64_t row = r0 + t * 16 + lane / 4;
+            row = row < a.rows ? row : a.rows - 1;
+            for (int s = 0; s < kSpans; ++s) {
+                const int64_t b = b0 + s * 4 + lane % 4;
+                w[t][s] = u32x4{};
+                if (b < kb) w[t][s] = *reinterpret_cast<const u32x4*>(a.packed + (row * kb + b) * 16);
+            }
+            row = r0 + t * 16 + l16;
+            row = row < a.rows ? row : a.rows - 1;
+            if (b0 + kSpans * 4 <= kb) {
+                const u32x2_any q = *reinterpret_cast<const u32x2_any*>(a.scales + row * kb + b0);
+                for (int s = 0; s < kSpans; ++s) e[t][s] = q[s];
+            } else {
                 for (int s = 0; s < kSpans; ++s) {
-                    const int64_t b = b0 + s * 4;
-                    w[t][s] = u32x4{};
-                    e[t][s] = 0;
-                    if (b < kb) {
-                        w[t][s] = *reinterpret_cast<const u32x4*>(a.packed + (row * kb + b) * 16);
-                        e[t][s] = a.scales[row * kb + b];
-                    }
+                    const int64_t b = b0 + s * 4 + j;
+                    e[t][s] = b < kb ? static_cast<uint32_t>(a.scales[row * kb + b]) << (8 * j) : 0;
                 }
             }
-            if (chunk < kb || g0 == static_cast<int64_t>(blockIdx.x) * tw)
-                for (int m = 0; m < MT; ++m)
-                    for (int s = 0; s < kSpans; ++s)
-                        load_vector<KIND>(a, m * 16 + l16, (b0 + s * 4) * 32, x[m][s]);
-            for (int s = 0; s < kSpans; ++s)
-                for (int t = 0; t < RT; ++t) {
-                    bf16x8 v[4];
-                    decode(w[t][s], e[t][s], v);
-                    for (int m = 0; m < MT; ++m)
-                        for (int i = 0; i < 4; ++i)
-                            acc[t][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                v[i], x[m][s][i], acc[t][m], 0, 0, 0);
-                }
         }
+    };
+    int64_t g0 = static_cast<int64_t>(blockIdx.x) * tw, c0 = 0;
+    u32x4 w[RT][kSpans];
+    uint32_t e[RT][kSpans];
+    f32x4 acc[RT][MT] = {};
+    if (g0 < groups) load(g0, c0, w, e);
+    bool first = true;
+    while (g0 < groups) {
+        // the next step's weights are under way during this step's products
+        int64_t g1 = g0, c1 = c0 + chunk;
+        if (c1 >= kb) {
+            c1 = 0;
+            g1 = g0 + static_cast<int64_t>(gridDim.x) * tw;
+        }
+        if (first || chunk < kb) {
+            const int64_t b0 = c0 + (static_cast<int64_t>(k_of) * kSpans) * 4 + j;
+            for (int m = 0; m < MT; ++m)
+                for (int s = 0; s < kSpans; ++s)
+                    load_vector<KIND>(a, m * 16 + l16, (b0 + s * 4) * 32, x[m][s]);
+            first = false;
+        }
+        u32x4 wn[RT][kSpans];
+        uint32_t en[RT][kSpans];
+        if (g1 < groups) load(g1, c1, wn, en);
+        for (int s = 0; s < kSpans; ++s)
+            for (int t = 0; t < RT; ++t) {
+                bf16x8 v[4];
+                u32x4 q;
+                for (int i = 0; i < 4; ++i)
+                    q[i] = static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(
+                        (l16 * 4 + j) * 4, static_cast<int>(w[t][s][i])));
+                decode(q, (e[t][s] >> (8 * j)) & 0xFFu, v);
+                for (int m = 0; m < MT; ++m)
+                    for (int i = 0; i < 4; ++i)
+                        acc[t][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[i], x[m][s][i],
+                                                                            acc[t][m], 0, 0, 0);
+            }
+        const int64_t row0 = (g0 + t_of) * (16 * RT);
+        const bool done = c1 == 0;
+        g0 = g1;
+        c0 = c1;
+        for (int t = 0; t < RT; ++t)
+            for (int s = 0; s < kSpans; ++s) {
+                w[t][s] = wn[t][s];
+                e[t][s] = en[t][s];
+            }
+        if (!done) continue;
         // Lane (j, l16) has rows 4j .. 4j+3 of vector l16 of each tile.
         __syncthreads();                      // the last rows' sums have been read
         for (int t = 0; t < RT; ++t)
@@ -225,6 +265,8 @@ __global__ __launch_bounds__(kMatThreads) void k_w4_matvec(MatvecArgs a, int kw)
                     if (row + i < a.rows) y[i] = from_f32<Y>(r[i]);
             }
         }
+        for (int t = 0; t < RT; ++t)
+            for (int m = 0; m < MT; ++m) acc[t][m] = f32x4{};
     }
 }
 
@@ -248,8 +290,8 @@ template <int KIND> hipError_t matvec_of(const MatvecArgs& a, int y_dtype, hipSt
     // over more workgroups instead.
     const bool many = a.rows >= 16 * 1024;
     if (a.count <= 16)
-        return many ? matvec<KIND, 1, 4>(a, y_dtype, s) : matvec<KIND, 1, 1>(a, y_dtype, s);
-    return many ? matvec<KIND, 2, 4>(a, y_dtype, s) : matvec<KIND, 2, 1>(a, y_dtype, s);
+        return many ? matvec<KIND, 1, 2>(a, y_dtype, s) : matvec<KIND, 1, 1>(a, y_dtype, s);
+    return many ? matvec<KIND, 2, 2>(a, y_dtype, s) : matvec<KIND, 2, 1>(a, y_dtype, s);
 }
 
 }  // namespace
