@@ -15,56 +15,90 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// 2^(e-127) for a scale byte; 255 is NaN.
-__device__ __forceinline__ float scale_of(uint32_t e) {
-    return e == 255 ? __uint_as_float(0x7FC00000u)
-                    : e == 0 ? 0x1p-127f : __uint_as_float(e << 23);
+// ---- the layout --------------------------------------------------------------
+//
+// Elementwise but for a block's largest magnitude, so bound by the bytes in and
+// out.  A lane takes eight neighbouring columns and four lanes a block: the
+// largest magnitude goes round them by DPP, and the hardware's conversion
+// rounds to the eight magnitudes (nearest, ties to even) with the scale a power
+// of two, so that nothing but this rounding is inexact.
+
+// Eight elements from column c on of a row of n, 0 past the end.
+template <typename T>
+__device__ __forceinline__ void load8(const T* row, int64_t c, int64_t n, float* v) {
+    constexpr int NV = Vec<T>::n;
+    if (c + 8 <= n) {
+        for (int i = 0; i < 8; i += NV) Vec<T>::unpack(Vec<T>::load(row + c + i), v + i);
+    } else {
+        for (int i = 0; i < 8; ++i) v[i] = c + i < n ? to_f32(row[c + i]) : 0.0f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* row, int64_t c, int64_t n, const float* v) {
+    constexpr int NV = Vec<T>::n;
+    if (c + 8 <= n) {
+        for (int i = 0; i < 8; i += NV) Vec<T>::store(row + c + i, Vec<T>::pack(v + i));
+    } else {
+        for (int i = 0; i < 8; ++i)
+            if (c + i < n) row[c + i] = from_f32<T>(v[i]);
+    }
 }
 
-// A code's value: sign bit 3, two exponent bits, one mantissa bit.
-__device__ __forceinline__ float e2m1(uint32_t c) {
-    const uint32_t e = (c >> 1) & 3u;
-    const float m = e == 0 ? 0.5f * static_cast<float>(c & 1u)
-                           : __uint_as_float(((126u + e) << 23) | ((c & 1u) << 22));
-    return (c & 8u) != 0 ? -m : m;
+template <typename F> __device__ __forceinline__ uint32_t bits_of(F v) {
+    static_assert(sizeof(F) == 4, "");
+    return __builtin_bit_cast(uint32_t, v);
 }
 
-// One thread a block of 32.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_w4_quantize(const T* w, int64_t ldw, int64_t rows,
                                                           int64_t cols, uint8_t* packed,
                                                           uint8_t* scales, T* values,
-                                                          int64_t ldv) {
-    const int64_t kb = (cols + 31) / 32;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    if (i >= rows * kb) return;
-    const int64_t row = i / kb, c0 = (i % kb) * 32;
-    const int n = static_cast<int>(cols - c0 < 32 ? cols - c0 : 32);
-    uint32_t b = 0;
-    for (int j = 0; j < n; ++j) {
-        const uint32_t u = abs_bits(to_f32(w[row * ldw + c0 + j]));
-        b = u > b ? u : b;
-    }
-    int e = static_cast<int>((b + 0x3FFFFFu) >> 23) - 2;
-    e = e < 0 ? 0 : e;
-    if (b >= 0x7F800000u) e = 255;
-    scales[i] = static_cast<uint8_t>(e);
-    const float back = e == 255 ? 0.0f : __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-    uint32_t byte = 0;
-    for (int j = 0; j < 32; ++j) {
-        uint32_t code = 0;
-        if (j < n && e != 255) {
-            const float v = to_f32(w[row * ldw + c0 + j]) * back, m = __builtin_fabsf(v);
-            code = (m > 0.25f) + (m >= 0.75f) + (m > 1.25f) + (m >= 1.75f) + (m > 2.5f) +
-                   (m >= 3.5f) + (m > 5.0f);
-            code |= (__float_as_uint(v) >> 31) << 3;
+                                                          int64_t ldv, int64_t slab) {
+    // All rows' groups of eight columns in a line, `slab` rows for each y of
+    // the grid so that 32 bits count them.
+    const uint32_t lanes = static_cast<uint32_t>((cols + 31) / 32 * 4);
+    const int64_t kb = lanes / 4;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.y) * slab;
+    const uint32_t n = static_cast<uint32_t>(rows - row0 < slab ? rows - row0 : slab) * lanes;
+    const uint32_t at = blockIdx.x * kThreads + threadIdx.x;
+    if (at < n) {                             // (four lanes of a block together)
+        const int64_t row = row0 + at / lanes, i = at % lanes;
+        float v[8];
+        load8(w + row * ldw, i * 8, cols, v);
+        uint32_t b = 0;
+        for (int k = 0; k < 8; ++k) b = Max{}(b, abs_bits(v[k]));
+        b = lanes_reduce<4>(b, Max{});
+        // the smallest power of two s with amax <= 6 s = 1.5 * 2^2 s
+        int e = static_cast<int>((b + 0x3FFFFFu) >> 23) - 2;
+        e = e < 0 ? 0 : e;
+        const bool bad = b >= 0x7F800000u;
+        const float back = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+        uint32_t q = 0;
+        if (bad) {
+            e = 255;
+        } else {
+            for (int k = 0; k < 8; ++k) v[k] *= back;
+            q = static_cast<uint32_t>(
+                __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[0], v[1], 1.0f, 0));
+            q = static_cast<uint32_t>(
+                __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[2], v[3], 1.0f, 1));
+            q = static_cast<uint32_t>(
+                __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[4], v[5], 1.0f, 2));
+            q = static_cast<uint32_t>(
+                __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[6], v[7], 1.0f, 3));
         }
-        if (j < n && values != nullptr)
-            values[row * ldv + c0 + j] = from_f32<T>(e2m1(code) * scale_of(e));
-        byte |= code << (4 * (j & 1));
-        if (j & 1) {
-            packed[i * 16 + j / 2] = static_cast<uint8_t>(byte);
-            byte = 0;
+        reinterpret_cast<uint32_t*>(packed)[row * kb * 4 + i] = q;
+        if (threadIdx.x % 4 == 0) scales[row * kb + i / 4] = static_cast<uint8_t>(e);
+        if (values != nullptr) {
+            // (the conversion takes the scale's exponent bits: all zeros is 2^-127, all ones NaN)
+            const float s = __uint_as_float(static_cast<uint32_t>(e) << 23);
+            typedef float f32x2 __attribute__((ext_vector_type(2)));
+            const f32x2 o[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 0),
+                                __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 1),
+                                __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 2),
+                                __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 3)};
+            for (int k = 0; k < 8; ++k) v[k] = o[k / 2][k % 2];
+            store8(values + row * ldv, i * 8, cols, v);
         }
     }
 }
@@ -94,11 +128,6 @@ typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
 constexpr int kMatThreads = 512;
 constexpr int kMatWaves = kMatThreads / kWave;
 constexpr int kSpans = 2;
-
-template <typename F> __device__ __forceinline__ uint32_t bits_of(F v) {
-    static_assert(sizeof(F) == 4, "");
-    return __builtin_bit_cast(uint32_t, v);
-}
 
 // 32 codes (four words) as 4 x 8 bf16 values, the block's scale applied.
 __device__ __forceinline__ void decode(u32x4 w, uint32_t byte, bf16x8* out) {
@@ -299,14 +328,18 @@ template <int KIND> hipError_t matvec_of(const MatvecArgs& a, int y_dtype, hipSt
 hipError_t w4_quantize(const void* w, int64_t ldw, int dtype, int64_t rows, int64_t cols,
                        uint8_t* packed, uint8_t* scales, void* values, int64_t ldvalues,
                        hipStream_t s) {
-    const int64_t blocks = rows * ((cols + 31) / 32);
-    const dim3 grid(static_cast<unsigned>((blocks + kThreads - 1) / kThreads)), block(kThreads);
+    const int64_t lanes = (cols + 31) / 32 * 4;
+    int64_t slab = (int64_t(1) << 30) / lanes;
+    slab = slab < rows ? slab : rows;
+    const dim3 grid(static_cast<unsigned>((slab * lanes + kThreads - 1) / kThreads),
+                    static_cast<unsigned>((rows + slab - 1) / slab)),
+        block(kThreads);
     if (dtype == DL_F32)
         k_w4_quantize<<<grid, block, 0, s>>>(static_cast<const float*>(w), ldw, rows, cols, packed,
-                                             scales, static_cast<float*>(values), ldvalues);
+                                             scales, static_cast<float*>(values), ldvalues, slab);
     else
         k_w4_quantize<<<grid, block, 0, s>>>(static_cast<const bf16*>(w), ldw, rows, cols, packed,
-                                             scales, static_cast<bf16*>(values), ldvalues);
+                                             scales, static_cast<bf16*>(values), ldvalues, slab);
     return hipGetLastError();
 }
 
