@@ -90,6 +90,27 @@ template <> struct Vec<bf16> {
     }
 };
 
+// Eight elements from column c on of a row of n, 0 past the end.
+template <typename T>
+__device__ __forceinline__ void load8(const T* row, int64_t c, int64_t n, float* v) {
+    constexpr int NV = Vec<T>::n;
+    if (c + 8 <= n) {
+        for (int i = 0; i < 8; i += NV) Vec<T>::unpack(Vec<T>::load(row + c + i), v + i);
+    } else {
+        for (int i = 0; i < 8; ++i) v[i] = c + i < n ? to_f32(row[c + i]) : 0.0f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* row, int64_t c, int64_t n, const float* v) {
+    constexpr int NV = Vec<T>::n;
+    if (c + 8 <= n) {
+        for (int i = 0; i < 8; i += NV) Vec<T>::store(row + c + i, Vec<T>::pack(v + i));
+    } else {
+        for (int i = 0; i < 8; ++i)
+            if (c + i < n) row[c + i] = from_f32<T>(v[i]);
+    }
+}
+
 // Reductions over a wavefront; every lane gets the result.  Within rows of 16
 // lanes values move by DPP (no LDS), in a fixed pairing that gives every lane
 // of a row the same bits; the four rows' are read as scalars.

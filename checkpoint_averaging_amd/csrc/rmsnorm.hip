@@ -2,6 +2,17 @@
 //
 //   s = x + residual ; inv = 1/sqrt(mean s^2 + eps) ; y = (s inv) w
 //   g = dy w ; h = s inv ; dx = inv (g - h mean(g h)) + dsum ; dw = sum dy h
+//
+// Both directions read each element once, keep the row in registers and write
+// once, so they are bound by these bytes.  A row is shared by 16, 64, 256 or
+// 1024 lanes, the fewest that hold it in four groups of eight columns each:
+// rows of up to 2048 columns need no barrier, and a wave has several rows'
+// loads under way with its neighbours.  The workgroups walk over the rows, so
+// that the weight is loaded once for many of them.
+//
+// What is rounded to 8 bits must not depend on an order of additions, so the
+// mean of squares is summed in binary64 (at most 2^-40 off for any order) and
+// everything after it is single binary32 operations.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -15,158 +26,329 @@ namespace dlk {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / kWave;
-constexpr int64_t kMaxGrid = 1 << 20;
+constexpr int kCols = 8;             // neighbouring columns a lane takes at once
+constexpr int kMaxPartials = 512;    // workgroups of the backward pass
 
-template <typename T> __device__ __forceinline__ T block_sum(T v, T* lds) {
-    v = wave_sum(v);
-    if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = v;
-    __syncthreads();
-    T t = lds[0];
-    for (int i = 1; i < kWaves; ++i) t += lds[i];
-    __syncthreads();
-    return t;
-}
+// Lanes a row, and threads a workgroup.
+template <int LANES> constexpr int threads_of() { return LANES > 256 ? LANES : 256; }
 
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* lds) {
-    v = wave_max(v);
-    if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = v;
-    __syncthreads();
-    uint32_t t = lds[0];
-    for (int i = 1; i < kWaves; ++i) t = lds[i] > t ? lds[i] : t;
-    __syncthreads();
-    return t;
-}
-
-__device__ __forceinline__ uint8_t e4m3_of(float v) {
-    return static_cast<uint8_t>(__builtin_amdgcn_cvt_pk_fp8_f32(v, 0.0f, 0, false) & 0xFF);
-}
-
-template <typename T>
-__device__ __forceinline__ float stream_value(const NormArgs& a, int64_t row, int c) {
-    const float x = to_f32(static_cast<const T*>(a.x)[row * a.ldx + c]);
-    if (a.residual == nullptr) return x;
-    return to_f32(from_f32<T>(x + to_f32(static_cast<const T*>(a.residual)[row * a.ldres + c])));
-}
-
-template <typename T>
-__global__ __launch_bounds__(kThreads) void k_rmsnorm(NormArgs a, int y_dtype, int scale_kind) {
-    __shared__ double lds_d[kWaves];
-    __shared__ uint32_t lds_u[kWaves];
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    double ss = 0;
-    for (int c = threadIdx.x; c < a.cols; c += kThreads) {
-        const double s = stream_value<T>(a, row, c);
-        ss += s * s;
-    }
-    ss = block_sum(ss, lds_d);
-    const float inv =
-        static_cast<float>(1.0 / sqrt(ss / a.cols + static_cast<double>(a.eps)));
-    if (threadIdx.x == 0 && a.inv_rms != nullptr) a.inv_rms[row] = inv;
-
-    uint32_t amax = 0;
-    float back = 0.0f;
-    if (scale_kind == DL_SCALE_ROW) {
-        for (int c = threadIdx.x; c < a.cols; c += kThreads) {
-            const uint32_t b = abs_bits((stream_value<T>(a, row, c) * inv) * a.weight[c]);
-            amax = b > amax ? b : amax;
+// A reduction over the LANES threads of a row; every one gets the result.
+template <int LANES, typename T, typename Op>
+__device__ __forceinline__ T row_reduce(T v, Op op, T* lds) {
+    if constexpr (LANES == 16) {
+        return lanes_reduce<16>(v, op);
+    } else {
+        v = wave_reduce(v, op);
+        if constexpr (LANES > kWave) {       // the row is the workgroup's
+            constexpr int kWaves = LANES / kWave;
+            __syncthreads();                 // an earlier result has been read
+            if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = v;
+            __syncthreads();
+            v = lds[0];
+            for (int i = 1; i < kWaves; ++i) v = op(v, lds[i]);
         }
-        amax = block_max(amax, lds_u);
-        const float m = __uint_as_float(amax);
-        float scale = 0.0f;
-        if (amax >= 0x7F800000u) {
-            scale = __uint_as_float(0x7FC00000u);
-        } else if (m >= 0x1p-100f) {
-            scale = m / 448.0f;
-            back = 448.0f / m;
-        }
-        if (threadIdx.x == 0) static_cast<float*>(a.scales)[row] = scale;
+        return v;
     }
-    const int padded = (a.cols + 31) / 32 * 32;
-    for (int c = threadIdx.x; c < padded; c += kThreads) {
-        const bool in = c < a.cols;
-        const float s = in ? stream_value<T>(a, row, c) : 0.0f;
-        const float y = in ? (s * inv) * a.weight[c] : 0.0f;
-        if (scale_kind == DL_SCALE_BLOCK32) {
-            uint32_t b = abs_bits(y);
-            for (int o = 16; o > 0; o >>= 1) {
-                const uint32_t u = __shfl_xor(b, o, 32);
-                b = u > b ? u : b;
+}
+
+// Eight e4m3 codes.
+__device__ __forceinline__ uint2 e4m3_of(const float* v) {
+    int a = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+    a = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], a, true);
+    int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);
+    b = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], b, true);
+    return uint2{static_cast<uint32_t>(a), static_cast<uint32_t>(b)};
+}
+
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+
+__device__ __forceinline__ void store_codes(uint8_t* row, int c, int n, uint2 q) {
+    if (c + kCols <= n) {
+        *reinterpret_cast<u32x2_any*>(row + c) = u32x2_any{q.x, q.y};
+    } else {
+        for (int i = 0; i < kCols; ++i)
+            if (c + i < n) row[c + i] = static_cast<uint8_t>((i < 4 ? q.x : q.y) >> (8 * (i % 4)));
+    }
+}
+
+// OUT: element type of y; KIND: its scales.
+template <typename T, int OUT, int KIND, int LANES, int NV>
+__global__ __launch_bounds__(threads_of<LANES>()) void k_rmsnorm(NormArgs a) {
+    constexpr int kThreads = threads_of<LANES>();
+    constexpr int kRows = kThreads / LANES;              // rows at a time
+    __shared__ double lds_d[LANES > kWave ? LANES / kWave : 1];
+    __shared__ uint32_t lds_u[LANES > kWave ? LANES / kWave : 1];
+    const int lane = threadIdx.x % LANES;
+    float w[NV][kCols];
+    for (int i = 0; i < NV; ++i) load8(a.weight, (i * LANES + lane) * kCols, a.cols, w[i]);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / LANES; row < a.rows;
+         row += step) {
+        float s[NV][kCols];
+        const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+        for (int i = 0; i < NV; ++i) load8(x, (i * LANES + lane) * kCols, a.cols, s[i]);
+        if (a.residual != nullptr) {
+            const T* r = static_cast<const T*>(a.residual) + row * a.ldres;
+            float t[NV][kCols];
+            for (int i = 0; i < NV; ++i) load8(r, (i * LANES + lane) * kCols, a.cols, t[i]);
+            for (int i = 0; i < NV; ++i)
+                for (int k = 0; k < kCols; ++k) s[i][k] = to_f32(from_f32<T>(s[i][k] + t[i][k]));
+            if (a.sum != nullptr)
+                for (int i = 0; i < NV; ++i)
+                    store8(static_cast<T*>(a.sum) + row * a.ldsum, (i * LANES + lane) * kCols, a.cols,
+                           s[i]);
+        }
+        double ss = 0;
+        for (int i = 0; i < NV; ++i)
+            for (int k = 0; k < kCols; ++k) {
+                const double d = s[i][k];
+                ss = __builtin_fma(d, d, ss);
             }
-            int e = static_cast<int>((b + 0x1FFFFFu) >> 23) - 8;
-            e = e < 0 ? 0 : e;
-            if (b >= 0x7F800000u) e = 255;
-            back = e == 255 ? 0.0f : __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-            if (c % 32 == 0)
-                static_cast<uint8_t*>(a.scales)[row * (padded / 32) + c / 32] =
-                    static_cast<uint8_t>(e);
+        ss = row_reduce<LANES>(ss, Sum{}, lds_d);
+        const float inv = static_cast<float>(1.0 / sqrt(ss / a.cols + static_cast<double>(a.eps)));
+        if (a.inv_rms != nullptr && lane == 0) a.inv_rms[row] = inv;
+        // y in place of s; columns past the end stay 0 unless inv is infinite
+        uint32_t amax = 0;
+        for (int i = 0; i < NV; ++i)
+            for (int k = 0; k < kCols; ++k) {
+                s[i][k] = (s[i][k] * inv) * w[i][k];
+                if constexpr (KIND != DL_SCALE_NONE)
+                    if ((i * LANES + lane) * kCols + k >= a.cols) s[i][k] = 0.0f;
+                if constexpr (KIND == DL_SCALE_ROW) amax = Max{}(amax, abs_bits(s[i][k]));
+            }
+        if constexpr (KIND == DL_SCALE_ROW) {
+            amax = row_reduce<LANES>(amax, Max{}, lds_u);
+            const float m = __uint_as_float(amax);
+            float scale = 0.0f, back = 0.0f;             // below 2^-100: zeros
+            if (amax >= 0x7F800000u) {
+                scale = __uint_as_float(0x7FC00000u);
+            } else if (m >= 0x1p-100f) {
+                scale = m / 448.0f;
+                back = 448.0f / m;
+            }
+            if (lane == 0) static_cast<float*>(a.scales)[row] = scale;
+            for (int i = 0; i < NV; ++i) {
+                for (int k = 0; k < kCols; ++k) s[i][k] = back == 0.0f ? 0.0f : s[i][k] * back;
+                store_codes(static_cast<uint8_t*>(a.y) + row * a.ldy, (i * LANES + lane) * kCols,
+                            a.cols, e4m3_of(s[i]));
+            }
+        } else if constexpr (KIND == DL_SCALE_BLOCK32) {
+            const int64_t kb = (a.cols + 31) / 32;
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * LANES + lane) * kCols;
+                uint32_t b = 0;
+                for (int k = 0; k < kCols; ++k) b = Max{}(b, abs_bits(s[i][k]));
+                b = lanes_reduce<4>(b, Max{});           // the 32 columns' four lanes
+                // the smallest power of two p with amax <= 448 p = 1.75 * 2^8 p
+                int e = static_cast<int>((b + 0x1FFFFFu) >> 23) - 8;
+                e = e < 0 ? 0 : e;
+                const bool bad = b >= 0x7F800000u;
+                const float back = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+                for (int k = 0; k < kCols; ++k) s[i][k] = bad ? 0.0f : s[i][k] * back;
+                if (lane % 4 == 0 && c < a.cols)
+                    static_cast<uint8_t*>(a.scales)[row * kb + c / 32] =
+                        static_cast<uint8_t>(bad ? 255 : e);
+                store_codes(static_cast<uint8_t*>(a.y) + row * a.ldy, c, a.cols, e4m3_of(s[i]));
+            }
+        } else if constexpr (OUT == DL_F32) {
+            for (int i = 0; i < NV; ++i)
+                store8(static_cast<float*>(a.y) + row * a.ldy, (i * LANES + lane) * kCols, a.cols,
+                       s[i]);
+        } else {
+            for (int i = 0; i < NV; ++i)
+                store8(static_cast<bf16*>(a.y) + row * a.ldy, (i * LANES + lane) * kCols, a.cols,
+                       s[i]);
         }
-        if (!in) continue;
-        if (a.sum != nullptr) static_cast<T*>(a.sum)[row * a.ldsum + c] = from_f32<T>(s);
-        const int64_t at = row * a.ldy + c;
-        if (y_dtype == DL_F32) static_cast<float*>(a.y)[at] = y;
-        else if (y_dtype == DL_BF16) static_cast<bf16*>(a.y)[at] = from_f32<bf16>(y);
-        else static_cast<uint8_t*>(a.y)[at] = back == 0.0f ? 0 : e4m3_of(y * back);
-    }
     }
 }
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void k_rmsnorm_dx(NormBackwardArgs a) {
-    __shared__ float lds[kWaves];
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const float inv = a.inv_rms[row];
-    const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
-    const T* sum = static_cast<const T*>(a.sum) + row * a.ldsum;
-    float c0 = 0;
-    for (int c = threadIdx.x; c < a.cols; c += kThreads)
-        c0 += to_f32(dy[c]) * a.weight[c] * (to_f32(sum[c]) * inv);
-    c0 = block_sum(c0, lds) / static_cast<float>(a.cols);
-    for (int c = threadIdx.x; c < a.cols; c += kThreads) {
-        const float g = to_f32(dy[c]) * a.weight[c], h = to_f32(sum[c]) * inv;
-        float d = inv * (g - h * c0);
-        if (a.dsum != nullptr) d += to_f32(static_cast<const T*>(a.dsum)[row * a.lddsum + c]);
-        static_cast<T*>(a.dx)[row * a.lddx + c] = from_f32<T>(d);
+// dx of the rows, and this workgroup's part of dweight.  With HOLD the row
+// stays in registers between the sum and its use; the longest rows (1024
+// lanes of 128 registers each) are read again instead.
+template <typename T, int LANES, int NV, bool HOLD>
+__global__ __launch_bounds__(threads_of<LANES>()) void k_rmsnorm_backward(NormBackwardArgs a) {
+    constexpr int kThreads = threads_of<LANES>();
+    constexpr int kRows = kThreads / LANES;
+    __shared__ float lds[LANES > kWave ? LANES / kWave : 1];
+    __shared__ float parts[kRows > 1 ? kThreads : 1][kCols];
+    const int lane = threadIdx.x % LANES;
+    float dw[NV][kCols] = {};
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+    // Every lane takes part in every turn: a row past the end is all zeros.
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows; r0 < a.rows; r0 += step) {
+        const int64_t row = r0 + threadIdx.x / LANES;
+        const bool here = row < a.rows;
+        const int n = here ? a.cols : 0;
+        const int64_t at = here ? row : 0;
+        const T* dy = static_cast<const T*>(a.dy) + at * a.lddy;
+        const T* sum = static_cast<const T*>(a.sum) + at * a.ldsum;
+        const float inv = a.inv_rms[at];
+        float y[HOLD ? NV : 1][kCols], s[HOLD ? NV : 1][kCols];
+        float c = 0;
+        for (int i = 0; i < NV; ++i) {
+            const int q = HOLD ? i : 0, col = (i * LANES + lane) * kCols;
+            load8(dy, col, n, y[q]);
+            load8(sum, col, n, s[q]);
+        }
+        for (int i = 0; i < NV; ++i) {
+            const int q = HOLD ? i : 0, col = (i * LANES + lane) * kCols;
+            if constexpr (!HOLD) {
+                load8(dy, col, n, y[q]);
+                load8(sum, col, n, s[q]);
+            }
+            float w[kCols];
+            load8(a.weight, col, a.cols, w);
+            for (int k = 0; k < kCols; ++k) c += (y[q][k] * w[k]) * (s[q][k] * inv);
+        }
+        c = row_reduce<LANES>(c, Sum{}, lds) / static_cast<float>(a.cols);
+        for (int i = 0; i < NV; ++i) {
+            const int q = HOLD ? i : 0, col = (i * LANES + lane) * kCols;
+            if constexpr (!HOLD) {
+                load8(dy, col, n, y[q]);
+                load8(sum, col, n, s[q]);
+            }
+            float w[kCols], d[kCols] = {};
+            load8(a.weight, col, a.cols, w);
+            if (a.dsum != nullptr)
+                load8(static_cast<const T*>(a.dsum) + at * a.lddsum, col, n, d);
+            for (int k = 0; k < kCols; ++k) {
+                const float h = s[q][k] * inv;
+                // (a term of nothing would be NaN where inv is infinite)
+                if (col + k < n) dw[i][k] += y[q][k] * h;
+                const float g = inv * (y[q][k] * w[k] - h * c);
+                d[k] = a.dsum != nullptr ? g + d[k] : g;
+            }
+            store8(static_cast<T*>(a.dx) + at * a.lddx, col, n, d);
+        }
     }
+    if (a.dweight == nullptr) return;
+    float* out = a.partial + static_cast<int64_t>(blockIdx.x) * a.cols;
+    for (int i = 0; i < NV; ++i) {
+        const int col = (i * LANES + lane) * kCols;
+        if constexpr (kRows > 1) {                       // the rows of one turn, in order
+            __syncthreads();
+            for (int k = 0; k < kCols; ++k) parts[threadIdx.x][k] = dw[i][k];
+            __syncthreads();
+            if (threadIdx.x < LANES)
+                for (int r = 1; r < kRows; ++r)
+                    for (int k = 0; k < kCols; ++k) dw[i][k] += parts[threadIdx.x + r * LANES][k];
+        }
+        if (threadIdx.x < LANES) store8(out, col, a.cols, dw[i]);
     }
 }
 
-// One column a thread, rows in order.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void k_rmsnorm_dw(NormBackwardArgs a) {
-    const int c = blockIdx.x * kThreads + threadIdx.x;
-    if (c >= a.cols) return;
+// dweight from the workgroups' parts: 64 columns a workgroup, 16 of its waves
+// take a sixteenth of the parts each.
+constexpr int kSumWaves = 16;
+
+__global__ __launch_bounds__(kSumWaves * kWave) void k_rmsnorm_dw(const float* partial, int parts,
+                                                                  int cols, float* dweight) {
+    __shared__ float lds[kSumWaves][kWave];
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    const int c = blockIdx.x * kWave + lane;
     float t = 0;
-    for (int64_t row = 0; row < a.rows; ++row)
-        t += to_f32(static_cast<const T*>(a.dy)[row * a.lddy + c]) *
-             (to_f32(static_cast<const T*>(a.sum)[row * a.ldsum + c]) * a.inv_rms[row]);
-    a.dweight[c] = t;
+    if (c < cols) {
+#pragma unroll 8
+        for (int p = wave; p < parts; p += kSumWaves) t += partial[static_cast<int64_t>(p) * cols + c];
+    }
+    lds[wave][lane] = t;
+    __syncthreads();
+    if (wave == 0 && c < cols) {
+        for (int i = 1; i < kSumWaves; ++i) t += lds[i][lane];
+        dweight[c] = t;
+    }
+}
+
+// Lanes a row and groups of eight columns a lane: the fewest lanes that hold
+// the row in four groups; few rows take more lanes instead, as one row's time
+// is then all there is.
+struct Shape {
+    int lanes, groups;
+};
+
+Shape shape_of(int64_t rows, int cols) {
+    int lanes = cols <= 512 ? 16 : cols <= 2048 ? 64 : cols <= 8192 ? 256 : 1024;
+    if (rows <= 256 && lanes < 256 && cols > 512) lanes = 256;
+    const int groups = (cols + lanes * kCols - 1) / (lanes * kCols);
+    return Shape{lanes, groups <= 1 ? 1 : groups <= 2 ? 2 : 4};
+}
+
+// Calls f(lanes, groups) with the shape as types.
+template <int N> struct Int {
+    static constexpr int value = N;
+};
+template <typename F> hipError_t with_shape(const Shape& s, F f) {
+    auto groups = [&](auto lanes) {
+        return s.groups == 1 ? f(lanes, Int<1>{})
+               : s.groups == 2 ? f(lanes, Int<2>{}) : f(lanes, Int<4>{});
+    };
+    return s.lanes == 16 ? groups(Int<16>{})
+           : s.lanes == 64 ? groups(Int<64>{})
+           : s.lanes == 256 ? groups(Int<256>{}) : groups(Int<1024>{});
+}
+
+// Workgroups of the forward pass: enough to fill the GPU, and several rows each.
+constexpr int64_t kMaxBlocks = 2048;
+
+template <typename T, int OUT, int KIND> hipError_t forward(const NormArgs& a, hipStream_t s) {
+    return with_shape(shape_of(a.rows, a.cols), [&](auto lanes, auto groups) {
+        constexpr int kLanes = decltype(lanes)::value;
+        constexpr int kRows = threads_of<kLanes>() / kLanes;
+        int64_t blocks = (a.rows + kRows - 1) / kRows;
+        blocks = blocks < kMaxBlocks ? blocks : kMaxBlocks;
+        k_rmsnorm<T, OUT, KIND, kLanes, decltype(groups)::value>
+            <<<dim3(static_cast<unsigned>(blocks)), dim3(threads_of<kLanes>()), 0, s>>>(a);
+        return hipGetLastError();
+    });
+}
+
+template <typename T>
+hipError_t forward_to(const NormArgs& a, int y_dtype, int kind, hipStream_t s) {
+    if (kind == DL_SCALE_ROW) return forward<T, DL_E4M3, DL_SCALE_ROW>(a, s);
+    if (kind == DL_SCALE_BLOCK32) return forward<T, DL_E4M3, DL_SCALE_BLOCK32>(a, s);
+    return y_dtype == DL_F32 ? forward<T, DL_F32, DL_SCALE_NONE>(a, s)
+                             : forward<T, DL_BF16, DL_SCALE_NONE>(a, s);
+}
+
+int64_t backward_blocks(int64_t rows, int cols) {
+    const int lanes = shape_of(rows, cols).lanes;
+    const int at_a_time = lanes < 256 ? 256 / lanes : 1;
+    const int64_t blocks = (rows + at_a_time - 1) / at_a_time;
+    return blocks < kMaxPartials ? blocks : kMaxPartials;
+}
+
+template <typename T> hipError_t backward(const NormBackwardArgs& a, hipStream_t s) {
+    return with_shape(shape_of(a.rows, a.cols), [&](auto lanes, auto groups) {
+        constexpr int kLanes = decltype(lanes)::value;
+        const int64_t blocks = backward_blocks(a.rows, a.cols);
+        k_rmsnorm_backward<T, kLanes, decltype(groups)::value, kLanes <= 256>
+            <<<dim3(static_cast<unsigned>(blocks)), dim3(threads_of<kLanes>()), 0, s>>>(a);
+        return hipGetLastError();
+    });
 }
 
 }  // namespace
 
 hipError_t rmsnorm(const NormArgs& a, int dtype, int y_dtype, int scale_kind, hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>(a.rows < kMaxGrid ? a.rows : kMaxGrid)), block(kThreads);
-    if (dtype == DL_F32) k_rmsnorm<float><<<grid, block, 0, s>>>(a, y_dtype, scale_kind);
-    else k_rmsnorm<bf16><<<grid, block, 0, s>>>(a, y_dtype, scale_kind);
-    return hipGetLastError();
+    return dtype == DL_F32 ? forward_to<float>(a, y_dtype, scale_kind, s)
+                           : forward_to<bf16>(a, y_dtype, scale_kind, s);
 }
 
-int64_t rmsnorm_workspace_bytes(int64_t, int64_t) { return 0; }
+int64_t rmsnorm_workspace_bytes(int64_t rows, int64_t cols) {
+    return rows == 0 ? 0 : backward_blocks(rows, static_cast<int>(cols)) * cols * 4;
+}
 
 hipError_t rmsnorm_backward(const NormBackwardArgs& a, int dtype, hipStream_t s) {
-    const dim3 block(kThreads);
-    if (a.dweight != nullptr) {     // before dx, which may be dy itself
-        const dim3 grid((a.cols + kThreads - 1) / kThreads);
-        if (dtype == DL_F32) k_rmsnorm_dw<float><<<grid, block, 0, s>>>(a);
-        else k_rmsnorm_dw<bf16><<<grid, block, 0, s>>>(a);
-        if (hipError_t e = hipGetLastError()) return e;
+    int64_t parts = 0;
+    if (a.rows > 0) {
+        const hipError_t e = dtype == DL_F32 ? backward<float>(a, s) : backward<bf16>(a, s);
+        if (e != hipSuccess) return e;
+        parts = backward_blocks(a.rows, a.cols);
     }
-    if (a.rows == 0) return hipSuccess;
-    const dim3 grid(static_cast<unsigned>(a.rows < kMaxGrid ? a.rows : kMaxGrid));
-    if (dtype == DL_F32) k_rmsnorm_dx<float><<<grid, block, 0, s>>>(a);
-    else k_rmsnorm_dx<bf16><<<grid, block, 0, s>>>(a);
+    if (a.dweight == nullptr) return hipSuccess;
+    k_rmsnorm_dw<<<dim3(static_cast<unsigned>((a.cols + kWave - 1) / kWave)),
+                   dim3(kSumWaves * kWave), 0, s>>>(a.partial, static_cast<int>(parts), a.cols,
+                                                    a.dweight);
     return hipGetLastError();
 }
 

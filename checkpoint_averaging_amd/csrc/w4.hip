@@ -23,27 +23,6 @@ constexpr int kThreads = 256;
 // rounds to the eight magnitudes (nearest, ties to even) with the scale a power
 // of two, so that nothing but this rounding is inexact.
 
-// Eight elements from column c on of a row of n, 0 past the end.
-template <typename T>
-__device__ __forceinline__ void load8(const T* row, int64_t c, int64_t n, float* v) {
-    constexpr int NV = Vec<T>::n;
-    if (c + 8 <= n) {
-        for (int i = 0; i < 8; i += NV) Vec<T>::unpack(Vec<T>::load(row + c + i), v + i);
-    } else {
-        for (int i = 0; i < 8; ++i) v[i] = c + i < n ? to_f32(row[c + i]) : 0.0f;
-    }
-}
-template <typename T>
-__device__ __forceinline__ void store8(T* row, int64_t c, int64_t n, const float* v) {
-    constexpr int NV = Vec<T>::n;
-    if (c + 8 <= n) {
-        for (int i = 0; i < 8; i += NV) Vec<T>::store(row + c + i, Vec<T>::pack(v + i));
-    } else {
-        for (int i = 0; i < 8; ++i)
-            if (c + i < n) row[c + i] = from_f32<T>(v[i]);
-    }
-}
-
 template <typename F> __device__ __forceinline__ uint32_t bits_of(F v) {
     static_assert(sizeof(F) == 4, "");
     return __builtin_bit_cast(uint32_t, v);
