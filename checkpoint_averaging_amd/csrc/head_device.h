@@ -100,14 +100,33 @@ __device__ __forceinline__ void load8(const T* row, int64_t c, int64_t n, float*
         for (int i = 0; i < 8; ++i) v[i] = c + i < n ? to_f32(row[c + i]) : 0.0f;
     }
 }
+// N elements (1, 2, 4) of a row in one access, at any element.
+template <int N, typename T> __device__ __forceinline__ void store_few(T* p, const float* v) {
+    T t[N];
+    for (int i = 0; i < N; ++i) t[i] = from_f32<T>(v[i]);
+    __builtin_memcpy(p, t, sizeof t);
+}
+
 template <typename T>
 __device__ __forceinline__ void store8(T* row, int64_t c, int64_t n, const float* v) {
     constexpr int NV = Vec<T>::n;
     if (c + 8 <= n) {
         for (int i = 0; i < 8; i += NV) Vec<T>::store(row + c + i, Vec<T>::pack(v + i));
-    } else {
-        for (int i = 0; i < 8; ++i)
-            if (c + i < n) row[c + i] = from_f32<T>(v[i]);
+    } else if (c < n) {
+        const int left = static_cast<int>(n - c);
+        float u[4] = {v[0], v[1], v[2], v[3]};
+        T* p = row + c;
+        if (left & 4) {
+            store_few<4>(p, v);
+            p += 4;
+            for (int i = 0; i < 4; ++i) u[i] = v[4 + i];
+        }
+        if (left & 2) {
+            store_few<2>(p, u);
+            p += 2;
+            u[0] = u[2];
+        }
+        if (left & 1) store_few<1>(p, u);
     }
 }
 

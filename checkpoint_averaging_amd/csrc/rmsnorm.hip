@@ -5,10 +5,9 @@
 //
 // Both directions read each element once, keep the row in registers and write
 // once, so they are bound by these bytes.  A row is shared by 16, 64, 256 or
-// 1024 lanes, the fewest that hold it in four groups of eight columns each:
-// rows of up to 2048 columns need no barrier, and a wave has several rows'
-// loads under way with its neighbours.  The workgroups walk over the rows, so
-// that the weight is loaded once for many of them.
+// 1024 lanes, each with up to four groups of eight neighbouring columns.  The
+// workgroups walk over the rows, so that the weight is loaded, and dweight's
+// part written, once for many of them.
 //
 // What is rounded to 8 bits must not depend on an order of additions, so the
 // mean of squares is summed in binary64 (at most 2^-40 off for any order) and
@@ -27,7 +26,7 @@ namespace dlk {
 namespace {
 
 constexpr int kCols = 8;             // neighbouring columns a lane takes at once
-constexpr int kMaxPartials = 512;    // workgroups of the backward pass
+constexpr int kMaxPartials = 1024;   // workgroups of the backward pass
 
 // Lanes a row, and threads a workgroup.
 template <int LANES> constexpr int threads_of() { return LANES > 256 ? LANES : 256; }
@@ -65,15 +64,28 @@ typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
 __device__ __forceinline__ void store_codes(uint8_t* row, int c, int n, uint2 q) {
     if (c + kCols <= n) {
         *reinterpret_cast<u32x2_any*>(row + c) = u32x2_any{q.x, q.y};
-    } else {
-        for (int i = 0; i < kCols; ++i)
-            if (c + i < n) row[c + i] = static_cast<uint8_t>((i < 4 ? q.x : q.y) >> (8 * (i % 4)));
+    } else if (c < n) {
+        const int left = n - c;
+        uint8_t* p = row + c;
+        uint32_t u = q.x;
+        if (left & 4) {
+            __builtin_memcpy(p, &u, 4);
+            p += 4;
+            u = q.y;
+        }
+        if (left & 2) {
+            const uint16_t h = static_cast<uint16_t>(u);
+            __builtin_memcpy(p, &h, 2);
+            p += 2;
+            u >>= 16;
+        }
+        if (left & 1) *p = static_cast<uint8_t>(u);
     }
 }
 
 // OUT: element type of y; KIND: its scales.
 template <typename T, int OUT, int KIND, int LANES, int NV>
-__global__ __launch_bounds__(threads_of<LANES>()) void k_rmsnorm(NormArgs a) {
+__global__ __launch_bounds__(threads_of<LANES>(), 4) void k_rmsnorm(NormArgs a) {
     constexpr int kThreads = threads_of<LANES>();
     constexpr int kRows = kThreads / LANES;              // rows at a time
     __shared__ double lds_d[LANES > kWave ? LANES / kWave : 1];
@@ -163,7 +175,7 @@ __global__ __launch_bounds__(threads_of<LANES>()) void k_rmsnorm(NormArgs a) {
 }
 
 // dx of the rows, and this workgroup's part of dweight.  With HOLD the row
-// stays in registers between the sum and its use; the longest rows (1024
+// stays in registers between the sum and its use; rows past 8192 columns (1024
 // lanes of 128 registers each) are read again instead.
 template <typename T, int LANES, int NV, bool HOLD>
 __global__ __launch_bounds__(threads_of<LANES>()) void k_rmsnorm_backward(NormBackwardArgs a) {
@@ -259,39 +271,40 @@ __global__ __launch_bounds__(kSumWaves * kWave) void k_rmsnorm_dw(const float* p
     }
 }
 
-// Lanes a row and groups of eight columns a lane: the fewest lanes that hold
-// the row in four groups; few rows take more lanes instead, as one row's time
-// is then all there is.
+// Lanes a row and groups of eight columns a lane.
 struct Shape {
     int lanes, groups;
 };
 
-Shape shape_of(int64_t rows, int cols) {
+// Forward: the fewest lanes that hold the row in four groups, as a wave needs
+// no barrier (16384 x 2048 bf16 to e4m3 with row scales: 50 us, 59 us with 256
+// lanes a row).  Few rows take more lanes, as one row's time is then all there
+// is.
+Shape forward_shape(int64_t rows, int cols) {
     int lanes = cols <= 512 ? 16 : cols <= 2048 ? 64 : cols <= 8192 ? 256 : 1024;
     if (rows <= 256 && lanes < 256 && cols > 512) lanes = 256;
     const int groups = (cols + lanes * kCols - 1) / (lanes * kCols);
     return Shape{lanes, groups <= 1 ? 1 : groups <= 2 ? 2 : 4};
 }
 
-// Calls f(lanes, groups) with the shape as types.
+// Backward: one group a lane, which leaves registers for more waves (8191 x
+// 2048 bf16: 34 us, 45 us with 64 lanes of four groups).
+Shape backward_shape(int cols) {
+    const int lanes = cols <= 128 ? 16 : cols <= 512 ? 64 : cols <= 2048 ? 256 : 1024;
+    const int groups = (cols + lanes * kCols - 1) / (lanes * kCols);
+    return Shape{lanes, groups <= 1 ? 1 : groups <= 2 ? 2 : 4};
+}
+
 template <int N> struct Int {
     static constexpr int value = N;
 };
-template <typename F> hipError_t with_shape(const Shape& s, F f) {
-    auto groups = [&](auto lanes) {
-        return s.groups == 1 ? f(lanes, Int<1>{})
-               : s.groups == 2 ? f(lanes, Int<2>{}) : f(lanes, Int<4>{});
-    };
-    return s.lanes == 16 ? groups(Int<16>{})
-           : s.lanes == 64 ? groups(Int<64>{})
-           : s.lanes == 256 ? groups(Int<256>{}) : groups(Int<1024>{});
-}
 
 // Workgroups of the forward pass: enough to fill the GPU, and several rows each.
 constexpr int64_t kMaxBlocks = 2048;
 
 template <typename T, int OUT, int KIND> hipError_t forward(const NormArgs& a, hipStream_t s) {
-    return with_shape(shape_of(a.rows, a.cols), [&](auto lanes, auto groups) {
+    const Shape shape = forward_shape(a.rows, a.cols);
+    auto launch = [&](auto lanes, auto groups) {
         constexpr int kLanes = decltype(lanes)::value;
         constexpr int kRows = threads_of<kLanes>() / kLanes;
         int64_t blocks = (a.rows + kRows - 1) / kRows;
@@ -299,7 +312,14 @@ template <typename T, int OUT, int KIND> hipError_t forward(const NormArgs& a, h
         k_rmsnorm<T, OUT, KIND, kLanes, decltype(groups)::value>
             <<<dim3(static_cast<unsigned>(blocks)), dim3(threads_of<kLanes>()), 0, s>>>(a);
         return hipGetLastError();
-    });
+    };
+    auto of_groups = [&](auto lanes) {
+        return shape.groups == 1 ? launch(lanes, Int<1>{})
+               : shape.groups == 2 ? launch(lanes, Int<2>{}) : launch(lanes, Int<4>{});
+    };
+    return shape.lanes == 16 ? of_groups(Int<16>{})
+           : shape.lanes == 64 ? of_groups(Int<64>{})
+           : shape.lanes == 256 ? of_groups(Int<256>{}) : of_groups(Int<1024>{});
 }
 
 template <typename T>
@@ -311,20 +331,27 @@ hipError_t forward_to(const NormArgs& a, int y_dtype, int kind, hipStream_t s) {
 }
 
 int64_t backward_blocks(int64_t rows, int cols) {
-    const int lanes = shape_of(rows, cols).lanes;
+    const int lanes = backward_shape(cols).lanes;
     const int at_a_time = lanes < 256 ? 256 / lanes : 1;
     const int64_t blocks = (rows + at_a_time - 1) / at_a_time;
-    return blocks < kMaxPartials ? blocks : kMaxPartials;
+    const int64_t most = lanes > 256 ? kMaxPartials / 2 : kMaxPartials;
+    return blocks < most ? blocks : most;
 }
 
 template <typename T> hipError_t backward(const NormBackwardArgs& a, hipStream_t s) {
-    return with_shape(shape_of(a.rows, a.cols), [&](auto lanes, auto groups) {
-        constexpr int kLanes = decltype(lanes)::value;
+    const Shape shape = backward_shape(a.cols);
+    auto launch = [&](auto lanes, auto groups) {
+        constexpr int kLanes = decltype(lanes)::value, kGroups = decltype(groups)::value;
         const int64_t blocks = backward_blocks(a.rows, a.cols);
-        k_rmsnorm_backward<T, kLanes, decltype(groups)::value, kLanes <= 256>
+        k_rmsnorm_backward<T, kLanes, kGroups, kGroups == 1>
             <<<dim3(static_cast<unsigned>(blocks)), dim3(threads_of<kLanes>()), 0, s>>>(a);
         return hipGetLastError();
-    });
+    };
+    return shape.lanes == 16 ? launch(Int<16>{}, Int<1>{})
+           : shape.lanes == 64 ? launch(Int<64>{}, Int<1>{})
+           : shape.lanes == 256 ? launch(Int<256>{}, Int<1>{})
+           : shape.groups == 1 ? launch(Int<1024>{}, Int<1>{})
+           : shape.groups == 2 ? launch(Int<1024>{}, Int<2>{}) : launch(Int<1024>{}, Int<4>{});
 }
 
 }  // namespace
