@@ -15,7 +15,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from .dlmerge import (DL_BF16, DL_F32, Array, _addr, _check, _stream, _ws, raw_lib)
+from .dlmerge import DL_BF16, DL_F32, Array, _addr, _check, _ws, raw_lib
 
 DL_E4M3 = 2
 DL_SCALE_NONE = 0
@@ -50,6 +50,18 @@ for _name in SYMBOLS:
 _DTYPES = {torch.float32: DL_F32, torch.bfloat16: DL_BF16, torch.float8_e4m3fn: DL_E4M3}
 
 
+def _stream(stream) -> Optional[int]:
+    """The stream's handle; by default the current one of the current device
+    (asked for directly: a torch.cuda.Stream object costs 3 us a call)."""
+    if stream is None:
+        if not torch.cuda.is_initialized():
+            return None
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if isinstance(stream, torch.cuda.Stream):
+        return stream.cuda_stream
+    return int(stream)
+
+
 def _matrix(a: Array, rows: int, cols: int, ld: Optional[int], name: str
             ) -> Tuple[Optional[int], int]:
     """(address, leading dimension) of a rows x cols matrix argument."""
@@ -57,22 +69,25 @@ def _matrix(a: Array, rows: int, cols: int, ld: Optional[int], name: str
         return (None if a is None else int(a)), int(cols if ld is None else ld)
     if not a.is_cuda:
         raise TypeError(f"{name}: device tensor required")
-    if a.dim() == 2:
-        if rows > 0 and (a.shape[0] < rows or a.shape[1] < cols):
-            raise ValueError(f"{name}: {tuple(a.shape)} does not hold {rows} x {cols}")
-        if a.shape[1] > 1 and a.stride(1) != 1:
+    shape, stride = a.shape, a.stride()
+    if len(shape) == 2:
+        if rows > 0 and (shape[0] < rows or shape[1] < cols):
+            raise ValueError(f"{name}: {tuple(shape)} does not hold {rows} x {cols}")
+        if stride[1] != 1 and shape[1] > 1:
             raise TypeError(f"{name}: rows must be contiguous")
-        if ld is None:
-            ld = a.stride(0) if a.shape[0] > 1 else max(cols, a.stride(0))
-        elif ld != a.stride(0) and a.shape[0] > 1:
-            raise ValueError(f"{name}: ld {ld} is not its row stride {a.stride(0)}")
+        if shape[0] == 1:
+            ld = max(cols, stride[0]) if ld is None else ld
+        elif ld is None:
+            ld = stride[0]
+        elif ld != stride[0]:
+            raise ValueError(f"{name}: ld {ld} is not its row stride {stride[0]}")
     else:
-        if a.dim() != 1 or not a.is_contiguous():
+        if len(shape) != 1 or (stride[0] != 1 and shape[0] > 1):
             raise TypeError(f"{name}: 2-D tensor, or contiguous 1-D tensor, required")
         ld = cols if ld is None else ld
-        if rows > 0 and a.numel() < (rows - 1) * ld + cols:
-            raise ValueError(f"{name}: {a.numel()} elements do not hold {rows} x {cols}")
-    return a.data_ptr(), int(ld)
+        if rows > 0 and shape[0] < (rows - 1) * ld + cols:
+            raise ValueError(f"{name}: {shape[0]} elements do not hold {rows} x {cols}")
+    return a.data_ptr(), ld
 
 
 def _dtype_of(a: Array, dtype: Optional[int], name: str) -> int:
@@ -93,6 +108,8 @@ def _same_type(a: Array, dtype: int, name: str) -> None:
 
 def _vector(a: Array, n: int, dtype: torch.dtype, name: str) -> Optional[int]:
     """Address of a contiguous array of at least n elements of dtype."""
+    if a is None:
+        return None
     if isinstance(a, torch.Tensor):
         if a.dtype != dtype:
             raise TypeError(f"{name} must be {dtype}")
