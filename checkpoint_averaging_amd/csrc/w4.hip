@@ -95,8 +95,15 @@ __global__ __launch_bounds__(kThreads) void k_w4_quantize(const T* w, int64_t ld
 // 128 columns): the four products of a span take eight codes each of every
 // lane, whatever columns these are, as x is laid out the same.  The vectors
 // stay in registers: a wave has kSpans spans of them and passes rows by, so
-// x is read once a workgroup, not once a tile.  The waves of a workgroup take
+// x is read once a workgroup, not once a tile (past 2048 columns, again for
+// every 2048; spans enough for 8192 in registers, or the next ones under way,
+// leave too few waves and were slower).  The waves of a workgroup take
 // different spans of the same rows, and their sums meet in LDS.
+//
+// The matrix cores also have a product of 4-bit and 8-bit values with block
+// scales (v_mfma_scale_f32_16x16x128_f8f6f4).  It drops low bits of the smaller
+// of its 128 products, some 1e-5 of the sum of magnitudes: too many for a
+// binary32 result.
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -286,7 +293,9 @@ hipError_t matvec(const MatvecArgs& a, int y_dtype, hipStream_t s) {
     const int64_t groups = (a.rows + 16 * RT - 1) / (16 * RT);
     const int64_t tw = kMatWaves / kw;
     int64_t blocks = (groups + tw - 1) / tw;
-    blocks = blocks < 512 ? blocks : 512;
+    // what is resident at once: two workgroups a CU, one with two tiles of vectors
+    constexpr int64_t kMost = MT == 1 ? 512 : 256;
+    blocks = blocks < kMost ? blocks : kMost;
     const dim3 grid(static_cast<unsigned>(blocks)), block(kMatThreads);
     if (y_dtype == DL_F32) k_w4_matvec<KIND, MT, RT, float><<<grid, block, 0, s>>>(a, kw);
     else k_w4_matvec<KIND, MT, RT, bf16><<<grid, block, 0, s>>>(a, kw);
@@ -294,9 +303,10 @@ hipError_t matvec(const MatvecArgs& a, int y_dtype, hipStream_t s) {
 }
 
 template <int KIND> hipError_t matvec_of(const MatvecArgs& a, int y_dtype, hipStream_t s) {
-    // Four row tiles a wave keep more bytes under way; few rows are spread
-    // over more workgroups instead.
-    const bool many = a.rows >= 16 * 1024;
+    // Two row tiles a wave keep more bytes under way (73760 x 2048: 19 us, 25 us
+    // with one, 22 us with four, which leave room for half the waves); few rows
+    // are spread over more workgroups instead (5632 x 2048: 4.3 us, 5.0 us).
+    const bool many = a.rows >= 8 * 1024;
     if (a.count <= 16)
         return many ? matvec<KIND, 1, 2>(a, y_dtype, s) : matvec<KIND, 1, 1>(a, y_dtype, s);
     return many ? matvec<KIND, 2, 2>(a, y_dtype, s) : matvec<KIND, 2, 1>(a, y_dtype, s);
