@@ -36,8 +36,6 @@ int64_t matrix_bytes(int64_t rows, int64_t cols, int64_t ld, int64_t esize) {
 // lies in a device allocation of the current device.
 class Arrays {
 public:
-    // `may_be` is the index of an input that this output may coincide with
-    // (same pointer and leading dimension), or -1.
     int add(const void* p, int64_t bytes, uintptr_t align, bool written, int64_t ld = 0) {
         if (status_ != DL_OK) return -1;
         if (p == nullptr || bytes < 0) {
@@ -88,7 +86,7 @@ public:
                 (void)hipGetLastError();
                 return DL_E_INVAL;
             }
-            if (at.device != dev) return DL_E_INVAL;
+            if (at.device != dev || at.type == hipMemoryTypeHost) return DL_E_INVAL;
         }
         return DL_OK;
     }

@@ -216,7 +216,7 @@ def check_backward(rows, cols, dtype, with_ds=True, **kw):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,cols", [(1, 1), (1, 2048), (7, 33), (129, 128), (1000, 500),
-                                       (513, 2048), (65, 2050), (33, 5632), (9, 8200), (5, 32768)])
+                                       (513, 2048), (3001, 2048), (65, 2050), (33, 5632), (9, 8200), (5, 32768)])
 def test_norm_backward(rows, cols, dtype):
     check_backward(rows, cols, dtype)
     check_backward(rows, cols, dtype, with_ds=False, pad=3)
@@ -436,6 +436,16 @@ def test_matvec_every_code_scale_and_special_value():
         check_matvec(packed, scales, rows, cols, x, kind, "f32")
 
 
+def test_matvec_of_a_vector_that_stands_for_nan():
+    """x in 8 bits with a NaN block (or row) scale: NaN for that vector alone."""
+    rng = np.random.default_rng(22)
+    packed, scales = random_w4(rng, 50, 160)
+    x = rng.standard_normal((4, 160)).astype(np.float32)
+    x[2, 70] = np.nan
+    check_matvec(packed, scales, 50, 160, x, dh.DL_SCALE_ROW, "f32")
+    check_matvec(packed, scales, 50, 160, x, dh.DL_SCALE_BLOCK32, "bf16")
+
+
 def test_matvec_of_the_embedding():
     """73,760 x 2048 (byte offsets past 2^26, every row tile), whole numbers."""
     rng = np.random.default_rng(2)
@@ -584,6 +594,24 @@ def test_alternatives_of_ordered_and_tied_rows(rows, dtype):
                   np.where(i >= vocab - 300, 3.0 + (i % 5), 0.0), np.where(i == 39_999, 1.0, 0.0)):
             check_logprobs(np.broadcast_to(x, (rows, vocab)).astype(np.float32), [5] * rows,
                            dtype, k)
+
+
+def test_logprobs_more_rows_than_a_grid():
+    """Rows past the launch limits of both directions, of five logits each."""
+    rows, vocab = (1 << 20) + 77, 5
+    x = torch.randn(rows, vocab, device=DEV)
+    t = torch.randint(0, vocab, (rows,), device=DEV)
+    lp, st = torch.empty(rows, device=DEV), torch.empty(rows, 2, device=DEV)
+    ids, top = torch.empty(rows, 1, dtype=torch.int64, device=DEV), torch.empty(rows, 1, device=DEV)
+    dh.dl_logprobs(x, rows, vocab, t, lp, stats=st, top_k=1, top_ids=ids, top_logprobs=top)
+    d = torch.empty_like(x)
+    dh.dl_logprobs_backward(x, rows, vocab, t, st, torch.ones(rows, device=DEV), d)
+    want = torch.log_softmax(x.double(), 1)
+    tol = 16 * U * (1 + x.abs().max().item() + 4)            # a few roundings of small values
+    assert (lp - want.gather(1, t[:, None])[:, 0]).abs().max().item() < tol
+    assert torch.equal(ids[:, 0], x.argmax(1))
+    hot = torch.zeros_like(want).scatter_(1, t[:, None], 1.0)
+    assert (d - (hot - want.exp())).abs().max().item() < 2 * tol
 
 
 def test_logprobs_targets_outside_the_vocabulary():
