@@ -8,6 +8,12 @@
 // nearly certain token's log probability and entropy keep their digits.  R
 // comes from the threads' sums but for the one that the maximum's own 1 went
 // through: its elements (one 256th of the row) are read once more.
+//
+// The pass is bound by the logits' bytes, with some ten instructions and one
+// exponential (four instructions' time) an element close behind: 2048 x 73760
+// bf16 56 us (5.4 TB/s; a plain read of them takes 50), 777 x 50277 fp32 with
+// five alternatives 34 us.  One row is a chain of latencies: 10 us with eight
+// alternatives, in 16 parts and two kernels, 13 us in one.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -255,14 +261,16 @@ __device__ __forceinline__ void choose(TopLds& s, const T* l, uint32_t n, uint32
 
 // What a row is split into: `parts` workgroups of `chunk` elements each.
 //
-// A workgroup a row fills the GPU from about 300 rows on; fewer are split, as
-// long as a part has 4096 elements, and a second kernel joins the parts.
+// A workgroup a row fills the GPU from about 300 rows on (300 x 50304: 17 us
+// either way).  Fewer are split, into parts of at least 4096 elements that a
+// second kernel joins, if they are long enough to win its 3 us back (one row
+// of 40000 bf16: 5.2 us in parts, 7.1 us whole; of 10000: 5.0 us, 3.8 us).
 struct Split {
     uint32_t parts, chunk;
 };
 
 Split split_of(int64_t rows, int64_t vocab) {
-    int64_t parts = rows < 512 ? 512 / rows : 1;
+    int64_t parts = rows < 512 && vocab >= 24 * 1024 ? 512 / rows : 1;
     parts = parts < kMaxParts ? parts : kMaxParts;
     const int64_t most = (vocab + 4095) / 4096;
     parts = parts < most ? parts : most;

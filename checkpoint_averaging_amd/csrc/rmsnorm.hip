@@ -9,6 +9,12 @@
 // workgroups walk over the rows, so that the weight is loaded, and dweight's
 // part written, once for many of them.
 //
+// Measured: 16384 x 2048 bf16 with the residual's addition to e4m3 with row
+// scales 50 us (4.7 TB/s; a large copy reaches 4.9), block scales 52 us; the
+// same rows 2047 long, whose ends are single elements, to bf16 67 us (2048: 53
+// us); 8191 x 2048 bf16 forward 27 us and backward 34 us with dweight's sum 4
+// us; one row 2.7 us.
+//
 // What is rounded to 8 bits must not depend on an order of additions, so the
 // mean of squares is summed in binary64 (at most 2^-40 off for any order) and
 // everything after it is single binary32 operations.

@@ -446,6 +446,19 @@ def test_matvec_of_a_vector_that_stands_for_nan():
     check_matvec(packed, scales, 50, 160, x, dh.DL_SCALE_BLOCK32, "bf16")
 
 
+def test_matvec_of_small_factors():
+    """Factors on one side near 2^-126 and below, large ones on the other, whole
+    multiples: results in the normal range are the exact ones."""
+    rng = np.random.default_rng(23)
+    rows, cols = 48, 160
+    packed, scales = random_w4(rng, rows, cols, 1, 4)            # weights of 2^-127 to 6 * 2^-124
+    x = (rng.integers(-7, 8, (3, cols)) * 2.0 ** 100).astype(np.float32)
+    check_matvec(packed, scales, rows, cols, x, dh.DL_SCALE_NONE, "f32", exact=True)
+    packed, scales = random_w4(rng, rows, cols, 220, 223)
+    x = (rng.integers(-7, 8, (3, cols)) * 2.0 ** -126).astype(np.float32)
+    check_matvec(packed, scales, rows, cols, x, dh.DL_SCALE_NONE, "f32", exact=True)
+
+
 def test_matvec_of_the_embedding():
     """73,760 x 2048 (byte offsets past 2^26, every row tile), whole numbers."""
     rng = np.random.default_rng(2)
