@@ -37,8 +37,8 @@ inline bool hip_error_pending() {
 // A host pointer or a span running past its allocation is rejected here
 // instead of faulting the GPU.  Every call reaches this check before its
 // launch, so a pending HIP error is reported here as DL_E_HIP, before the
-// runtime is asked anything.
-inline int check_device_span(const void* p, int64_t bytes) {
+// runtime is asked anything.  `allocation`, if given, receives the allocation.
+inline int check_device_span(const void* p, int64_t bytes, Span* allocation = nullptr) {
     if (p == nullptr) return DL_E_INVAL;
     if (hip_error_pending()) return DL_E_HIP;
     hipDeviceptr_t base = nullptr;
@@ -50,6 +50,7 @@ inline int check_device_span(const void* p, int64_t bytes) {
     const uintptr_t b = reinterpret_cast<uintptr_t>(base);
     const uintptr_t a = reinterpret_cast<uintptr_t>(p);
     if (a < b || bytes < 0 || static_cast<uint64_t>(bytes) > size - (a - b)) return DL_E_INVAL;
+    if (allocation != nullptr) *allocation = Span{b, b + size};
     return DL_OK;
 }
 

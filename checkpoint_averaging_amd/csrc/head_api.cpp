@@ -78,9 +78,19 @@ public:
             }
             if (sdev != dev) return DL_E_INVAL;
         }
+        // Small tensors of one program share allocations: the runtime is asked
+        // once for each that the call meets.
+        Span known[kMost];
+        int n_known = 0;
         for (int i = 0; i < n_; ++i) {
             if (item_[i].bytes == 0) continue;
-            if (int st = check_device_span(item_[i].p, item_[i].bytes)) return st;
+            const Span s = span_of(item_[i].p, item_[i].bytes);
+            bool found = false;
+            for (int j = 0; j < n_known && !found; ++j)
+                found = s.lo >= known[j].lo && s.hi >= s.lo && s.hi <= known[j].hi;
+            if (found) continue;
+            if (int st = check_device_span(item_[i].p, item_[i].bytes, &known[n_known])) return st;
+            ++n_known;
             hipPointerAttribute_t at;
             if (hipPointerGetAttributes(&at, item_[i].p) != hipSuccess) {
                 (void)hipGetLastError();

@@ -314,9 +314,10 @@ __device__ __forceinline__ float rest_of(float* lds, int* owner, const T* l, uin
                                          const Stats& mine, const Stats& row) {
     constexpr int NV = Vec<T>::n;
     const int tid = threadIdx.x;
-    if (mine.m == row.m) *owner = tid;        // one thread: two would make S 2
+    const bool owns = mine.s > 0.0f && mine.m == row.m;
+    if (owns) *owner = tid;                   // one thread: two would make S 2
     __syncthreads();
-    float r = mine.m == row.m ? 0.0f : mine.s * exp_of(fmaxf(mine.m - row.m, kFar));
+    float r = owns ? 0.0f : mine.s * exp_of(fmaxf(mine.m - row.m, kFar));
     const uint32_t steps = (n + kThreads * NV - 1) / (kThreads * NV);
     for (uint32_t j = tid; j < steps; j += kThreads) {
         const uint32_t at = (j * kThreads + *owner) * NV;

@@ -15,7 +15,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from .dlmerge import DL_BF16, DL_F32, Array, _addr, _check, _ws, raw_lib
+from .dlmerge import DL_BF16, DL_F32, Array, _check, _ws, raw_lib
 
 DL_E4M3 = 2
 DL_SCALE_NONE = 0
@@ -47,6 +47,7 @@ _lib.dl_logprobs_backward.argtypes = [_p, _i64, _i32, _i64, _i64, _p, _p, _p, _p
 for _name in SYMBOLS:
     getattr(_lib, _name).restype = _i32
 
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 _DTYPES = {torch.float32: DL_F32, torch.bfloat16: DL_BF16, torch.float8_e4m3fn: DL_E4M3}
 
 
@@ -56,7 +57,7 @@ def _stream(stream) -> Optional[int]:
     if stream is None:
         if not torch.cuda.is_initialized():
             return None
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _raw_stream(_current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -110,12 +111,15 @@ def _vector(a: Array, n: int, dtype: torch.dtype, name: str) -> Optional[int]:
     """Address of a contiguous array of at least n elements of dtype."""
     if a is None:
         return None
-    if isinstance(a, torch.Tensor):
-        if a.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}")
-        if a.numel() < n:
-            raise ValueError(f"{name}: {a.numel()} elements, {n} needed")
-    return _addr(a)
+    if not isinstance(a, torch.Tensor):
+        return int(a)
+    if a.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if not (a.is_cuda and a.is_contiguous()):
+        raise TypeError(f"{name}: contiguous device tensor required")
+    if a.numel() < n:
+        raise ValueError(f"{name}: {a.numel()} elements, {n} needed")
+    return a.data_ptr()
 
 
 def _scales(a: Array, kind: int, rows: int, cols: int, name: str) -> Optional[int]:

@@ -191,8 +191,9 @@ int dl_w4_matvec(const uint8_t *packed, const uint8_t *scales, int64_t rows, int
  * entropy 0 and stats (-infinity, 0).  A row with a NaN or +infinity gives NaN
  * (its top_ids are still as above).
  *
- * workspace: dl_logprobs_workspace_bytes bytes (0 for many rows: then NULL is
- * allowed).  1 <= vocab <= 2^31 - 1; rows = 0 is a no-op.
+ * workspace: dl_logprobs_workspace_bytes bytes (a few long rows are split over
+ * the GPU; 0 for many rows or short ones: then NULL is allowed).  1 <= vocab <=
+ * 2^31 - 1; rows = 0 is a no-op.
  */
 int dl_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int top_k, int64_t *bytes);
 int dl_logprobs(const void *logits, int64_t ldl, int dtype, int64_t rows, int64_t vocab,
