@@ -12,8 +12,8 @@
 // Measured: 16384 x 2048 bf16 with the residual's addition to e4m3 with row
 // scales 50 us (4.7 TB/s; a large copy reaches 4.9), block scales 52 us; the
 // same rows 2047 long, whose ends are single elements, to bf16 67 us (2048: 53
-// us); 8191 x 2048 bf16 forward 27 us and backward 34 us with dweight's sum 4
-// us; one row 2.7 us.
+// us); 8191 x 2048 bf16 forward 28 us, backward 34 us and dweight's sum 3 us; one
+// row 2.7 us.
 //
 // What is rounded to 8 bits must not depend on an order of additions, so the
 // mean of squares is summed in binary64 (at most 2^-40 off for any order) and
@@ -255,26 +255,33 @@ __global__ __launch_bounds__(threads_of<LANES>()) void k_rmsnorm_backward(NormBa
     }
 }
 
-// dweight from the workgroups' parts: 64 columns a workgroup, 16 of its waves
-// take a sixteenth of the parts each.
-constexpr int kSumWaves = 16;
+// dweight from the workgroups' parts: 16 columns a workgroup, whose 64 groups
+// of 16 threads take every 64th part.  A chain of loads and little else, so many
+// threads share it (1024 parts of 2048 columns: 2 us less than the 5 us of 64
+// columns and 16 groups a workgroup).
+constexpr int kSumCols = 16, kSumGroups = 64;
 
-__global__ __launch_bounds__(kSumWaves * kWave) void k_rmsnorm_dw(const float* partial, int parts,
-                                                                  int cols, float* dweight) {
-    __shared__ float lds[kSumWaves][kWave];
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-    const int c = blockIdx.x * kWave + lane;
+__global__ __launch_bounds__(kSumCols * kSumGroups) void k_rmsnorm_dw(const float* partial,
+                                                                      int parts, int cols,
+                                                                      float* dweight) {
+    __shared__ float lds[kSumGroups][kSumCols];
+    const int g = threadIdx.x / kSumCols, k = threadIdx.x % kSumCols;
+    const int c = blockIdx.x * kSumCols + k;
     float t = 0;
     if (c < cols) {
 #pragma unroll 8
-        for (int p = wave; p < parts; p += kSumWaves) t += partial[static_cast<int64_t>(p) * cols + c];
+        for (int p = g; p < parts; p += kSumGroups) t += partial[static_cast<int64_t>(p) * cols + c];
     }
-    lds[wave][lane] = t;
-    __syncthreads();
-    if (wave == 0 && c < cols) {
-        for (int i = 1; i < kSumWaves; ++i) t += lds[i][lane];
-        dweight[c] = t;
+    for (int n = kSumGroups; n > 1; n /= 8) {             // eight groups' sums into one, in order
+        lds[g][k] = t;
+        __syncthreads();
+        if (g < n / 8) {
+            t = lds[8 * g][k];
+            for (int i = 1; i < 8; ++i) t += lds[8 * g + i][k];
+        }
+        __syncthreads();
     }
+    if (g == 0 && c < cols) dweight[c] = t;
 }
 
 // Lanes a row and groups of eight columns a lane.
@@ -379,9 +386,9 @@ hipError_t rmsnorm_backward(const NormBackwardArgs& a, int dtype, hipStream_t s)
         parts = backward_blocks(a.rows, a.cols);
     }
     if (a.dweight == nullptr) return hipSuccess;
-    k_rmsnorm_dw<<<dim3(static_cast<unsigned>((a.cols + kWave - 1) / kWave)),
-                   dim3(kSumWaves * kWave), 0, s>>>(a.partial, static_cast<int>(parts), a.cols,
-                                                    a.dweight);
+    k_rmsnorm_dw<<<dim3(static_cast<unsigned>((a.cols + kSumCols - 1) / kSumCols)),
+                   dim3(kSumCols * kSumGroups), 0, s>>>(a.partial, static_cast<int>(parts), a.cols,
+                                                        a.dweight);
     return hipGetLastError();
 }
 
