@@ -182,7 +182,6 @@ template <typename T, typename Op> __device__ __forceinline__ T wave_reduce(T v,
     return op(op(lane_value(v, 0), lane_value(v, 16)), op(lane_value(v, 32), lane_value(v, 48)));
 }
 template <typename T> __device__ __forceinline__ T wave_sum(T v) { return wave_reduce(v, Sum{}); }
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) { return wave_reduce(v, Max{}); }
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
