@@ -60,7 +60,7 @@ class Head:
         self.embed = flat[off:off + names["embed"]].view(self.vocab, self.width)
         self.eps, self.max_rows, dev = eps, max_rows, flat.device
         self._blocks = (self.width + 31) // 32
-        self._packed = self._scales = self._product_ws = None
+        self._packed = self._scales = None
 
         def new(*shape, dtype=torch.float32):
             return torch.empty(*shape, dtype=dtype, device=dev)
@@ -77,6 +77,10 @@ class Head:
                                                   min(dh.DL_MAX_TOP, self.vocab))
                    for r in range(1, min(max_rows, 512) + 1))
         self._ws = new(max(need, 256), dtype=torch.uint8)
+        # (a graph that captured score() keeps this address, so no call may replace it)
+        need = max(dl.dl_matmul_workspace_bytes(r, self.vocab, self.width)
+                   for r in range(1, max_rows + 1))
+        self._product_ws = new(max(need, 256), dtype=torch.uint8)
 
     def publish(self) -> None:
         """Lays the embedding, as it is now, out in 4 bits."""
@@ -120,12 +124,13 @@ class Head:
         dh.dl_rmsnorm(x, rows, self.width, self.weight, self._h, eps=self.eps,
                       residual=residual, sum_=sum_, inv_rms=self._inv)
         if rows > 0:
-            need = dl.dl_matmul_workspace_bytes(rows, self.vocab, self.width)
-            if self._product_ws is None or self._product_ws.numel() < need:
-                self._product_ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+            # The bytes it is told of decide how the product is cut: those of these rows, so
+            # that max_rows does not change the bits.
             dl.dl_matmul_f32(dl.DL_NT, self._h, self.width, self.embed, self.width, rows,
                              self.vocab, self.width, self._logits, self.vocab,
-                             workspace=self._product_ws if need else None)
+                             workspace=self._product_ws,
+                             workspace_bytes=dl.dl_matmul_workspace_bytes(rows, self.vocab,
+                                                                          self.width))
         return self._read(rows, targets, top_k)
 
     def _read(self, rows: int, targets: Optional[torch.Tensor], top_k: int) -> Answer:

@@ -1,0 +1,49 @@
+"""The Head's own rules, on the CPU: the library's calls are replaced by ones
+that record their arguments, so nothing is launched."""
+import pytest
+import torch
+
+from checkpoint_averaging_amd import dlhead as dh
+from checkpoint_averaging_amd import dlmerge as dl
+from checkpoint_averaging_amd import synth
+from checkpoint_averaging_amd.head import Head
+
+WIDTH, VOCAB = 96, 1000
+LAYOUT = synth.Layout("small", (("embed", VOCAB * WIDTH), ("final_norm.weight", WIDTH)))
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """(name, arguments) of each library call that would have launched."""
+    made = []
+
+    def record(module, name):
+        monkeypatch.setattr(module, name, lambda *a, **k: made.append((name, a, k)))
+
+    record(dl, "dl_matmul_f32")
+    for name in ("dl_rmsnorm", "dl_w4_quantize", "dl_w4_matvec", "dl_logprobs"):
+        record(dh, name)
+    return made
+
+
+def products(calls):
+    return [k for name, _, k in calls if name == "dl_matmul_f32"]
+
+
+@pytest.mark.parametrize("order", [(4, 300, 1000), (1000, 4, 300)], ids=["growing", "shrinking"])
+def test_score_keeps_one_product_workspace(calls, order):
+    """The need grows with the rows here (384 KiB for 4, more for 300 and 1000),
+    and every call has the same memory, which no later call gives back: a call
+    captured into a graph keeps its address."""
+    head = Head(LAYOUT, torch.zeros(LAYOUT.n_params), max_rows=1000)
+    for rows in order:
+        head.score(torch.zeros(rows, WIDTH))
+    needs = [dl.dl_matmul_workspace_bytes(r, VOCAB, WIDTH) for r in order]
+    assert len(set(needs)) == 3
+    made = products(calls)
+    assert len({k["workspace"].data_ptr() for k in made}) == 1
+    for k, need in zip(made, needs):
+        assert k["workspace"].numel() * k["workspace"].element_size() >= need
+        # the product's plan goes by the bytes it is told of: those of its own rows,
+        # whatever the head could hold and whatever ran before
+        assert k["workspace_bytes"] == need
