@@ -91,7 +91,9 @@ class Head:
             self._scales = torch.empty(scales, dtype=torch.uint8, device=dev)
         dh.dl_w4_quantize(self.embed, self.vocab, self.width, self._packed, self._scales)
 
-    def _rows(self, x: torch.Tensor) -> int:
+    def _rows(self, x: torch.Tensor, top_k: int = 0) -> int:
+        if not 0 <= top_k <= min(dh.DL_MAX_TOP, self.vocab):
+            raise ValueError(f"top_k: 0 to {min(dh.DL_MAX_TOP, self.vocab)} required, got {top_k}")
         if x.dim() != 2 or x.shape[1] != self.width or x.shape[0] > self.max_rows:
             raise ValueError(f"x: at most {self.max_rows} x {self.width} required, got "
                              f"{tuple(x.shape)}")
@@ -104,7 +106,7 @@ class Head:
         (DL_MAX_VECTORS tokens a pass), log probabilities."""
         if self._packed is None:
             raise RuntimeError("publish() first")
-        rows = self._rows(x)
+        rows = self._rows(x, top_k)
         dh.dl_rmsnorm(x, rows, self.width, self.weight, self._h8, eps=self.eps,
                       residual=residual, scales=self._h8_scales,
                       scale_kind=dh.DL_SCALE_BLOCK32)
@@ -120,7 +122,7 @@ class Head:
               sum_: Optional[torch.Tensor] = None) -> Answer:
         """The same from the candidate's own fp32 embedding (dl_matmul_f32).
         sum_, if given, receives x + residual (backward() wants it)."""
-        rows = self._rows(x)
+        rows = self._rows(x, top_k)
         dh.dl_rmsnorm(x, rows, self.width, self.weight, self._h, eps=self.eps,
                       residual=residual, sum_=sum_, inv_rms=self._inv)
         if rows > 0:

@@ -47,3 +47,23 @@ def test_score_keeps_one_product_workspace(calls, order):
         # the product's plan goes by the bytes it is told of: those of its own rows,
         # whatever the head could hold and whatever ran before
         assert k["workspace_bytes"] == need
+
+
+@pytest.mark.parametrize("top_k", [-1, dh.DL_MAX_TOP + 1])
+@pytest.mark.parametrize("rows", [1, 4])
+def test_head_refuses_alternatives_before_any_launch(calls, rows, top_k):
+    """The same error for any number of rows, with the last answer still in the buffers."""
+    head = Head(LAYOUT, torch.zeros(LAYOUT.n_params), max_rows=4)
+    head.publish()
+    calls.clear()
+    for call in (head.score, head.answer):
+        with pytest.raises(ValueError, match="top_k"):
+            call(torch.zeros(rows, WIDTH), top_k=top_k)
+    assert not calls
+    few = synth.Layout("few", (("embed", 5 * WIDTH), ("final_norm.weight", WIDTH)))
+    head = Head(few, torch.zeros(few.n_params), max_rows=4)
+    with pytest.raises(ValueError, match="top_k"):
+        head.score(torch.zeros(rows, WIDTH), top_k=6)                # of five tokens
+    assert not calls
+    head.score(torch.zeros(rows, WIDTH), top_k=5)
+    assert [name for name, _, _ in calls] == ["dl_rmsnorm", "dl_matmul_f32", "dl_logprobs"]
