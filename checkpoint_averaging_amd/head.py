@@ -48,8 +48,10 @@ class Head:
         names = dict(layout.tensors)
         if "final_norm.weight" not in names or "embed" not in names:
             raise ValueError(f"{layout.name}: no RMS norm and tied embedding at its end")
-        if flat.dtype != torch.float32 or flat.numel() != layout.n_params:
-            raise ValueError("flat: the layout's parameters in float32 required")
+        if (flat.dtype != torch.float32 or flat.numel() != layout.n_params or
+                not flat.is_contiguous()):
+            raise ValueError("flat: the layout's parameters in float32 required, contiguous")
+        flat = flat.view(-1)
         if max_rows < 1:
             raise ValueError("max_rows must be at least 1")
         self.width = names["final_norm.weight"]

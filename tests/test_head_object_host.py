@@ -67,3 +67,17 @@ def test_head_refuses_alternatives_before_any_launch(calls, rows, top_k):
     assert not calls
     head.score(torch.zeros(rows, WIDTH), top_k=5)
     assert [name for name, _, _ in calls] == ["dl_rmsnorm", "dl_matmul_f32", "dl_logprobs"]
+
+
+def test_head_takes_its_views_from_the_elements_in_order():
+    """A flat vector seen as a matrix is the same vector; one with gaps has no
+    views that the kernels could read."""
+    n = LAYOUT.n_params
+    flat = torch.arange(n, dtype=torch.float32)
+    for shape in ((n,), (n // 2, 2), (1, n)):
+        head = Head(LAYOUT, flat.view(shape), max_rows=4)
+        assert torch.equal(head.embed, flat[:VOCAB * WIDTH].view(VOCAB, WIDTH))
+        assert torch.equal(head.weight, flat[VOCAB * WIDTH:])
+        assert head.weight.data_ptr() == flat.data_ptr() + 4 * VOCAB * WIDTH
+    with pytest.raises(ValueError, match="flat"):
+        Head(LAYOUT, torch.zeros(2 * n)[::2], max_rows=4)
