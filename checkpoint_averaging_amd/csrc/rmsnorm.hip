@@ -203,11 +203,12 @@ __global__ __launch_bounds__(threads_of<LANES>()) void k_rmsnorm_backward(NormBa
         const float inv = a.inv_rms[at];
         float y[HOLD ? NV : 1][kCols], s[HOLD ? NV : 1][kCols];
         float c = 0;
-        for (int i = 0; i < NV; ++i) {
-            const int q = HOLD ? i : 0, col = (i * LANES + lane) * kCols;
-            load8(dy, col, n, y[q]);
-            load8(sum, col, n, s[q]);
-        }
+        if constexpr (HOLD)
+            for (int i = 0; i < NV; ++i) {
+                const int col = (i * LANES + lane) * kCols;
+                load8(dy, col, n, y[i]);
+                load8(sum, col, n, s[i]);
+            }
         for (int i = 0; i < NV; ++i) {
             const int q = HOLD ? i : 0, col = (i * LANES + lane) * kCols;
             if constexpr (!HOLD) {
@@ -326,9 +327,11 @@ template <typename T, int OUT, int KIND> hipError_t forward(const NormArgs& a, h
             <<<dim3(static_cast<unsigned>(blocks)), dim3(threads_of<kLanes>()), 0, s>>>(a);
         return hipGetLastError();
     };
+    // (64 lanes come with 513 columns or more, 1024 with 8193, so with two groups at least)
     auto of_groups = [&](auto lanes) {
-        return shape.groups == 1 ? launch(lanes, Int<1>{})
-               : shape.groups == 2 ? launch(lanes, Int<2>{}) : launch(lanes, Int<4>{});
+        if constexpr (decltype(lanes)::value == 16 || decltype(lanes)::value == 256)
+            if (shape.groups == 1) return launch(lanes, Int<1>{});
+        return shape.groups <= 2 ? launch(lanes, Int<2>{}) : launch(lanes, Int<4>{});
     };
     return shape.lanes == 16 ? of_groups(Int<16>{})
            : shape.lanes == 64 ? of_groups(Int<64>{})
