@@ -62,8 +62,8 @@ struct MatvecArgs {
     void* y;
     int64_t ldy;
 };
-hipError_t w4_matvec(const MatvecArgs& a, int x_dtype, int x_scale_kind, int y_dtype,
-                     hipStream_t s);
+// x in bfloat16 with DL_SCALE_NONE, in e4m3 with the other kinds
+hipError_t w4_matvec(const MatvecArgs& a, int x_scale_kind, int y_dtype, hipStream_t s);
 
 struct LogprobsArgs {
     const void* logits;

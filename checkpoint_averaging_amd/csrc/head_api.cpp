@@ -260,8 +260,7 @@ int dl_w4_matvec(const uint8_t* packed, const uint8_t* scales, int64_t rows, int
     a.out(y, matrix_bytes(count, rows, ldy, ye), ye);
     if (int st = a.check(stream)) return st;
     const dlk::MatvecArgs k{packed, scales, rows, cols, x, ldx, x_scales, count, y, ldy};
-    return launched(
-        dlk::w4_matvec(k, x_dtype, x_scale_kind, y_dtype, static_cast<hipStream_t>(stream)));
+    return launched(dlk::w4_matvec(k, x_scale_kind, y_dtype, static_cast<hipStream_t>(stream)));
 }
 
 int dl_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int top_k, int64_t* bytes) {

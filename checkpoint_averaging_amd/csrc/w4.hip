@@ -333,7 +333,7 @@ hipError_t w4_quantize(const void* w, int64_t ldw, int dtype, int64_t rows, int6
     return hipGetLastError();
 }
 
-hipError_t w4_matvec(const MatvecArgs& a, int, int x_scale_kind, int y_dtype, hipStream_t s) {
+hipError_t w4_matvec(const MatvecArgs& a, int x_scale_kind, int y_dtype, hipStream_t s) {
     if (x_scale_kind == DL_SCALE_NONE) return matvec_of<DL_SCALE_NONE>(a, y_dtype, s);
     if (x_scale_kind == DL_SCALE_ROW) return matvec_of<DL_SCALE_ROW>(a, y_dtype, s);
     return matvec_of<DL_SCALE_BLOCK32>(a, y_dtype, s);
