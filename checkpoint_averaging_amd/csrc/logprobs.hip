@@ -11,9 +11,10 @@
 //
 // The pass is bound by the logits' bytes, with some ten instructions and one
 // exponential (four instructions' time) an element close behind: 2048 x 73760
-// bf16 56 us (5.4 TB/s; a plain read of them takes 50), 777 x 50277 fp32 with
-// five alternatives 34 us.  One row is a chain of latencies: 10 us with eight
-// alternatives, in 16 parts and two kernels, 13 us in one.
+// bf16 54 us (5.6 TB/s; a plain read of them takes 50), fp32 95 us (6.4 TB/s),
+// 777 x 50277 fp32 with five alternatives 34 us.  One row is a chain of
+// latencies: 10 us with eight alternatives, in 16 parts and two kernels, 13 us in
+// one.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -52,7 +53,11 @@ template <int N> struct Count {
     __device__ constexpr operator int() const { return N; }
 };
 
-// exp(d) for d <= 0; NaN stays NaN.
+// exp(d) for d <= 0; NaN stays NaN.  The product with log2(e) is rounded once, so
+// a term is off by some |d| 2^-23 of itself beside the exponential's own last
+// place: terms far below the maximum, which weigh little in S.  (Log
+// probabilities and entropies come out 6e-8 to 8e-8 from the exact ones, 4e-8 to
+// 6e-8 by torch's operations in fp32.)
 __device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
 
 __device__ __forceinline__ float nan_f() { return __uint_as_float(0x7FC00000u); }
@@ -261,16 +266,18 @@ __device__ __forceinline__ void choose(TopLds& s, const T* l, uint32_t n, uint32
 
 // What a row is split into: `parts` workgroups of `chunk` elements each.
 //
-// A workgroup a row fills the GPU from about 300 rows on (300 x 50304: 17 us
-// either way).  Fewer are split, into parts of at least 4096 elements that a
-// second kernel joins, if they are long enough to win its 3 us back (one row
-// of 40000 bf16: 5.2 us in parts, 7.1 us whole; of 10000: 5.0 us, 3.8 us).
+// Up to 256 rows, one for each CU, are split into parts of at least 4096
+// elements that a second kernel joins, if they are long enough to win its 3 us
+// back (one row of 40000 bf16: 5.2 us in parts, 7.1 us whole; of 10000: 5.0 us,
+// 3.8 us).  From 257 rows on a row is one workgroup's: 256 x 50304 in two parts
+// and 257 whole are 13.2 and 15.3 us in fp32, 11.4 and 10.0 us in bf16 (with 20
+// alternatives 19.1 and 20.9, 16.2 and 15.4).
 struct Split {
     uint32_t parts, chunk;
 };
 
 Split split_of(int64_t rows, int64_t vocab) {
-    int64_t parts = rows < 512 && vocab >= 24 * 1024 ? 512 / rows : 1;
+    int64_t parts = rows <= 256 && vocab >= 24 * 1024 ? 512 / rows : 1;
     parts = parts < kMaxParts ? parts : kMaxParts;
     const int64_t most = (vocab + 4095) / 4096;
     parts = parts < most ? parts : most;
@@ -345,8 +352,8 @@ __global__ __launch_bounds__(kThreads, 8) void k_logprobs(LogprobsArgs a, uint32
     __shared__ int owner;
     __shared__ char top_lds[TOP ? sizeof(TopLds) : 1] __attribute__((aligned(16)));
     const int tid = threadIdx.x;
-    // Fewer than 512 rows are in parts, so jobs, and all indices within a row
-    // (below 2^31), are whole numbers of 32 bits.
+    // At most 256 rows are in parts, so jobs, and all indices within a row (below
+    // 2^31), are whole numbers of 32 bits.
     const uint32_t jobs = static_cast<uint32_t>(a.rows) * parts;
     for (uint32_t job = blockIdx.x; job < jobs; job += gridDim.x) {
         const uint32_t r0 = job / parts;

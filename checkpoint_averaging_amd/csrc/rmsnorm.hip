@@ -3,17 +3,23 @@
 //   s = x + residual ; inv = 1/sqrt(mean s^2 + eps) ; y = (s inv) w
 //   g = dy w ; h = s inv ; dx = inv (g - h mean(g h)) + dsum ; dw = sum dy h
 //
-// Both directions read each element once, keep the row in registers and write
-// once, so they are bound by these bytes.  A row is shared by 16, 64, 256 or
-// 1024 lanes, each with up to four groups of eight neighbouring columns.  The
-// workgroups walk over the rows, so that the weight is loaded, and dweight's
-// part written, once for many of them.
+// Forward, and backward for rows of up to 8192 columns, each element is read
+// once and the row kept in registers, so these are bound by the bytes in and
+// out.  A row is shared by 16, 64, 256 or 1024 lanes, each with up to four
+// groups of eight neighbouring columns.  The workgroups walk over the rows, so
+// that the weight is loaded, and dweight's part written, once for many of them.
 //
-// Measured: 16384 x 2048 bf16 with the residual's addition to e4m3 with row
-// scales 50 us (4.7 TB/s; a large copy reaches 4.9), block scales 52 us; the
-// same rows 2047 long, whose ends are single elements, to bf16 67 us (2048: 53
-// us); 8191 x 2048 bf16 forward 28 us, backward 34 us and dweight's sum 3 us; one
-// row 2.7 us.
+// Measured (out of the caches; a large copy reaches 4.9 TB/s): 16384 x 2048 bf16
+// with the residual's addition to e4m3 with row scales 50 us (4.7 TB/s), block
+// scales 52 us; the same rows 2047 long, whose ends are single elements, to bf16
+// 67 us (2048: 53 us); 8191 x 2048 bf16 forward 28 us, backward 34 us and
+// dweight's sum 5 us; one row 2.8 us.  fp32 in and out 5.3 to 5.7 TB/s from 2048
+// to 32768 columns, to e4m3 with block scales 4.2 to 5.1.
+//
+// Four groups a lane take all 128 registers: most e4m3 forms then, and some of
+// 256 lanes to the other types, put up to 32 of them (12 to 72 bytes a lane) into
+// scratch memory.  It shows most where the bytes are fewest: 47662 x 5632 bf16 to
+// e4m3 with block scales 312 us (2.6 TB/s; to bf16 215 us, 5.0).
 //
 // What is rounded to 8 bits must not depend on an order of additions, so the
 // mean of squares is summed in binary64 (at most 2^-40 off for any order) and
@@ -182,7 +188,10 @@ __global__ __launch_bounds__(threads_of<LANES>(), 4) void k_rmsnorm(NormArgs a) 
 
 // dx of the rows, and this workgroup's part of dweight.  With HOLD the row
 // stays in registers between the sum and its use; rows past 8192 columns (1024
-// lanes of 128 registers each) are read again instead.
+// lanes of 128 registers each) are read again instead: 8192 x 16384 fp32 391 us
+// (4.1 TB/s of the bytes that one read and one write take), and past 16384
+// columns, where dweight's sums spill too (some 450 bytes a lane), 4096 x 32768
+// 553 us (2.9 TB/s; 16384 x 8192, held: 300 us, 5.4).
 template <typename T, int LANES, int NV, bool HOLD>
 __global__ __launch_bounds__(threads_of<LANES>()) void k_rmsnorm_backward(NormBackwardArgs a) {
     constexpr int kThreads = threads_of<LANES>();
@@ -258,8 +267,8 @@ __global__ __launch_bounds__(threads_of<LANES>()) void k_rmsnorm_backward(NormBa
 
 // dweight from the workgroups' parts: 16 columns a workgroup, whose 64 groups
 // of 16 threads take every 64th part.  A chain of loads and little else, so many
-// threads share it (1024 parts of 2048 columns: 2 us less than the 5 us of 64
-// columns and 16 groups a workgroup).
+// threads share it (1024 parts of 128 columns: 3.6 us, 4.4 us with 64 columns and
+// 16 groups a workgroup; of 2048 columns 5 us either way).
 constexpr int kSumCols = 16, kSumGroups = 64;
 
 __global__ __launch_bounds__(kSumCols * kSumGroups) void k_rmsnorm_dw(const float* partial,

@@ -16,6 +16,11 @@ layers below it, which give the residual stream, are the caller's.
     a = head.answer(x, residual, top_k=8)        # from the published one
 
 Results are views of the head's buffers: the next call on it writes over them.
+All buffers, workspaces included, are taken when the head is built and the
+published embedding when it is first published; they stay where they are, so
+calls may be captured into a graph.  Calls on one head go in one stream's order
+(one head for each stream otherwise, and for graphs that may run at once), and a
+head outlives the work that uses it.
 """
 from __future__ import annotations
 
@@ -105,7 +110,8 @@ class Head:
                targets: Optional[torch.Tensor] = None, top_k: int = 0) -> Answer:
         """The published head's answer for the residual stream x (+ residual),
         in bf16 or fp32: norm in 8 bits with block scales, 4-bit product
-        (DL_MAX_VECTORS tokens a pass), log probabilities."""
+        (DL_MAX_VECTORS tokens a pass), log probabilities.  (With more bits in
+        the stream: dl_rmsnorm to bf16 and dl_w4_matvec.)"""
         if self._packed is None:
             raise RuntimeError("publish() first")
         rows = self._rows(x, top_k)
@@ -163,7 +169,9 @@ class Head:
                  dweight: Optional[torch.Tensor] = None,
                  workspace: Optional[torch.Tensor] = None) -> None:
         """The norm's gradients for the gradient dy of its output, after the
-        score() that left sum_ (or took it as x)."""
+        score() that left sum_ (or took it as x).  dy = dlogits x embedding is
+        the caller's product: for n rows, dl_matmul_f32(DL_TN,
+        dlogits.t().contiguous(), n, embed, width, n, width, vocab, dy, width)."""
         rows = self._rows(sum_)
         dh.dl_rmsnorm_backward(dy, sum_, rows, self.width, self.weight, self._inv, dx,
                                dweight=dweight, workspace=workspace)

@@ -159,8 +159,9 @@ int dl_w4_quantize(const void *w, int64_t ldw, int dtype, int64_t rows, int64_t 
  *   y         count x rows of y_dtype (DL_F32 or DL_BF16).
  *
  * Products are exact and summed in binary32 on the matrix cores (block scales
- * of x are applied in bf16, exact for values of at least 2^-133; products and
- * partial sums below 2^-126 may count as 0).  Any code
+ * of x are applied in bf16, exact for values of at least 2^-133; a row scale
+ * multiplies the sum of its codes' products, which is what has to fit binary32;
+ * products and partial sums below 2^-126 may count as 0).  Any code
  * and scale byte is accepted; an element of W that stands for 2^128 or more is
  * infinite.  rows = 0 is a no-op; cols >= 1.
  */
