@@ -11,7 +11,7 @@
 //
 // The pass is bound by the logits' bytes, with some ten instructions and one
 // exponential (four instructions' time) an element close behind: 2048 x 73760
-// bf16 54 us (5.6 TB/s; a plain read of them takes 50), fp32 95 us (6.4 TB/s),
+// bf16 54 us (5.6 TB/s; a plain read of them takes 50), fp32 92 us (6.5 TB/s),
 // 777 x 50277 fp32 with five alternatives 34 us.  One row is a chain of
 // latencies: 10 us with eight alternatives, in 16 parts and two kernels, 13 us in
 // one.
@@ -32,6 +32,9 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 constexpr int kUnroll = 4;          // 16-byte loads a thread has under way
 constexpr int kTogether = 2;        // of these, vectors whose maximum is taken together
+// Vectors of a row that the threads' sums go through before they start anew: 64
+// turns of kUnroll loads, so no row of fewer than 262144 elements does.
+constexpr uint32_t kRun = 64 * kUnroll * kThreads;
 constexpr int64_t kMaxGrid = 1 << 20;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLowest = -3.40282347e38f;
@@ -56,41 +59,30 @@ template <int N> struct Count {
 // exp(d) for d <= 0; NaN stays NaN.  The product with log2(e) is rounded once, so
 // a term is off by some |d| 2^-23 of itself beside the exponential's own last
 // place: terms far below the maximum, which weigh little in S.  (Log
-// probabilities and entropies come out 6e-8 to 8e-8 from the exact ones, 4e-8 to
-// 6e-8 by torch's operations in fp32.)
+// probabilities of 2048 x 73760 come out 3e-8 off, root mean square, as by torch's
+// operations in fp32; entropies 5e-8.)
 __device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
 
 __device__ __forceinline__ float nan_f() { return __uint_as_float(0x7FC00000u); }
 __device__ __forceinline__ float minus_inf() { return __uint_as_float(0xFF800000u); }
 
-// Running statistics of the elements seen so far.  The first maximum is the
-// lowest finite value: an element of -infinity then adds exp(-infinity) = 0,
-// one of +infinity or NaN turns S into NaN.  r is the sum without the (single)
+// Statistics of some elements of a row.  r is the sum without the (single)
 // maximum, where S is below 1.5.
 struct Stats {
     float m, s, r, t;
 
     static __device__ __forceinline__ Stats none() { return Stats{kLowest, 0.0f, 0.0f, 0.0f}; }
 
-    // Moves the maximum up to m2 > m: every element seen is below it.  The
-    // distance is cut off where its exponential is 0, or 0 * infinity would
-    // make a NaN of it.
-    __device__ __forceinline__ void raise(float m2) {
-        const float d = fmaxf(m - m2, kFar), a = exp_of(d);
-        t = a * (t + d * s);
-        s *= a;
-        m = m2;
-    }
-    // Adds an element that is not above the maximum.
-    template <bool ENTROPY> __device__ __forceinline__ void add(float l) {
-        const float d = l - m, e = exp_of(d);
-        s += e;
-        if constexpr (ENTROPY) t = __builtin_fmaf(e, fmaxf(d, kFar), t);
-    }
     // The same elements against a maximum m2 >= m.
     __device__ __forceinline__ Stats at(float m2) const {
         const float d = fmaxf(m - m2, kFar), a = exp_of(d);
         return m == m2 ? *this : Stats{m2, a * s, a * s, a * (t + d * s)};
+    }
+    // The statistics (without r) of these elements and of others.
+    __device__ __forceinline__ Stats with(const Stats& o) const {
+        const float m2 = fmaxf(m, o.m);
+        const Stats p = at(m2), q = o.at(m2);
+        return Stats{m2, p.s + q.s, 0.0f, p.t + q.t};
     }
     // The statistics of 16 neighbouring lanes, or of the wave (without r), in one.
     __device__ __forceinline__ Stats of_lanes() const {
@@ -107,6 +99,46 @@ struct Stats {
     __device__ __forceinline__ float log_sum() const {
         return nothing() ? 0.0f : nearly_certain() ? log1pf(r) : logf(s);
     }
+};
+
+// A thread's running statistics.  The first maximum is the lowest finite value:
+// an element of -infinity then adds exp(-infinity) = 0, one of +infinity or NaN
+// turns S into NaN.
+//
+// Equal terms round the same way at each addition, so that a chain of them shows
+// at its full length (150001 logits of two values, 586 a thread in one chain: log
+// S 9e-6 off; 2^30 of them: 3e-3).  Up to 16 elements are therefore added to each
+// other first, and their sum to the thread's, which starts anew after kRun: 9e-7
+// and 2e-6.
+struct Running {
+    float m, s, t;
+
+    static __device__ __forceinline__ Running none() { return Running{kLowest, 0.0f, 0.0f}; }
+
+    // Moves the maximum up to m2 > m: every element seen is below it.  The
+    // distance is cut off where its exponential is 0, or 0 * infinity would
+    // make a NaN of it.
+    template <bool ENTROPY> __device__ __forceinline__ void raise(float m2) {
+        const float d = fmaxf(m - m2, kFar), a = exp_of(d);
+        if constexpr (ENTROPY) t = a * (t + d * s);
+        s *= a;
+        m = m2;
+    }
+    // Adds N elements that are not above the maximum.
+    template <bool ENTROPY, int N> __device__ __forceinline__ void add(const float* l) {
+        float gs, gt;
+        for (int i = 0; i < N; ++i) {
+            const float d = l[i] - m, e = exp_of(d);
+            gs = i == 0 ? e : gs + e;
+            if constexpr (ENTROPY) {
+                const float f = fmaxf(d, kFar);
+                gt = i == 0 ? e * f : __builtin_fmaf(e, f, gt);
+            }
+        }
+        s += gs;
+        if constexpr (ENTROPY) t += gt;
+    }
+    __device__ __forceinline__ Stats stats() const { return Stats{m, s, 0.0f, t}; }
 };
 
 // The order of alternatives as whole numbers: larger logits first, NaN before
@@ -270,8 +302,8 @@ __device__ __forceinline__ void choose(TopLds& s, const T* l, uint32_t n, uint32
 // elements that a second kernel joins, if they are long enough to win its 3 us
 // back (one row of 40000 bf16: 5.2 us in parts, 7.1 us whole; of 10000: 5.0 us,
 // 3.8 us).  From 257 rows on a row is one workgroup's: 256 x 50304 in two parts
-// and 257 whole are 13.2 and 15.3 us in fp32, 11.4 and 10.0 us in bf16 (with 20
-// alternatives 19.1 and 20.9, 16.2 and 15.4).
+// and 257 whole are 12.5 and 14.0 us in fp32, 11.2 and 10.3 us in bf16 (with 20
+// alternatives 18.5 and 19.9, 16.7 and 15.8).
 struct Split {
     uint32_t parts, chunk;
 };
@@ -369,40 +401,63 @@ __global__ __launch_bounds__(kThreads, 8) void k_logprobs(LogprobsArgs a, uint32
             target = a.targets[row];
             if (target >= 0 && target < a.vocab) target_logit = to_f32(whole[target]);
         }
-        Stats st = Stats::none();
+        Running run = Running::none();
+        Stats before = Stats::none();             // of the runs before this one
         const uint32_t full = n / NV;             // whole vectors
         uint32_t v = tid;
-        // The maximum is looked at once for kTogether vectors.
-        auto take = [&](const raw* r, auto count) {
-            float x[decltype(count)::value][NV];
-            float mx = kLowest;
-            for (int u = 0; u < count; ++u) {
-                Vec<T>::unpack(r[u], x[u]);
-                for (int i = 0; i < NV; ++i) mx = fmaxf(mx, x[u][i]);
-            }
-            if (mx > st.m) st.raise(mx);
-            for (int u = 0; u < count; ++u)
-                for (int i = 0; i < NV; ++i) st.template add<ENTROPY>(x[u][i]);
+        auto max_of = [&](const raw& r) {
+            float x[NV], mx = kLowest;
+            Vec<T>::unpack(r, x);
+            for (int i = 0; i < NV; ++i) mx = fmaxf(mx, x[i]);
+            return mx;
         };
-        for (; v + (kUnroll - 1) * kThreads < full; v += kUnroll * kThreads) {
-            raw r[kUnroll];
-            for (int u = 0; u < kUnroll; ++u)
-                r[u] = Vec<T>::template load<NT>(l + static_cast<size_t>(v + u * kThreads) * NV);
-            for (int u = 0; u < kUnroll; u += kTogether) take(r + u, Count<kTogether>{});
+        // The maximum is looked at once for kTogether vectors; mx is the first one's.
+        auto take = [&](const raw* r, float mx, auto count) {
+            constexpr int kElems = decltype(count)::value * NV;
+            float x[kElems];
+            for (int u = 0; u < count; ++u) Vec<T>::unpack(r[u], x + u * NV);
+            for (int i = NV; i < kElems; ++i) mx = fmaxf(mx, x[i]);
+            if (mx > run.m) {
+                // (no instruction: keeps the branch, as the few instructions of a seldom
+                // raise are a tenth of the pass where every group does them)
+                __asm__("" : "+v"(mx));
+                run.template raise<ENTROPY>(mx);
+            }
+            run.template add<ENTROPY, kElems>(x);
+        };
+        uint32_t end = full < kRun ? full : kRun;
+        for (;;) {
+            for (; v + (kUnroll - 1) * kThreads < end; v += kUnroll * kThreads) {
+                // The last two loads go out once the first has come (777 x 50304 fp32: 25
+                // us, 27 us with all four at once; 2048 x 73760: 91 us, 89 us).
+                raw r[kUnroll];
+                float first;
+                for (int u = 0; u < kUnroll; ++u) {
+                    if (u == kTogether) __builtin_amdgcn_sched_barrier(0);
+                    r[u] = Vec<T>::template load<NT>(l + static_cast<size_t>(v + u * kThreads) * NV);
+                    if (u == kTogether - 1) first = max_of(r[0]);
+                }
+                for (int u = 0; u < kUnroll; u += kTogether)
+                    take(r + u, u == 0 ? first : max_of(r[u]), Count<kTogether>{});
+            }
+            if (end == full) break;
+            before = before.with(run.stats());
+            run = Running::none();
+            end = full - end < kRun ? full : end + kRun;
         }
         for (; v < full; v += kThreads) {
             const raw r = Vec<T>::load(l + static_cast<size_t>(v) * NV);
-            take(&r, Count<1>{});
+            take(&r, max_of(r), Count<1>{});
         }
         if (v == full) {                          // the row's last, partial vector
             for (uint32_t i = full * NV; i < n; ++i) {
                 const float x = to_f32(l[i]);
-                if (x > st.m) st.raise(x);
-                st.template add<ENTROPY>(x);
+                if (x > run.m) run.template raise<ENTROPY>(x);
+                run.template add<ENTROPY, 1>(&x);
             }
         }
-        const Stats mine = st;
-        st = st.of_wave();
+        const Stats mine = full <= kRun ? run.stats() : before.with(run.stats());
+        Stats st = mine.of_wave();
         if (tid % kWave == 0) lds[tid / kWave] = st;
         __syncthreads();
         {

@@ -13,7 +13,7 @@
 // with the residual's addition to e4m3 with row scales 50 us (4.7 TB/s), block
 // scales 52 us; the same rows 2047 long, whose ends are single elements, to bf16
 // 67 us (2048: 53 us); 8191 x 2048 bf16 forward 28 us, backward 34 us and
-// dweight's sum 5 us; one row 2.8 us.  fp32 in and out 5.3 to 5.7 TB/s from 2048
+// dweight's sum 5 us; one row 2.5 us.  fp32 in and out 5.3 to 5.7 TB/s from 2048
 // to 32768 columns, to e4m3 with block scales 4.2 to 5.1.
 //
 // Four groups a lane take all 128 registers: most e4m3 forms then, and some of

@@ -186,7 +186,9 @@ int dl_w4_matvec(const uint8_t *packed, const uint8_t *scales, int64_t rows, int
  *
  * log S is formed as log1p of the other elements' sum, so the log probability
  * and entropy of a nearly certain token keep their relative accuracy
- * (exponentials below 2^-126 may count as 0).  Logits
+ * (exponentials below 2^-126 may count as 0).  S is off by at most 1e-5 of itself
+ * for up to 2^18 tokens and 4e-5 for more (equal terms; some 1e-7 otherwise).
+ * Logits
  * of -infinity (masked tokens) have probability 0 and log probability
  * -infinity.  A row of nothing else has log probability -infinity everywhere,
  * entropy 0 and stats (-infinity, 0).  A row with a NaN or +infinity gives NaN

@@ -323,6 +323,42 @@ def test_logprobs_gradient_of_an_infinite_loss_weight_stays_in_its_row():
     assert torch.equal(d[[0, 3]], want[[0, 3]])
 
 
+@pytest.mark.parametrize("level", [-1.17, -3.3, -6.9])
+@pytest.mark.parametrize("rows,vocab,dtype", [(2, 73_760, "bf16"), (260, 150_001, "f32"),
+                                              (260, 1 << 20, "bf16"), (1, (1 << 30) + 7, "bf16")])
+def test_log_sum_of_many_equal_logits(rows, vocab, dtype, level):
+    """Every 101st token at 0 (so every thread meets one early) and all others at
+    the same level: S = n0 + (vocab - n0) e^level.  Equal terms added one by one
+    round the same way every time, so a chain of additions would show at its full
+    length.  A term is off by 2^-22 + 3 u |level| (see sum_error) and each
+    addition by one rounding: 16 elements (8 in fp32) in a group, the groups of a
+    thread in runs of at most 128, 5 for what is left of a row, one for each
+    run, 8 for the threads, 4 for the parts.  Log S adds 3 roundings of its own; the
+    entropy is log S and a quotient of two such sums times |level|."""
+    group = 16 if dtype == "bf16" else 8
+    mine = vocab / (16 if rows <= 256 else 1) / 256                  # a thread's share
+    chain = group + min(128, mine / group) + 5 + mine // (128 * group) + 12
+    x = torch.full((rows, vocab), level, device=DEV, dtype=hg.TORCH[dtype])
+    x[:, ::101] = 0
+    n0 = -(-vocab // 101)
+    level = float(x[0, 1])
+    t = torch.full((rows,), vocab - 1, dtype=torch.int64, device=DEV)
+    lp, h, st = (torch.full(n, 9.0, device=DEV) for n in ((rows,), (rows,), (rows, 2)))
+    need = dh.dl_logprobs_workspace_bytes(rows, vocab)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV) if need else None
+    dh.dl_logprobs(x, rows, vocab, t, lp, h, st, workspace=ws)
+    rest = (vocab - n0) * np.exp(level)
+    log_s = np.log(n0 + rest)
+    es = 2.0 ** -22 + 3 * hg.U * abs(level) + chain * hg.U
+    hg.within(hg.host(st)[:, 1], np.full(rows, log_s), es + 3 * hg.U * log_s, "log sum")
+    hg.within(hg.host(lp), np.full(rows, level - log_s),
+              es + 4 * hg.U * log_s + 2 * hg.U * (log_s - level), "logprobs")
+    mean = rest * level / (n0 + rest)
+    hg.within(hg.host(h), np.full(rows, log_s - mean),
+              es + 4 * hg.U * log_s + (2 * es + 4 * hg.U) * abs(mean), "entropy")
+    assert bool((st[:, 0] == 0).all())
+
+
 # --------------------------------------------------------------------------
 # The training path through the library's calls alone
 # --------------------------------------------------------------------------
