@@ -359,6 +359,86 @@ def test_log_sum_of_many_equal_logits(rows, vocab, dtype, level):
     assert bool((st[:, 0] == 0).all())
 
 
+def split_logprobs(x, t, ws, k, stream=None):
+    rows, vocab = x.shape
+    out = dict(logprobs=torch.empty(rows, device=DEV), entropy=torch.empty(rows, device=DEV),
+               stats=torch.empty(rows, 2, device=DEV),
+               top_ids=torch.empty(rows, k, dtype=torch.int64, device=DEV),
+               top_logprobs=torch.empty(rows, k, device=DEV))
+    dh.dl_logprobs(x, rows, vocab, t, top_k=k, workspace=ws, stream=stream, **out)
+    return out
+
+
+def test_split_rows_in_two_graphs_and_on_two_streams_at_once():
+    """Rows in parts, whose results meet in a workspace: one each for two graphs
+    that are replayed at the same time, and for two streams given by argument."""
+    rows, vocab, k = 9, 60_000, 11
+    need = dh.dl_logprobs_workspace_bytes(rows, vocab, k)
+    assert need > 0
+    g = torch.Generator(device=DEV).manual_seed(51)
+    xs = [torch.empty(rows, vocab, device=DEV) for _ in range(2)]
+    ts = [torch.randint(0, vocab, (rows,), generator=g, device=DEV) for _ in range(2)]
+    wss = [torch.empty(need, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for x in xs:
+        x.normal_(generator=g)
+    for x, t, ws in zip(xs, ts, wss):
+        split_logprobs(x, t, ws, k)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for x, t, ws in zip(xs, ts, wss):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(split_logprobs(x, t, ws, k))
+    for _ in range(4):
+        for x in xs:
+            x.normal_(generator=g).mul_(3)
+        torch.cuda.synchronize()
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        want = [split_logprobs(x, t, torch.empty(need, dtype=torch.uint8, device=DEV), k)
+                for x, t in zip(xs, ts)]
+        torch.cuda.synchronize()
+        got = [split_logprobs(x, t, ws, k, stream=s)
+               for x, t, ws, s in zip(xs, ts, wss, streams)]
+        torch.cuda.synchronize()
+        for a, b, c in zip(outs, want, got):
+            for name in a:
+                assert torch.equal(a[name], b[name]), name
+                assert torch.equal(c[name], b[name]), name
+
+
+def test_published_in_a_graph_follows_the_candidate():
+    """publish() and answer() captured together: each replay lays out the flat
+    vector as it is then, and eager work on the same head in between is its own."""
+    global_, ema = hp.merged()
+    flat = global_.clone()
+    head = Head(hp.LAYOUT, flat, 40)
+    x, r, t = hp.stream(20, 3)
+    head.publish()
+    head.answer(x, r, t, top_k=5)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        head.publish()
+        a = head.answer(x, r, t, top_k=5)
+        got = [v.clone() for v in (a.logits, a.logprobs, a.entropy, a.top_ids)]
+    for k, source in enumerate((ema, global_, ema, global_)):
+        flat.copy_(source)
+        head.publish()
+        head.answer(*hp.stream(33, 60 + k), top_k=3)
+        torch.cuda.synchronize()
+        graph.replay()
+        other = Head(hp.LAYOUT, source, 20)
+        other.publish()
+        b = other.answer(x, r, t, top_k=5)
+        torch.cuda.synchronize()
+        for u, v in zip(got, (b.logits, b.logprobs, b.entropy, b.top_ids)):
+            assert torch.equal(u, v)
+
+
 # --------------------------------------------------------------------------
 # The training path through the library's calls alone
 # --------------------------------------------------------------------------
