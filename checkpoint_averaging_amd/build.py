@@ -23,7 +23,8 @@ ARCH = "gfx950"
 SOURCES = [os.path.join(CSRC, "kernels.hip"), os.path.join(CSRC, "polar.hip"),
            os.path.join(CSRC, "noalloc.hip"), os.path.join(CSRC, "api.cpp"),
            os.path.join(CSRC, "rmsnorm.hip"), os.path.join(CSRC, "w4.hip"),
-           os.path.join(CSRC, "logprobs.hip"), os.path.join(CSRC, "head_api.cpp")]
+           os.path.join(CSRC, "logprobs.hip"), os.path.join(CSRC, "headloss.hip"),
+           os.path.join(CSRC, "e4m3.hip"), os.path.join(CSRC, "head_api.cpp")]
 DRIVER = os.path.join(PKG, "dlmerge_driver")
 DRIVER_SOURCES = [os.path.join(CSRC, "merge_driver.hip")]
 POLAR_DRIVER = os.path.join(PKG, "dlpolar_driver")

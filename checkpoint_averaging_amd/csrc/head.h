@@ -97,4 +97,62 @@ struct LogprobsBackwardArgs {
 };
 hipError_t logprobs_backward(const LogprobsBackwardArgs& a, int dtype, hipStream_t s);
 
+struct HeadArgs {
+    const void* x;
+    int64_t ldx;
+    const void* embed;
+    int64_t lde;
+    int64_t rows;
+    int64_t vocab;
+    int64_t width;
+    const int64_t* targets;      // or nullptr
+    float* logprobs;             // or nullptr
+    float* entropy;              // or nullptr
+    float* stats;                // or nullptr
+    void* workspace;             // head_workspace_bytes
+};
+int64_t head_workspace_bytes(int64_t rows, int64_t vocab, int64_t width, int dtype,
+                             bool with_backward);
+hipError_t head_logprobs(const HeadArgs& a, int dtype, hipStream_t s);
+
+struct HeadBackwardArgs {
+    const void* x;
+    int64_t ldx;
+    const void* embed;
+    int64_t lde;
+    int64_t rows;
+    int64_t vocab;
+    int64_t width;
+    const int64_t* targets;
+    const float* stats;
+    const float* entropy;        // or nullptr
+    const float* dlogprobs;
+    const float* dentropy;       // or nullptr
+    void* dx;                    // or nullptr
+    int64_t lddx;
+    void* dembed;                // or nullptr
+    int64_t ldde;
+    void* workspace;             // head_workspace_bytes, with the backward pass
+};
+hipError_t head_logprobs_backward(const HeadBackwardArgs& a, int dtype, hipStream_t s);
+
+hipError_t e4m3_quantize(const void* x, int64_t ldx, int dtype, int64_t rows, int64_t cols,
+                         uint8_t* codes, int64_t ldc, uint8_t* scales, int scale_kind,
+                         void* values, int64_t ldvalues, hipStream_t s);
+
+struct E4m3ProductArgs {
+    const uint8_t* w;
+    int64_t ldw;
+    const uint8_t* w_scales;
+    int64_t rows;
+    int64_t cols;
+    const uint8_t* x;
+    int64_t ldx;
+    const uint8_t* x_scales;
+    int64_t count;
+    void* y;
+    int64_t ldy;
+};
+hipError_t e4m3_matmul(const E4m3ProductArgs& a, int y_dtype, hipStream_t s);
+
 }  // namespace dlk

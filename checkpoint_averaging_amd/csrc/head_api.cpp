@@ -128,8 +128,20 @@ int launched(hipError_t e) { return e == hipSuccess ? DL_OK : DL_E_HIP; }
 
 // Bytes of the scales of a rows x cols matrix; 0 for DL_SCALE_NONE.
 int64_t scale_bytes(int kind, int64_t rows, int64_t cols) {
-    return kind == DL_SCALE_ROW ? 4 * rows : kind == DL_SCALE_BLOCK32 ? rows * ((cols + 31) / 32) : 0;
+    const int64_t blocks = (cols + 127) / 128;
+    return kind == DL_SCALE_ROW        ? 4 * rows
+           : kind == DL_SCALE_BLOCK32  ? rows * ((cols + 31) / 32)
+           : kind == DL_SCALE_BLOCK128 ? rows * blocks
+           : kind == DL_SCALE_TILE128  ? (rows + 127) / 128 * blocks
+                                       : 0;
 }
+
+// Scales that a norm writes with its e4m3 output.
+bool norm_scale(int kind) {
+    return kind == DL_SCALE_ROW || kind == DL_SCALE_BLOCK32 || kind == DL_SCALE_BLOCK128;
+}
+
+bool dim(int64_t n, int64_t least) { return n >= least && n <= kMaxDim; }
 
 }  // namespace
 
@@ -140,8 +152,7 @@ int dl_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldres, 
                int64_t ldsum, void* y, int64_t ldy, int y_dtype, void* scales, int scale_kind,
                float* inv_rms, void* stream) {
     if (!float_type(dtype) || !(float_type(y_dtype) || y_dtype == DL_E4M3)) return DL_E_INVAL;
-    if (y_dtype == DL_E4M3 ? (scale_kind != DL_SCALE_ROW && scale_kind != DL_SCALE_BLOCK32)
-                           : scale_kind != DL_SCALE_NONE)
+    if (y_dtype == DL_E4M3 ? !norm_scale(scale_kind) : scale_kind != DL_SCALE_NONE)
         return DL_E_INVAL;
     if ((scales != nullptr) != (scale_kind != DL_SCALE_NONE)) return DL_E_INVAL;
     if (rows < 0 || rows > kMaxDim || cols < 1 || cols > DL_MAX_NORM_COLS) return DL_E_INVAL;
@@ -326,6 +337,114 @@ int dl_logprobs_backward(const void* logits, int64_t ldl, int dtype, int64_t row
     const dlk::LogprobsBackwardArgs k{logits,  ldl,       rows,     vocab,   targets, stats,
                                       entropy, dlogprobs, dentropy, dlogits, lddl};
     return launched(dlk::logprobs_backward(k, dtype, static_cast<hipStream_t>(stream)));
+}
+
+int dl_head_workspace_bytes(int64_t rows, int64_t vocab, int64_t width, int dtype, int backward,
+                            int64_t* bytes) {
+    if (bytes == nullptr || !float_type(dtype) || !dim(rows, 0) || !dim(vocab, 1) || width < 1 ||
+        width > DL_MAX_NORM_COLS)
+        return DL_E_INVAL;
+    if (rows > 0 && vocab + width > (int64_t(1) << 50) / rows) return DL_E_INVAL;
+    *bytes = rows == 0 ? 0 : dlk::head_workspace_bytes(rows, vocab, width, dtype, backward != 0);
+    return DL_OK;
+}
+
+int dl_head_logprobs(const void* x, int64_t ldx, const void* embed, int64_t lde, int dtype,
+                     int64_t rows, int64_t vocab, int64_t width, const int64_t* targets,
+                     float* logprobs, float* entropy, float* stats, void* workspace,
+                     int64_t workspace_bytes, void* stream) {
+    int64_t need = 0;
+    if (int st = dl_head_workspace_bytes(rows, vocab, width, dtype, 0, &need)) return st;
+    if ((targets != nullptr) != (logprobs != nullptr)) return DL_E_INVAL;
+    if (rows == 0) return DL_OK;
+    if (workspace == nullptr || workspace_bytes < need) return DL_E_INVAL;
+    const int64_t e = esize_of(dtype);
+    Arrays a;
+    a.in(x, matrix_bytes(rows, width, ldx, e), e);
+    a.in(embed, matrix_bytes(vocab, width, lde, e), e);
+    if (targets != nullptr) {
+        a.in(targets, 8 * rows, 8);
+        a.out(logprobs, 4 * rows, 4);
+    }
+    if (entropy != nullptr) a.out(entropy, 4 * rows, 4);
+    if (stats != nullptr) a.out(stats, 8 * rows, 4);
+    a.out(workspace, need, 256);
+    if (int st = a.check(stream)) return st;
+    const dlk::HeadArgs k{x,       ldx,      embed,   lde,   rows,     vocab, width,
+                          targets, logprobs, entropy, stats, workspace};
+    return launched(dlk::head_logprobs(k, dtype, static_cast<hipStream_t>(stream)));
+}
+
+int dl_head_logprobs_backward(const void* x, int64_t ldx, const void* embed, int64_t lde,
+                              int dtype, int64_t rows, int64_t vocab, int64_t width,
+                              const int64_t* targets, const float* stats, const float* entropy,
+                              const float* dlogprobs, const float* dentropy, void* dx,
+                              int64_t lddx, void* dembed, int64_t ldde, void* workspace,
+                              int64_t workspace_bytes, void* stream) {
+    int64_t need = 0;
+    if (int st = dl_head_workspace_bytes(rows, vocab, width, dtype, 1, &need)) return st;
+    if ((entropy != nullptr) != (dentropy != nullptr)) return DL_E_INVAL;
+    if (dx == nullptr && dembed == nullptr) return DL_E_INVAL;
+    if (rows == 0 && dembed == nullptr) return DL_OK;
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return DL_E_INVAL;
+    const int64_t e = esize_of(dtype);
+    Arrays a;
+    if (rows > 0) {
+        a.in(x, matrix_bytes(rows, width, ldx, e), e);
+        a.in(embed, matrix_bytes(vocab, width, lde, e), e);
+        a.in(targets, 8 * rows, 8);
+        a.in(stats, 8 * rows, 4);
+        a.in(dlogprobs, 4 * rows, 4);
+        if (entropy != nullptr) {
+            a.in(entropy, 4 * rows, 4);
+            a.in(dentropy, 4 * rows, 4);
+        }
+        if (dx != nullptr) a.out(dx, matrix_bytes(rows, width, lddx, e), e);
+        a.out(workspace, need, 256);
+    }
+    if (dembed != nullptr) a.out(dembed, matrix_bytes(vocab, width, ldde, e), e);
+    if (int st = a.check(stream)) return st;
+    const dlk::HeadBackwardArgs k{x,       ldx,   embed,   lde,       rows,     vocab,
+                                  width,   targets, stats, entropy,   dlogprobs, dentropy,
+                                  dx,      lddx,  dembed,  ldde,      workspace};
+    return launched(dlk::head_logprobs_backward(k, dtype, static_cast<hipStream_t>(stream)));
+}
+
+int dl_e4m3_quantize(const void* x, int64_t ldx, int dtype, int64_t rows, int64_t cols,
+                     uint8_t* codes, int64_t ldc, uint8_t* scales, int scale_kind, void* values,
+                     int64_t ldvalues, void* stream) {
+    if (!float_type(dtype) || !dim(rows, 0) || !dim(cols, 1)) return DL_E_INVAL;
+    if (scale_kind != DL_SCALE_TILE128 && scale_kind != DL_SCALE_BLOCK128) return DL_E_INVAL;
+    if (rows == 0) return DL_OK;
+    const int64_t e = esize_of(dtype);
+    Arrays a;
+    const int ix = a.in(x, matrix_bytes(rows, cols, ldx, e), e, ldx);
+    a.out(codes, matrix_bytes(rows, cols, ldc, 1), 1);
+    a.out(scales, scale_bytes(scale_kind, rows, cols), 1);
+    if (values != nullptr)
+        a.may_be(a.out(values, matrix_bytes(rows, cols, ldvalues, e), e, ldvalues), ix);
+    if (int st = a.check(stream)) return st;
+    return launched(dlk::e4m3_quantize(x, ldx, dtype, rows, cols, codes, ldc, scales, scale_kind,
+                                       values, ldvalues, static_cast<hipStream_t>(stream)));
+}
+
+int dl_e4m3_matmul(const uint8_t* w, int64_t ldw, const uint8_t* w_scales, int64_t rows,
+                   int64_t cols, const uint8_t* x, int64_t ldx, const uint8_t* x_scales,
+                   int64_t count, void* y, int64_t ldy, int y_dtype, void* stream) {
+    if (!float_type(y_dtype) || !dim(rows, 0) || !dim(cols, 1) || !dim(count, 0))
+        return DL_E_INVAL;
+    if (rows == 0 || count == 0) return DL_OK;
+    const int64_t ye = esize_of(y_dtype);
+    Arrays a;
+    a.in(w, matrix_bytes(rows, cols, ldw, 1), 1);
+    a.in(w_scales, scale_bytes(DL_SCALE_TILE128, rows, cols), 1);
+    a.in(x, matrix_bytes(count, cols, ldx, 1), 1);
+    a.in(x_scales, scale_bytes(DL_SCALE_BLOCK128, count, cols), 1);
+    a.out(y, matrix_bytes(count, rows, ldy, ye), ye);
+    if (int st = a.check(stream)) return st;
+    const dlk::E4m3ProductArgs k{w,   ldw,      w_scales, rows, cols, x,
+                                 ldx, x_scales, count,    y,    ldy};
+    return launched(dlk::e4m3_matmul(k, y_dtype, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

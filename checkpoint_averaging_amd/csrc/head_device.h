@@ -130,6 +130,40 @@ __device__ __forceinline__ void store8(T* row, int64_t c, int64_t n, const float
     }
 }
 
+// Eight e4m3 codes, nearest, ties to even.
+__device__ __forceinline__ uint2 e4m3_of(const float* v) {
+    int a = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+    a = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], a, true);
+    int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);
+    b = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], b, true);
+    return uint2{static_cast<uint32_t>(a), static_cast<uint32_t>(b)};
+}
+
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+
+// Eight codes from column c on of a row of n.
+__device__ __forceinline__ void store_codes(uint8_t* row, int64_t c, int64_t n, uint2 q) {
+    if (c + 8 <= n) {
+        *reinterpret_cast<u32x2_any*>(row + c) = u32x2_any{q.x, q.y};
+    } else if (c < n) {
+        const int left = static_cast<int>(n - c);
+        uint8_t* p = row + c;
+        uint32_t u = q.x;
+        if (left & 4) {
+            __builtin_memcpy(p, &u, 4);
+            p += 4;
+            u = q.y;
+        }
+        if (left & 2) {
+            const uint16_t h = static_cast<uint16_t>(u);
+            __builtin_memcpy(p, &h, 2);
+            p += 2;
+            u >>= 16;
+        }
+        if (left & 1) *p = static_cast<uint8_t>(u);
+    }
+}
+
 // Reductions over a wavefront; every lane gets the result.  Within rows of 16
 // lanes values move by DPP (no LDS), in a fixed pairing that gives every lane
 // of a row the same bits; the four rows' are read as scalars.

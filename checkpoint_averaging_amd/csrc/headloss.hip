@@ -1,0 +1,505 @@
+// Log probabilities of given tokens straight from the head's inputs, and their
+// gradients, without the logits.
+//
+//   l = x E^T ; m = max l ; S = sum exp(l - m)
+//   log p_t = (l_t - m) - log S ;  H = log S - sum exp(l - m)(l - m) / S
+//   d = a (delta_t - p) - b p (log p + H) ;  dx = d E ;  dE = d^T x
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "dlhead.h"
+#include "head.h"
+#include "head_device.h"
+#include "tiles.h"
+
+#pragma clang fp contract(off)
+
+namespace dlk {
+
+namespace {
+
+constexpr float kLog2e = 0x1.715476p+0f;
+
+__device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
+
+// What a wave leaves of its span of the vocabulary for one token: the largest
+// logit m, the sum of exp(l - m) without one largest element's own 1, and the
+// sum of exp(l - m)(l - m).
+struct Part {
+    float m, rest, dot;
+};
+
+// ---- forward -----------------------------------------------------------------
+
+__device__ __forceinline__ float across_groups(float v, bool largest) {
+    for (int k = 16; k < kWave; k *= 2) {
+        const float o = __shfl_xor(v, k);
+        v = largest ? fmaxf(v, o) : v + o;
+    }
+    return v;
+}
+
+struct StatsTile : NoSteps {
+    Part* parts;                          // one row of `rows` for each wave's span
+    int64_t rows;
+    const int64_t* targets;               // or nullptr
+    float* at_target;                     // the targets' logits
+
+    template <int MT, int NT>
+    __device__ __forceinline__ void finish(const f32x4 (&acc)[MT][NT], const Place& at) const {
+        const int lane = threadIdx.x % kWave;
+        const int64_t left = at.m - at.m0;                 // of the vocabulary from here on
+        if (left <= 0) return;
+        const bool whole = left >= MT * 16;
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+            const int64_t n = at.n0 + u * 16 + lane % 16;
+            float v[MT * 4];
+            for (int p = 0; p < MT / 2; ++p) eight(acc, p, u, v + 8 * p);
+            // element q of v is token m0 + 32 (q/8) + 8 (lane/16) + q%8
+            const int first = lane / 16 * 8;
+            if (!whole)
+                for (int q = 0; q < MT * 4; ++q)
+                    if (32 * (q / 8) + first + q % 8 >= left) v[q] = -__builtin_inff();
+            if (targets != nullptr) {
+                const int64_t t = n < at.n ? targets[n] - at.m0 : -1;
+                const bool mine = t >= 0 && t < MT * 16 && t < left && (t / 8) % 4 == lane / 16;
+                if (__any(mine)) {
+                    float l = 0;
+                    for (int q = 0; q < MT * 4; ++q)
+                        if (32 * (q / 8) + first + q % 8 == t) l = v[q];
+                    if (mine) at_target[n] = l;
+                }
+            }
+            float m = v[0];
+            for (int q = 1; q < MT * 4; ++q) m = fmaxf(m, v[q]);
+            m = across_groups(m, true);
+            const float from = m == -__builtin_inff() ? 0.0f : m;
+            float s = 0, dot = 0;
+            for (int q = 0; q < MT * 4; ++q) {
+                const float d = v[q] - from, x = exp_of(d);
+                s += x;
+                dot += x > 0 ? x * d : (x != x ? x : 0.0f);
+            }
+            s = across_groups(s, false);
+            dot = across_groups(dot, false);
+            float rest = s - 1;
+            // a nearly certain token: the others' sum by itself, with all its digits
+            if (__any(s < 1.5f)) {
+                float r = 0, same = 0;
+                for (int q = 0; q < MT * 4; ++q) {
+                    const bool top = v[q] == m;
+                    same += top ? 1.0f : 0.0f;
+                    r += top ? 0.0f : exp_of(v[q] - from);
+                }
+                r = across_groups(r, false);
+                same = across_groups(same, false);
+                if (s < 1.5f) rest = r + (same - 1);
+            }
+            if (lane < 16 && n < at.n)
+                parts[at.m0 / (MT * 16) * rows + n] = Part{m, rest, dot};
+        }
+    }
+};
+
+// The row's results from its spans' parts: 16 rows a workgroup, 64 threads each.
+constexpr int kJoinRows = 16, kJoinParts = 64;
+
+__global__ __launch_bounds__(kJoinRows * kJoinParts) void k_join(
+    const Part* parts, int n_parts, int64_t rows, int64_t vocab, const int64_t* targets,
+    const float* at_target, float* logprobs, float* entropy, float* stats) {
+    __shared__ float lds[3][kJoinParts][kJoinRows];
+    const int r = threadIdx.x % kJoinRows, g = threadIdx.x / kJoinRows;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kJoinRows + r;
+    const int64_t safe = row < rows ? row : rows - 1;
+    float m = -__builtin_inff();
+    int top = n_parts;                                     // the first part with the largest
+    for (int p = g; p < n_parts; p += kJoinParts) {
+        const float v = parts[p * rows + safe].m;
+        if (v > m) {
+            m = v;
+            top = p;
+        }
+    }
+    lds[0][g][r] = m;
+    lds[1][g][r] = __int_as_float(top);
+    __syncthreads();
+    for (int h = kJoinParts / 2; h > 0; h /= 2) {
+        if (g < h) {
+            const float o = lds[0][g + h][r];
+            const int ot = __float_as_int(lds[1][g + h][r]), mt = __float_as_int(lds[1][g][r]);
+            if (o > lds[0][g][r] || (o == lds[0][g][r] && ot < mt)) {
+                lds[0][g][r] = o;
+                lds[1][g][r] = __int_as_float(ot);
+            }
+        }
+        __syncthreads();
+    }
+    m = lds[0][0][r];
+    top = __float_as_int(lds[1][0][r]);
+    __syncthreads();
+    const bool nothing = m == -__builtin_inff();
+    const float from = nothing ? 0.0f : m;
+    float rest = 0, dot = 0;
+    for (int p = g; p < n_parts; p += kJoinParts) {
+        const Part q = parts[p * rows + safe];
+        if (q.m == -__builtin_inff() && q.rest == q.rest) continue;      // all of it masked
+        const float d = q.m - from, w = exp_of(d);
+        rest += w * (p == top ? q.rest : 1 + q.rest);
+        if (w > 0 || w != w) dot += w * (q.dot + d * (1 + q.rest));
+    }
+    lds[0][g][r] = rest;
+    lds[1][g][r] = dot;
+    __syncthreads();
+    for (int h = kJoinParts / 2; h > 0; h /= 2) {
+        if (g < h) {
+            lds[0][g][r] += lds[0][g + h][r];
+            lds[1][g][r] += lds[1][g + h][r];
+        }
+        __syncthreads();
+    }
+    if (g != 0 || row >= rows) return;
+    rest = lds[0][0][r];
+    dot = lds[1][0][r];
+    const float log_s = nothing && rest == rest ? 0.0f : log1pf(rest);
+    if (stats != nullptr) {
+        stats[2 * row] = m;
+        stats[2 * row + 1] = log_s;
+    }
+    if (entropy != nullptr)
+        entropy[row] = nothing && rest == rest ? 0.0f : log_s - dot / (1 + rest);
+    if (logprobs != nullptr) {
+        const int64_t t = targets[row];
+        float lp = 0.0f;
+        if (t >= vocab) lp = __uint_as_float(0x7FC00000u);
+        else if (t >= 0) lp = nothing && rest == rest ? m : (at_target[row] - m) - log_s;
+        logprobs[row] = lp;
+    }
+}
+
+// ---- backward ----------------------------------------------------------------
+
+// What the gradient in a row's logits needs beside them.
+struct __attribute__((aligned(16))) RowTerms {
+    float m, log_s, a, b, entropy;
+    int32_t target;                       // or -1
+    int32_t pad[2];
+};
+
+// The rows that have a part in the gradients, in order: those with a target, or all
+// if there is a gradient of the entropies.  One workgroup.
+constexpr int kSelectThreads = 1024;
+
+__global__ __launch_bounds__(kSelectThreads) void k_select(const int64_t* targets, bool all,
+                                                           int64_t rows, int* index, int* where,
+                                                           int* count) {
+    __shared__ int waves[2][kSelectThreads / kWave];
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    int before = 0;
+    for (int64_t r0 = 0, turn = 0; r0 < rows; r0 += kSelectThreads, ++turn) {
+        const int64_t row = r0 + threadIdx.x;
+        const bool in = row < rows && (all || targets[row] >= 0);
+        const uint64_t votes = __ballot(in);
+        if (lane == 0) waves[turn % 2][wave] = __popcll(votes);
+        __syncthreads();
+        int at = before;
+        for (int w = 0; w < kSelectThreads / kWave; ++w) {
+            const int c = waves[turn % 2][w];
+            if (w < wave) at += c;
+            before += c;
+        }
+        at += __popcll(votes & ((uint64_t(1) << lane) - 1));
+        if (in) index[at] = static_cast<int>(row);
+        if (row < rows) where[row] = in ? at : -1;
+    }
+    if (threadIdx.x == 0) *count = before;
+}
+
+struct GatherArgs {
+    const void* x;
+    int64_t ldx, rows, vocab;
+    int width;
+    const int64_t* targets;
+    const float* stats;
+    const float* entropy;                 // or nullptr
+    const float* dlogprobs;
+    const float* dentropy;                // or nullptr
+    const int* index;
+    const int* count;
+    void* to;
+    int64_t ldto;
+    RowTerms* terms;
+};
+
+template <typename T> __global__ __launch_bounds__(256) void k_gather(GatherArgs a) {
+    const int n = *a.count;
+    for (int64_t j = blockIdx.x; j < n; j += gridDim.x) {
+        const int64_t row = a.index[j];
+        const T* from = static_cast<const T*>(a.x) + row * a.ldx;
+        T* to = static_cast<T*>(a.to) + j * a.ldto;
+        for (int c = threadIdx.x * 8; c < a.width; c += 256 * 8) {
+            float v[8];
+            load8(from, c, a.width, v);
+            store8(to, c, a.width, v);
+        }
+        if (threadIdx.x == 0) {
+            const int64_t t = a.targets[row];
+            RowTerms r{};
+            r.m = a.stats[2 * row];
+            r.log_s = a.stats[2 * row + 1];
+            r.a = t < 0 ? 0.0f : t >= a.vocab ? __uint_as_float(0x7FC00000u) : a.dlogprobs[row];
+            r.b = a.dentropy != nullptr ? a.dentropy[row] : 0.0f;
+            r.entropy = a.dentropy != nullptr ? a.entropy[row] : 0.0f;
+            r.target = t < 0 || t >= a.vocab ? -1 : static_cast<int32_t>(t);
+            a.terms[j] = r;
+        }
+    }
+}
+
+// The gradient in the logits of a piece of the vocabulary.
+template <typename T, bool ENTROPY> struct GradTile : NoSteps {
+    const RowTerms* terms;
+    T* out;
+    int64_t ld;
+    int64_t first;                        // token that the piece begins with
+
+    template <int MT, int NT>
+    __device__ __forceinline__ void finish(const f32x4 (&acc)[MT][NT], const Place& at) const {
+        const int lane = threadIdx.x % kWave;
+        if (at.m - at.m0 <= 0) return;
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+            const int64_t n = at.n0 + u * 16 + lane % 16;
+            if (n >= at.n) continue;
+            const RowTerms r = terms[n];
+            const int64_t t = r.target < 0 ? -1 : r.target - first - at.m0 - lane / 16 * 8;
+            const bool hot = t >= 0 && t < MT * 16 && t % 32 < 8;
+            // (a row of masked tokens only: their log probabilities are the logits)
+            const float from = r.m == -__builtin_inff() ? 0.0f : r.m;
+            for (int p = 0; p < MT / 2; ++p) {
+                float v[8];
+                eight(acc, p, u, v);
+                for (int q = 0; q < 8; ++q) {
+                    const float lp = (v[q] - from) - r.log_s;
+                    const float x = exp_of(lp);
+                    float d = -r.a * x;
+                    const float h = ENTROPY ? (x > 0 ? r.b * x * (lp + r.entropy) : 0.0f) : 0.0f;
+                    if (hot && t == 32 * p + q) d = -r.a * expm1f(lp);
+                    v[q] = x != x ? x : d - h;
+                }
+                store8(out + n * ld, at.m0 + p * 32 + lane / 16 * 8, at.m, v);
+            }
+        }
+    }
+};
+
+// Sums of dx in binary32, a matrix of rows x width for each slice of the vocabulary,
+// added up over its pieces.
+struct SumTile : NoSteps {
+    float* sums;
+    int64_t rows, ld;
+    bool first;
+
+    template <int MT, int NT>
+    __device__ __forceinline__ void finish(const f32x4 (&acc)[MT][NT], const Place& at) const {
+        const int lane = threadIdx.x % kWave;
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+            const int64_t n = at.n0 + u * 16 + lane % 16;
+            if (n >= at.n) continue;
+            float* row = sums + (at.slice * rows + n) * ld;
+            for (int p = 0; p < MT / 2; ++p) {
+                const int64_t c = at.m0 + p * 32 + lane / 16 * 8;
+                float v[8];
+                eight(acc, p, u, v);
+                if (!first) {
+                    float w[8];
+                    load8(row, c, at.m, w);
+                    for (int i = 0; i < 8; ++i) v[i] += w[i];
+                }
+                store8(row, c, at.m, v);
+            }
+        }
+    }
+};
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_dx(const float* sums, int slices, int64_t rows,
+                                            int64_t lds, int width, const int* where, T* dx,
+                                            int64_t lddx) {
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+        const int at = where[row];
+        for (int c = threadIdx.x * 8; c < width; c += 256 * 8) {
+            float v[8] = {};
+            if (at >= 0) {
+                load8(sums + at * lds, c, width, v);
+                for (int s = 1; s < slices; ++s) {
+                    float w[8];
+                    load8(sums + (s * rows + at) * lds, c, width, w);
+                    for (int i = 0; i < 8; ++i) v[i] += w[i];
+                }
+            }
+            store8(dx + row * lddx, c, width, v);
+        }
+    }
+}
+
+// ---- plans -------------------------------------------------------------------
+
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// Rows of the vocabulary that a wave leaves one part of.
+constexpr int kSpan = 128, kSpanSplit = 64;
+
+template <typename T> constexpr int span_of() { return sizeof(T) == 2 ? kSpan : kSpanSplit; }
+
+struct Backward {
+    int64_t piece, pieces;                // of the vocabulary; the last takes the rest
+    int64_t ld_p, ld_x, ld_s;
+    int slices;
+    int64_t index, where, count, terms, x, p, sums, bytes;      // places in the workspace
+};
+
+constexpr int64_t kPieceBytes = int64_t(128) << 20;
+
+Backward backward_plan(int64_t rows, int64_t vocab, int64_t width, int64_t esize) {
+    Backward b{};
+    int64_t most = kPieceBytes / (rows * esize) / 256 * 256;
+    most = most < 2048 ? 2048 : most;
+    b.pieces = (vocab + most - 1) / most;
+    b.piece = b.pieces == 1 ? vocab : vocab / b.pieces / 256 * 256;
+    if (b.piece == 0) {
+        b.piece = vocab;
+        b.pieces = 1;
+    }
+    const int64_t widest = vocab - (b.pieces - 1) * b.piece;
+    b.ld_p = up(widest, 8);
+    b.ld_x = up(width, 8);
+    b.ld_s = up(width, 4);
+    const int64_t tiles = up(width, 256) / 256 * (up(rows, 256) / 256);
+    b.slices = static_cast<int>(tiles >= 256 ? 1 : 256 / tiles > 16 ? 16 : 256 / tiles);
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += up(bytes, 256);
+        return here;
+    };
+    b.index = take(4 * rows);
+    b.where = take(4 * rows);
+    b.count = take(4);
+    b.terms = take(static_cast<int64_t>(sizeof(RowTerms)) * rows);
+    b.x = take(rows * b.ld_x * esize);
+    b.p = take(rows * b.ld_p * esize);
+    b.sums = take(b.slices * rows * b.ld_s * 4);
+    b.bytes = at;
+    return b;
+}
+
+template <class Via, bool SA, bool SB, int TM, int TN, int WM, int WN, class E>
+hipError_t product(const ProductArgs& a, const E& e, hipStream_t s) {
+    const dim3 grid(product_grid(a.m, a.n, TM, TN, a.slices, kTileGroups)), block(kTileThreads);
+    k_product<Via, SA, SB, TM, TN, WM, WN, E><<<grid, block, 0, s>>>(a, e);
+    return hipGetLastError();
+}
+
+// bf16: 256 x 256 tiles; binary32, whose three planes fill the LDS: 256 x 128.
+template <typename T, bool SA, bool SB, class E>
+hipError_t product_of(const ProductArgs& a, const E& e, hipStream_t s) {
+    if constexpr (sizeof(T) == 2) return product<ViaBf16, SA, SB, 256, 256, 2, 4>(a, e, s);
+    else return product<ViaSplit, SA, SB, 256, 128, 4, 2>(a, e, s);
+}
+
+template <typename T> hipError_t forward(const HeadArgs& a, hipStream_t s) {
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    const int parts = static_cast<int>((a.vocab + span_of<T>() - 1) / span_of<T>());
+    StatsTile e{};
+    e.at_target = reinterpret_cast<float*>(ws);
+    e.parts = reinterpret_cast<Part*>(ws + up(4 * a.rows, 256));
+    e.rows = a.rows;
+    e.targets = a.targets;
+    const ProductArgs p{a.embed, a.lde, a.x, a.ldx, a.vocab, a.rows, a.width, 1, nullptr, false};
+    const hipError_t st = product_of<T, false, false>(p, e, s);
+    if (st != hipSuccess) return st;
+    k_join<<<dim3(static_cast<unsigned>((a.rows + kJoinRows - 1) / kJoinRows)),
+             dim3(kJoinRows * kJoinParts), 0, s>>>(e.parts, parts, a.rows, a.vocab, a.targets,
+                                                   e.at_target, a.logprobs, a.entropy, a.stats);
+    return hipGetLastError();
+}
+
+template <typename T> hipError_t backward(const HeadBackwardArgs& a, hipStream_t s) {
+    if (a.rows == 0) {
+        const ProductArgs none{nullptr, 0, nullptr, 0, a.width, a.vocab, 0, 1, nullptr, false};
+        return product_of<T, true, true>(none, StoreTile<T>(a.dembed, a.ldde), s);
+    }
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    const Backward b = backward_plan(a.rows, a.vocab, a.width, sizeof(T));
+    int* index = reinterpret_cast<int*>(ws + b.index);
+    int* where = reinterpret_cast<int*>(ws + b.where);
+    int* count = reinterpret_cast<int*>(ws + b.count);
+    RowTerms* terms = reinterpret_cast<RowTerms*>(ws + b.terms);
+    T* x = reinterpret_cast<T*>(ws + b.x);
+    T* p = reinterpret_cast<T*>(ws + b.p);
+    float* sums = reinterpret_cast<float*>(ws + b.sums);
+    k_select<<<dim3(1), dim3(kSelectThreads), 0, s>>>(a.targets, a.dentropy != nullptr, a.rows,
+                                                      index, where, count);
+    hipError_t st = hipGetLastError();
+    if (st != hipSuccess) return st;
+    const unsigned walkers = static_cast<unsigned>(a.rows < 2048 ? a.rows : 2048);
+    const GatherArgs g{a.x,       a.ldx,      a.rows, a.vocab, static_cast<int>(a.width),
+                       a.targets, a.stats,    a.entropy, a.dlogprobs, a.dentropy,
+                       index,     count,      x,      b.ld_x,  terms};
+    k_gather<T><<<dim3(walkers), dim3(256), 0, s>>>(g);
+    if ((st = hipGetLastError()) != hipSuccess) return st;
+    for (int64_t i = 0; i < b.pieces; ++i) {
+        const int64_t v0 = i * b.piece;
+        const int64_t n = i + 1 < b.pieces ? b.piece : a.vocab - v0;
+        const T* embed = static_cast<const T*>(a.embed) + v0 * a.lde;
+        const ProductArgs lp{embed, a.lde, x, b.ld_x, n, a.rows, a.width, 1, count, false};
+        if (a.dentropy != nullptr) {
+            const GradTile<T, true> e{{}, terms, p, b.ld_p, v0};
+            st = product_of<T, false, false>(lp, e, s);
+        } else {
+            const GradTile<T, false> e{{}, terms, p, b.ld_p, v0};
+            st = product_of<T, false, false>(lp, e, s);
+        }
+        if (st != hipSuccess) return st;
+        if (a.dx != nullptr) {
+            const ProductArgs dp{embed, a.lde, p, b.ld_p, a.width, a.rows, n, b.slices, count,
+                                 false};
+            const SumTile e{{}, sums, a.rows, b.ld_s, i == 0};
+            if ((st = product_of<T, true, false>(dp, e, s)) != hipSuccess) return st;
+        }
+        if (a.dembed != nullptr) {
+            const ProductArgs ep{x, b.ld_x, p, b.ld_p, a.width, n, a.rows, 1, count, true};
+            const StoreTile<T> e(static_cast<T*>(a.dembed) + v0 * a.ldde, a.ldde);
+            if ((st = product_of<T, true, true>(ep, e, s)) != hipSuccess) return st;
+        }
+    }
+    if (a.dx == nullptr) return hipSuccess;
+    k_dx<T><<<dim3(walkers), dim3(256), 0, s>>>(sums, b.slices, a.rows, b.ld_s,
+                                                static_cast<int>(a.width), where,
+                                                static_cast<T*>(a.dx), a.lddx);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t head_workspace_bytes(int64_t rows, int64_t vocab, int64_t width, int dtype,
+                             bool with_backward) {
+    const int64_t span = dtype == DL_BF16 ? kSpan : kSpanSplit;
+    const int64_t fwd = up(4 * rows, 256) +
+                        up((vocab + span - 1) / span * rows * static_cast<int64_t>(sizeof(Part)), 256);
+    if (!with_backward) return fwd;
+    const int64_t bwd = backward_plan(rows, vocab, width, dtype == DL_BF16 ? 2 : 4).bytes;
+    return fwd > bwd ? fwd : bwd;
+}
+
+hipError_t head_logprobs(const HeadArgs& a, int dtype, hipStream_t s) {
+    return dtype == DL_BF16 ? forward<bf16>(a, s) : forward<float>(a, s);
+}
+
+hipError_t head_logprobs_backward(const HeadBackwardArgs& a, int dtype, hipStream_t s) {
+    return dtype == DL_BF16 ? backward<bf16>(a, s) : backward<float>(a, s);
+}
+
+}  // namespace dlk

@@ -62,39 +62,6 @@ __device__ __forceinline__ T row_reduce(T v, Op op, T* lds) {
     }
 }
 
-// Eight e4m3 codes.
-__device__ __forceinline__ uint2 e4m3_of(const float* v) {
-    int a = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
-    a = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], a, true);
-    int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);
-    b = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], b, true);
-    return uint2{static_cast<uint32_t>(a), static_cast<uint32_t>(b)};
-}
-
-typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
-
-__device__ __forceinline__ void store_codes(uint8_t* row, int c, int n, uint2 q) {
-    if (c + kCols <= n) {
-        *reinterpret_cast<u32x2_any*>(row + c) = u32x2_any{q.x, q.y};
-    } else if (c < n) {
-        const int left = n - c;
-        uint8_t* p = row + c;
-        uint32_t u = q.x;
-        if (left & 4) {
-            __builtin_memcpy(p, &u, 4);
-            p += 4;
-            u = q.y;
-        }
-        if (left & 2) {
-            const uint16_t h = static_cast<uint16_t>(u);
-            __builtin_memcpy(p, &h, 2);
-            p += 2;
-            u >>= 16;
-        }
-        if (left & 1) *p = static_cast<uint8_t>(u);
-    }
-}
-
 // OUT: element type of y; KIND: its scales.
 template <typename T, int OUT, int KIND, int LANES, int NV>
 __global__ __launch_bounds__(threads_of<LANES>(), 4) void k_rmsnorm(NormArgs a) {
@@ -156,21 +123,22 @@ __global__ __launch_bounds__(threads_of<LANES>(), 4) void k_rmsnorm(NormArgs a) 
                 store_codes(static_cast<uint8_t*>(a.y) + row * a.ldy, (i * LANES + lane) * kCols,
                             a.cols, e4m3_of(s[i]));
             }
-        } else if constexpr (KIND == DL_SCALE_BLOCK32) {
-            const int64_t kb = (a.cols + 31) / 32;
+        } else if constexpr (KIND == DL_SCALE_BLOCK32 || KIND == DL_SCALE_BLOCK128) {
+            constexpr int kBlock = KIND == DL_SCALE_BLOCK32 ? 32 : 128;
+            const int64_t kb = (a.cols + kBlock - 1) / kBlock;
             for (int i = 0; i < NV; ++i) {
                 const int c = (i * LANES + lane) * kCols;
                 uint32_t b = 0;
                 for (int k = 0; k < kCols; ++k) b = Max{}(b, abs_bits(s[i][k]));
-                b = lanes_reduce<4>(b, Max{});           // the 32 columns' four lanes
+                b = lanes_reduce<kBlock / kCols>(b, Max{});          // the block's lanes
                 // the smallest power of two p with amax <= 448 p = 1.75 * 2^8 p
                 int e = static_cast<int>((b + 0x1FFFFFu) >> 23) - 8;
                 e = e < 0 ? 0 : e;
                 const bool bad = b >= 0x7F800000u;
                 const float back = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
                 for (int k = 0; k < kCols; ++k) s[i][k] = bad ? 0.0f : s[i][k] * back;
-                if (lane % 4 == 0 && c < a.cols)
-                    static_cast<uint8_t*>(a.scales)[row * kb + c / 32] =
+                if (c % kBlock == 0 && c < a.cols)
+                    static_cast<uint8_t*>(a.scales)[row * kb + c / kBlock] =
                         static_cast<uint8_t>(bad ? 255 : e);
                 store_codes(static_cast<uint8_t*>(a.y) + row * a.ldy, c, a.cols, e4m3_of(s[i]));
             }
@@ -351,6 +319,7 @@ template <typename T>
 hipError_t forward_to(const NormArgs& a, int y_dtype, int kind, hipStream_t s) {
     if (kind == DL_SCALE_ROW) return forward<T, DL_E4M3, DL_SCALE_ROW>(a, s);
     if (kind == DL_SCALE_BLOCK32) return forward<T, DL_E4M3, DL_SCALE_BLOCK32>(a, s);
+    if (kind == DL_SCALE_BLOCK128) return forward<T, DL_E4M3, DL_SCALE_BLOCK128>(a, s);
     return y_dtype == DL_F32 ? forward<T, DL_F32, DL_SCALE_NONE>(a, s)
                              : forward<T, DL_BF16, DL_SCALE_NONE>(a, s);
 }

@@ -21,13 +21,17 @@ DL_E4M3 = 2
 DL_SCALE_NONE = 0
 DL_SCALE_ROW = 1
 DL_SCALE_BLOCK32 = 2
+DL_SCALE_TILE128 = 3
+DL_SCALE_BLOCK128 = 4
 DL_MAX_NORM_COLS = 32768
 DL_MAX_VECTORS = 32
 DL_MAX_TOP = 32
 
 SYMBOLS = ("dl_rmsnorm", "dl_rmsnorm_workspace_bytes", "dl_rmsnorm_backward",
            "dl_w4_bytes", "dl_w4_quantize", "dl_w4_matvec",
-           "dl_logprobs_workspace_bytes", "dl_logprobs", "dl_logprobs_backward")
+           "dl_logprobs_workspace_bytes", "dl_logprobs", "dl_logprobs_backward",
+           "dl_head_workspace_bytes", "dl_head_logprobs", "dl_head_logprobs_backward",
+           "dl_e4m3_quantize", "dl_e4m3_matmul")
 
 _lib = raw_lib()
 _p, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
@@ -44,6 +48,13 @@ _lib.dl_logprobs_workspace_bytes.argtypes = [_i64, _i64, _i32, ctypes.POINTER(_i
 _lib.dl_logprobs.argtypes = [_p, _i64, _i32, _i64, _i64, _p, _p, _p, _p, _i32, _p, _p, _p, _i64,
                              _p]
 _lib.dl_logprobs_backward.argtypes = [_p, _i64, _i32, _i64, _i64, _p, _p, _p, _p, _p, _p, _i64, _p]
+_lib.dl_head_workspace_bytes.argtypes = [_i64, _i64, _i64, _i32, _i32, ctypes.POINTER(_i64)]
+_lib.dl_head_logprobs.argtypes = [_p, _i64, _p, _i64, _i32, _i64, _i64, _i64, _p, _p, _p, _p, _p,
+                                  _i64, _p]
+_lib.dl_head_logprobs_backward.argtypes = [_p, _i64, _p, _i64, _i32, _i64, _i64, _i64, _p, _p, _p,
+                                           _p, _p, _p, _i64, _p, _i64, _p, _i64, _p]
+_lib.dl_e4m3_quantize.argtypes = [_p, _i64, _i32, _i64, _i64, _p, _i64, _p, _i32, _p, _i64, _p]
+_lib.dl_e4m3_matmul.argtypes = [_p, _i64, _p, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _i32, _p]
 for _name in SYMBOLS:
     getattr(_lib, _name).restype = _i32
 
@@ -125,6 +136,9 @@ def _vector(a: Array, n: int, dtype: torch.dtype, name: str) -> Optional[int]:
 def _scales(a: Array, kind: int, rows: int, cols: int, name: str) -> Optional[int]:
     if kind == DL_SCALE_ROW:
         return _vector(a, rows, torch.float32, name)
+    if kind in (DL_SCALE_TILE128, DL_SCALE_BLOCK128):
+        groups = rows if kind == DL_SCALE_BLOCK128 else (rows + 127) // 128
+        return _vector(a, groups * ((cols + 127) // 128), torch.uint8, name)
     return _vector(a, rows * ((cols + 31) // 32), torch.uint8, name)
 
 
@@ -271,3 +285,98 @@ def dl_logprobs_backward(logits: Array, rows: int, vocab: int, targets: Array, s
                                      _vector(dentropy, rows, f32, "dentropy"), da, lddl,
                                      _stream(stream)),
            "dl_logprobs_backward")
+
+
+def _dtype_code(dtype) -> int:
+    return _DTYPES[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+
+
+def dl_head_workspace_bytes(rows: int, vocab: int, width: int, dtype, backward: bool = False
+                            ) -> int:
+    """dtype: a torch type or DL_F32, DL_BF16."""
+    b = _i64()
+    _check(_lib.dl_head_workspace_bytes(int(rows), int(vocab), int(width), _dtype_code(dtype),
+                                        int(backward), ctypes.byref(b)),
+           "dl_head_workspace_bytes")
+    return b.value
+
+
+def dl_head_logprobs(x: Array, embed: Array, rows: int, vocab: int, width: int,
+                     targets: Array = None, logprobs: Array = None, entropy: Array = None,
+                     stats: Array = None, workspace: Array = None,
+                     workspace_bytes: Optional[int] = None, ldx: Optional[int] = None,
+                     lde: Optional[int] = None, dtype: Optional[int] = None,
+                     stream=None) -> None:
+    dtype = _dtype_of(x, dtype, "x")
+    _same_type(embed, dtype, "embed")
+    xa, ldx = _matrix(x, rows, width, ldx, "x")
+    ea, lde = _matrix(embed, vocab, width, lde, "embed")
+    w, wb = _workspace(workspace, workspace_bytes)
+    f32 = torch.float32
+    _check(_lib.dl_head_logprobs(xa, ldx, ea, lde, dtype, rows, vocab, width,
+                                 _vector(targets, rows, torch.int64, "targets"),
+                                 _vector(logprobs, rows, f32, "logprobs"),
+                                 _vector(entropy, rows, f32, "entropy"),
+                                 _vector(stats, 2 * rows, f32, "stats"), w, wb, _stream(stream)),
+           "dl_head_logprobs")
+
+
+def dl_head_logprobs_backward(x: Array, embed: Array, rows: int, vocab: int, width: int,
+                              targets: Array, stats: Array, dlogprobs: Array, dx: Array = None,
+                              dembed: Array = None, entropy: Array = None,
+                              dentropy: Array = None, workspace: Array = None,
+                              workspace_bytes: Optional[int] = None, ldx: Optional[int] = None,
+                              lde: Optional[int] = None, lddx: Optional[int] = None,
+                              ldde: Optional[int] = None, dtype: Optional[int] = None,
+                              stream=None) -> None:
+    dtype = _dtype_of(x, dtype, "x")
+    for a, name in ((embed, "embed"), (dx, "dx"), (dembed, "dembed")):
+        _same_type(a, dtype, name)
+    xa, ldx = _matrix(x, rows, width, ldx, "x")
+    ea, lde = _matrix(embed, vocab, width, lde, "embed")
+    dxa, lddx = _matrix(dx, rows, width, lddx, "dx")
+    dea, ldde = _matrix(dembed, vocab, width, ldde, "dembed")
+    w, wb = _workspace(workspace, workspace_bytes)
+    f32 = torch.float32
+    _check(_lib.dl_head_logprobs_backward(xa, ldx, ea, lde, dtype, rows, vocab, width,
+                                          _vector(targets, rows, torch.int64, "targets"),
+                                          _vector(stats, 2 * rows, f32, "stats"),
+                                          _vector(entropy, rows, f32, "entropy"),
+                                          _vector(dlogprobs, rows, f32, "dlogprobs"),
+                                          _vector(dentropy, rows, f32, "dentropy"), dxa, lddx,
+                                          dea, ldde, w, wb, _stream(stream)),
+           "dl_head_logprobs_backward")
+
+
+def dl_e4m3_quantize(x: Array, rows: int, cols: int, codes: Array, scales: Array,
+                     scale_kind: int, values: Array = None, ldx: Optional[int] = None,
+                     ldc: Optional[int] = None, ldvalues: Optional[int] = None,
+                     dtype: Optional[int] = None, stream=None) -> None:
+    dtype = _dtype_of(x, dtype, "x")
+    _same_type(codes, DL_E4M3, "codes")
+    _same_type(values, dtype, "values")
+    xa, ldx = _matrix(x, rows, cols, ldx, "x")
+    ca, ldc = _matrix(codes, rows, cols, ldc, "codes")
+    va, ldvalues = _matrix(values, rows, cols, ldvalues, "values")
+    _check(_lib.dl_e4m3_quantize(xa, ldx, dtype, rows, cols, ca, ldc,
+                                 _scales(scales, scale_kind, rows, cols, "scales"), scale_kind,
+                                 va, ldvalues, _stream(stream)),
+           "dl_e4m3_quantize")
+
+
+def dl_e4m3_matmul(w: Array, w_scales: Array, rows: int, cols: int, x: Array, x_scales: Array,
+                   count: int, y: Array, ldw: Optional[int] = None, ldx: Optional[int] = None,
+                   ldy: Optional[int] = None, y_dtype: Optional[int] = None,
+                   stream=None) -> None:
+    y_dtype = _dtype_of(y, y_dtype, "y")
+    _same_type(w, DL_E4M3, "w")
+    _same_type(x, DL_E4M3, "x")
+    wa, ldw = _matrix(w, rows, cols, ldw, "w")
+    xa, ldx = _matrix(x, count, cols, ldx, "x")
+    ya, ldy = _matrix(y, count, rows, ldy, "y")
+    _check(_lib.dl_e4m3_matmul(wa, ldw, _scales(w_scales, DL_SCALE_TILE128, rows, cols,
+                                                "w_scales"),
+                               rows, cols, xa, ldx,
+                               _scales(x_scales, DL_SCALE_BLOCK128, count, cols, "x_scales"),
+                               count, ya, ldy, y_dtype, _stream(stream)),
+           "dl_e4m3_matmul")

@@ -18,6 +18,12 @@
  *   dl_logprobs           log probabilities of given tokens, entropy, the most
  *                         likely alternatives
  *   dl_logprobs_backward  the gradient of both in the logits
+ *   dl_head_logprobs      log probabilities and entropy straight from the norm's
+ *                         output and the embedding, without the logits
+ *   dl_head_logprobs_backward  the gradients of both in these inputs
+ *   dl_e4m3_quantize      a matrix laid out in 8 bits with a scale for each 128
+ *                         x 128 elements, or each 128 of a row
+ *   dl_e4m3_matmul        the product of the two kinds, for one token or many
  *
  * Library, status codes and element types are those of dlmerge.h.
  *
@@ -56,16 +62,21 @@ extern "C" {
 #endif
 
 /* 8-bit floating point (one sign, four exponent, three mantissa bits, largest
- * value 448, no infinity): an output of dl_rmsnorm and input of dl_w4_matvec. */
+ * value 448, no infinity): an output of dl_rmsnorm and dl_e4m3_quantize, and an
+ * input of dl_w4_matvec and dl_e4m3_matmul. */
 enum { DL_E4M3 = 2 };
 
 /* Scales that go with a matrix held in DL_E4M3. */
 enum dl_scale {
     DL_SCALE_NONE = 0,     /* none (the other types)                            */
     DL_SCALE_ROW = 1,      /* one fp32 for each row                             */
-    DL_SCALE_BLOCK32 = 2   /* one byte e, standing for 2^(e-127), for each 32
+    DL_SCALE_BLOCK32 = 2,  /* one byte e, standing for 2^(e-127), for each 32
                               columns of a row: rows x ceil(cols/32) bytes,
                               row after row; 255 stands for NaN                 */
+    DL_SCALE_TILE128 = 3,  /* such a byte for each 128 rows of 128 columns:
+                              ceil(rows/128) x ceil(cols/128) bytes             */
+    DL_SCALE_BLOCK128 = 4  /* such a byte for each 128 columns of a row: rows x
+                              ceil(cols/128) bytes                              */
 };
 
 #define DL_MAX_NORM_COLS 32768
@@ -91,9 +102,9 @@ enum dl_scale {
  *                DL_SCALE_ROW      scale = amax/448 of the row's |y|, elements
  *                                  y * (448/amax); a row whose amax is below
  *                                  2^-100 is held as zeros with scale 0.
- *                DL_SCALE_BLOCK32  for each 32 columns the smallest power of
- *                                  two b >= 2^-127 with amax <= 448 b,
- *                                  elements y / b.
+ *                DL_SCALE_BLOCK32, DL_SCALE_BLOCK128  for each 32 or 128 columns
+ *                                  the smallest power of two b >= 2^-127 with
+ *                                  amax <= 448 b, elements y / b.
  *                Elements are rounded to nearest, ties to even; none is
  *                clipped.  A row (block) that holds a NaN or infinity has a
  *                NaN scale and zeros: all of it stands for NaN.
@@ -220,6 +231,91 @@ int dl_logprobs_backward(const void *logits, int64_t ldl, int dtype, int64_t row
                          const int64_t *targets, const float *stats, const float *entropy,
                          const float *dlogprobs, const float *dentropy, void *dlogits,
                          int64_t lddl, void *stream);
+
+/*
+ * dl_logprobs for the logits l[i][v] = sum over k < width of x[i][k] *
+ * embed[v][k], i < rows, v < vocab, which are formed piece by piece and not
+ * kept: a probe's log probabilities under a candidate, a training step's loss.
+ *
+ *   x             rows x width of dtype (DL_F32 or DL_BF16), e.g. dl_rmsnorm's y.
+ *   embed         vocab x width of dtype.
+ *   targets, logprobs, entropy, stats   as for dl_logprobs.
+ *
+ * Products are exact and summed in binary32 (DL_F32: a product is off by at
+ * most 2^-25 of itself; parts of an element below 2^-126 may count as 0, and
+ * 2^128 - 2^119 or more as infinite).  A row of x that holds an infinity or NaN
+ * may have results of NaN, and so may all rows if embed holds one.
+ *
+ * workspace: dl_head_workspace_bytes bytes; `backward` nonzero asks for what the
+ * gradients need too (never less than without).  rows = 0 is a no-op.
+ * 1 <= vocab <= 2^31 - 1, 1 <= width <= DL_MAX_NORM_COLS, and rows x (vocab
+ * + width) at most 2^50.
+ */
+int dl_head_workspace_bytes(int64_t rows, int64_t vocab, int64_t width, int dtype, int backward,
+                            int64_t *bytes);
+int dl_head_logprobs(const void *x, int64_t ldx, const void *embed, int64_t lde, int dtype,
+                     int64_t rows, int64_t vocab, int64_t width, const int64_t *targets,
+                     float *logprobs, float *entropy, float *stats, void *workspace,
+                     int64_t workspace_bytes, void *stream);
+
+/*
+ * The gradients of dl_head_logprobs' logprobs and entropy: with dlogits as
+ * dl_logprobs_backward gives it,
+ *     dx = dlogits x embed ;  dembed = dlogits^T x x
+ * stats and entropy are the forward call's (entropy is needed with dentropy,
+ * else NULL).  dx: rows x width, dembed: vocab x width of dtype, each written (not
+ * added to); either may be NULL.  The logits are formed again piece by piece;
+ * dlogits is rounded to dtype, and its products summed in binary32.
+ *
+ * Without dentropy, a row without a target has no part: its dx is 0 and it adds
+ * nothing to dembed, whatever its x, stats and dlogprobs hold.  A row with target
+ * >= vocab has NaN for its dx and makes dembed NaN.  rows = 0 writes zeros to
+ * dembed.
+ */
+int dl_head_logprobs_backward(const void *x, int64_t ldx, const void *embed, int64_t lde,
+                              int dtype, int64_t rows, int64_t vocab, int64_t width,
+                              const int64_t *targets, const float *stats, const float *entropy,
+                              const float *dlogprobs, const float *dentropy, void *dx,
+                              int64_t lddx, void *dembed, int64_t ldde, void *workspace,
+                              int64_t workspace_bytes, void *stream);
+
+/*
+ * x (rows x cols, DL_F32 or DL_BF16) in 8 bits: codes, rows x cols in DL_E4M3
+ * with rows ldc bytes apart, and scales of scale_kind: DL_SCALE_TILE128 (weights,
+ * e.g. a matrix of a merged global) or DL_SCALE_BLOCK128 (activations).  A block's
+ * scale b is the smallest power of two >= 2^-127 with amax <= 448 b; elements
+ * x / b are rounded to nearest, ties to even, and none is clipped.  A block that
+ * holds a NaN or infinity has scale 255 and code 0: all of it stands for NaN.
+ * values, if not NULL, receives what the codes stand for (rows x cols of
+ * dtype: exact, infinite where they round up past its range), e.g. to score the
+ * published matrix; it may be x itself.
+ * 1 <= cols, rows <= 2^31 - 1; rows = 0 is a no-op.
+ */
+int dl_e4m3_quantize(const void *x, int64_t ldx, int dtype, int64_t rows, int64_t cols,
+                     uint8_t *codes, int64_t ldc, uint8_t *scales, int scale_kind, void *values,
+                     int64_t ldvalues, void *stream);
+
+/*
+ * y[i][r] = sum over k < cols of x[i][k] * W[r][k] for r < rows and i < count:
+ * a matrix in 8 bits with DL_SCALE_TILE128 times tokens' vectors in 8 bits with
+ * DL_SCALE_BLOCK128.
+ *
+ *   w         rows x cols codes, rows ldw bytes apart;  w_scales its scales.
+ *   x         count x cols codes, rows ldx bytes apart;  x_scales its scales.
+ *   y         count x rows of y_dtype.  DL_F32: products are exact and summed in
+ *             binary32 (block scales are applied in bf16, exact for values of at
+ *             least 2^-133; products and partial sums below 2^-126 may count as 0).
+ *             DL_BF16: the matrix cores' own 8-bit products, which drop low bits
+ *             of small addends beside large ones (at most 2^-13 of the sum of
+ *             magnitudes of 128 products, some 2e-5 of a typical result), then
+ *             bf16's rounding.
+ *
+ * Any code and scale byte is accepted.  rows = 0 and count = 0 are no-ops;
+ * 1 <= cols, all at most 2^31 - 1.
+ */
+int dl_e4m3_matmul(const uint8_t *w, int64_t ldw, const uint8_t *w_scales, int64_t rows,
+                   int64_t cols, const uint8_t *x, int64_t ldx, const uint8_t *x_scales,
+                   int64_t count, void *y, int64_t ldy, int y_dtype, void *stream);
 
 #ifdef __cplusplus
 }

@@ -197,3 +197,35 @@ def logprobs_backward(lp, h, targets, dlogprobs, dentropy):
             plp = np.where(p > 0, p * (lp + h[:, None]), np.where(np.isnan(p), np.nan, 0.0))
             d -= dentropy.astype(F64)[:, None] * plp
     return d
+
+
+def tile_bytes(x, high):
+    """Exponent byte of each `high` rows of 128 columns: the smallest power of two
+    b >= 2^-127 with amax <= 448 b; 255 where the block holds a NaN or infinity."""
+    rows, cols = x.shape
+    p = np.zeros((-(-rows // high) * high, -(-cols // 128) * 128), F64)
+    p[:rows, :cols] = np.abs(x.astype(F64))
+    p = p.reshape(-1, high, p.shape[1] // 128, 128)
+    ok = np.isfinite(p).all(axis=(1, 3))
+    amax = np.where(ok, np.where(np.isfinite(p), p, 0).max(axis=(1, 3)), 0.0)
+    _, e = np.frexp(amax / 448.0)                # amax/448 <= 2^e, and > 2^(e-1)
+    e = np.where(amax == 448.0 * 2.0 ** (e - 1.0), e - 1, e)
+    e = np.where(amax == 0, 0, np.maximum(e + 127, 0))
+    return np.where(ok, e, 255).astype(np.uint8)
+
+
+def tile_spread(scales, shape, high):
+    """Each element's scale."""
+    b = scale_value(scales)
+    return np.repeat(np.repeat(b, high, axis=0), 128, axis=1)[:shape[0], :shape[1]]
+
+
+def e4m3_quantize(x, high):
+    """(codes, exponent bytes, values) of binary32 x with a scale for each
+    `high` rows of 128 columns."""
+    e = tile_bytes(x, high)
+    b = tile_spread(e, x.shape, high)
+    with np.errstate(invalid="ignore"):
+        q = np.where(np.isnan(b), 0.0, x.astype(F64) / b)
+    codes = np.where(np.isnan(b), 0, e4m3_code(q)).astype(np.uint8)
+    return codes, e, e4m3_value(codes) * b
