@@ -119,125 +119,138 @@ template <typename T> __global__ __launch_bounds__(kThreads) void k_e4m3_tiles(Q
 // (1.7e-3), too much for a binary32 result.  That one takes codes as bf16 numbers, which
 // they are exactly with their scales, at half the rate.
 
-template <bool EXACT, typename Y> struct ProductTile {
-    StoreTile<Y> store;
+template <typename Y> struct ProductTile : StoreTile<Y> {
     const uint8_t* w_scales;
     const uint8_t* x_scales;
     int64_t kb;
+};
 
-    template <int NT> struct Steps {
-        const uint8_t* ws;
-        const uint8_t* xs[NT];
-        uint32_t w, x[NT];
-        int64_t at, end;
-        __device__ __forceinline__ void read() {
-            if (at >= end) return;
-            w = ws[at];
-#pragma unroll
-            for (int u = 0; u < NT; ++u) x[u] = xs[u][at];
-            ++at;
-        }
-        __device__ __forceinline__ void enter(const ProductTile& e, const Place& p, int64_t) {
-            const int64_t m = p.m0 < p.m ? p.m0 : p.m - 1;
-            ws = e.w_scales + m / kBlock * e.kb;
-#pragma unroll
-            for (int u = 0; u < NT; ++u) {
-                const int64_t n = p.n0 + u * 16 + threadIdx.x % 16;
-                xs[u] = e.x_scales + (n < p.n ? n : p.n - 1) * e.kb;
-            }
-            at = 0;
-            end = e.kb;
-            read();
-        }
+// The scales of a wave's rows of W (in one block of 128) and of its lanes' tokens, read one
+// step ahead.
+template <class Epilogue, int NT> struct Scales {
+    const uint8_t* ws;
+    const uint8_t* xs[NT];
+    uint32_t w, x[NT], w_next, x_next[NT];
+    int64_t at, end;
 
-        template <class SideA, class SideB, int MT, class Middle>
-        __device__ __forceinline__ void product(const uint8_t* la, const uint8_t* lb, int wm, int wn,
-                                                f32x4 (&acc)[MT][NT], Middle middle) {
-            const uint32_t ew = w;
-            uint32_t ex[NT];
-#pragma unroll
-            for (int u = 0; u < NT; ++u) ex[u] = x[u];
-            read();                       // the next step's
-            if constexpr (EXACT) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (h == 1) middle();
-                    bf16x8 vb[NT][2];
-#pragma unroll
-                    for (int u = 0; u < NT; ++u) decode(SideB::codes(lb, wn, u, h), ex[u], vb[u]);
-#pragma unroll
-                    for (int t = 0; t < MT; ++t) {
-                        bf16x8 va[2];
-                        decode(SideA::codes(la, wm, t, h), ew, va);
-#pragma unroll
-                        for (int q = 0; q < 2; ++q)
-                            for (int u = 0; u < NT; ++u)
-                                acc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                    va[q], vb[u][q], acc[t][u], 0, 0, 0);
-                    }
-                }
-            } else {
-                auto whole = [](u32x4 a, u32x4 b) {
-                    return i32x8{static_cast<int>(a[0]), static_cast<int>(a[1]),
-                                 static_cast<int>(a[2]), static_cast<int>(a[3]),
-                                 static_cast<int>(b[0]), static_cast<int>(b[1]),
-                                 static_cast<int>(b[2]), static_cast<int>(b[3])};
-                };
-                i32x8 vb[NT];
-#pragma unroll
-                for (int u = 0; u < NT; ++u)
-                    vb[u] = whole(SideB::codes(lb, wn, u, 0), SideB::codes(lb, wn, u, 1));
-#pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    if (t == MT / 2) middle();
-                    const i32x8 va = whole(SideA::codes(la, wm, t, 0), SideA::codes(la, wm, t, 1));
-#pragma unroll
-                    for (int u = 0; u < NT; ++u)
-                        acc[t][u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            va, vb[u], acc[t][u], 0, 0, 0, static_cast<int>(ew), 0,
-                            static_cast<int>(ex[u]));
-                }
-            }
+    __device__ __forceinline__ void read() {
+        const int64_t i = at < end ? at : end - 1;
+        w_next = ws[i];
+        for (int u = 0; u < NT; ++u) x_next[u] = xs[u][i];
+        ++at;
+    }
+    __device__ __forceinline__ void enter(const Epilogue& e, const Place& p) {
+        const int64_t m = p.m0 < p.m ? p.m0 : p.m - 1;
+        ws = e.w_scales + m / kBlock * e.kb;
+        for (int u = 0; u < NT; ++u) {
+            const int64_t n = p.n0 + u * kSquare + threadIdx.x % kSquare;
+            xs[u] = e.x_scales + (n < p.n ? n : p.n - 1) * e.kb;
         }
-
-        // 16 codes as 2 x 8 bf16 values, the scale applied.
-        static __device__ __forceinline__ void decode(u32x4 c, uint32_t byte, bf16x8* out) {
-            const float b = __uint_as_float(byte << 23);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const u32x4 v = {
-                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(
-                                                     c[2 * i], b, false)),
-                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(
-                                                     c[2 * i], b, true)),
-                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(
-                                                     c[2 * i + 1], b, false)),
-                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(
-                                                     c[2 * i + 1], b, true))};
-                out[i] = __builtin_bit_cast(bf16x8, v);
-            }
-        }
-    };
-
-    template <int MT, int NT>
-    __device__ __forceinline__ void finish(const f32x4 (&acc)[MT][NT], const Place& at) const {
-        store.finish(acc, at);
+        at = 0;
+        end = e.kb;
+        read();
+    }
+    __device__ __forceinline__ void step() {
+        w = w_next;
+        for (int u = 0; u < NT; ++u) x[u] = x_next[u];
+        read();
     }
 };
 
-template <bool EXACT, typename Y> hipError_t matmul_of(const E4m3ProductArgs& a, hipStream_t s) {
+// The matrix cores' 8-bit products: 64 codes of a row at once, 32 of them in each half of the
+// lanes.
+template <class Epilogue, int MT, int NT, int SUBS> struct CodeMath : Scales<Epilogue, NT> {
+    static constexpr int kSubs = SUBS / 2, kAhead = 1, kSlots = 2;
+    struct A {
+        u32x4 h[2];
+    };
+    struct B {
+        A v[NT];
+    };
+    __device__ __forceinline__ void take(const B&) {}
+    template <class S> __device__ __forceinline__ A read_a(const uint8_t* l, int w, int t, int sub) {
+        const int c = 4 * sub + threadIdx.x % kWave / 32 * 2;
+        return A{{S::codes(l, w, t, c), S::codes(l, w, t, c + 1)}};
+    }
+    template <class S> __device__ __forceinline__ B read_b(const uint8_t* l, int w, int sub) {
+        B b;
+        for (int u = 0; u < NT; ++u) b.v[u] = read_a<S>(l, w, u, sub);
+        return b;
+    }
+    __device__ __forceinline__ void multiply(const A& a, const B& b, f32x16 (&acc)[NT]) {
+        const i32x8 va = __builtin_bit_cast(i32x8, a);
+        for (int u = 0; u < NT; ++u)
+            acc[u] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                va, __builtin_bit_cast(i32x8, b.v[u]), acc[u], 0, 0, 0, static_cast<int>(this->w),
+                0, static_cast<int>(this->x[u]));
+    }
+};
+
+// Codes as bf16 numbers, which they are exactly with their scales: 16 of each lane's row at
+// once, for two bf16 instructions.
+template <class Epilogue, int MT, int NT, int SUBS> struct ExactCodeMath : Scales<Epilogue, NT> {
+    static constexpr int kSubs = SUBS, kAhead = 1, kSlots = 1;
+    typedef u32x4 A;
+    struct B {
+        u32x4 v[NT];
+    };
+    bf16x8 held[NT][2];
+
+    // 16 codes as 2 x 8 bf16 values, the scale applied.
+    static __device__ __forceinline__ void decode(u32x4 c, uint32_t byte, bf16x8* out) {
+        const float b = __uint_as_float(byte << 23);
+        for (int i = 0; i < 2; ++i) {
+            const u32x4 v = {
+                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(
+                                                 c[2 * i], b, false)),
+                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(
+                                                 c[2 * i], b, true)),
+                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(
+                                                 c[2 * i + 1], b, false)),
+                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(
+                                                 c[2 * i + 1], b, true))};
+            out[i] = __builtin_bit_cast(bf16x8, v);
+        }
+    }
+    __device__ __forceinline__ void take(const B& b) {
+        for (int u = 0; u < NT; ++u) decode(b.v[u], this->x[u], held[u]);
+    }
+    template <class S> __device__ __forceinline__ A read_a(const uint8_t* l, int w, int t, int sub) {
+        return S::codes(l, w, t, sub * 2 + threadIdx.x % kWave / 32);
+    }
+    template <class S> __device__ __forceinline__ B read_b(const uint8_t* l, int w, int sub) {
+        B b;
+        for (int u = 0; u < NT; ++u) b.v[u] = read_a<S>(l, w, u, sub);
+        return b;
+    }
+    __device__ __forceinline__ void multiply(const A& a, const B&, f32x16 (&acc)[NT]) {
+        bf16x8 va[2];
+        decode(a, this->w, va);
+        for (int q = 0; q < 2; ++q)
+            for (int u = 0; u < NT; ++u)
+                acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(va[q], held[u][q], acc[u], 0, 0, 0);
+    }
+};
+
+template <template <class, int, int, int> class Math, typename Y>
+hipError_t matmul_of(const E4m3ProductArgs& a, hipStream_t s) {
+    typedef ProductTile<Y> E;
     const ProductArgs p{a.w, a.ldw, a.x, a.ldx, a.rows, a.count, a.cols, 1, nullptr, false};
-    const ProductTile<EXACT, Y> e{StoreTile<Y>(a.y, a.ldy), a.w_scales, a.x_scales,
-                                  (a.cols + kBlock - 1) / kBlock};
+    const E e{StoreTile<Y>(a.y, a.ldy), a.w_scales, a.x_scales, (a.cols + kBlock - 1) / kBlock};
     const dim3 block(kTileThreads);
     // Few tiles: smaller ones, so that more CUs have some.
     const int64_t big = (a.rows + 255) / 256 * ((a.count + 255) / 256);
     if (big >= 128) {
-        k_product<ViaCodes, false, false, 256, 256, 2, 4, ProductTile<EXACT, Y>>
-            <<<dim3(product_grid(a.rows, a.count, 256, 256, 1, kTileGroups)), block, 0, s>>>(p, e);
+        const dim3 grid(product_grid(a.rows, a.count, 256, 256, 1, kTileGroups));
+        if (direct(a.w, a.ldw, 1, a.cols) && direct(a.x, a.ldx, 1, a.cols))
+            k_product_direct<ViaCodes, false, false, 256, 256, 2, 4, E, Math>
+                <<<grid, block, 0, s>>>(p, e);
+        else
+            k_product<ViaCodes, false, false, 256, 256, 2, 4, E, Math><<<grid, block, 0, s>>>(p, e);
     } else {
-        k_product<ViaCodes, false, false, 128, 64, 4, 2, ProductTile<EXACT, Y>>
-            <<<dim3(product_grid(a.rows, a.count, 128, 64, 1, 2 * kTileGroups)), block, 0, s>>>(p, e);
+        k_product<ViaCodes, false, false, 128, 64, 4, 2, E, Math>
+            <<<dim3(product_grid(a.rows, a.count, 128, 64, 1, 2 * kTileGroups)), block, 0, s>>>(p,
+                                                                                               e);
     }
     return hipGetLastError();
 }
@@ -265,7 +278,7 @@ hipError_t e4m3_quantize(const void* x, int64_t ldx, int dtype, int64_t rows, in
 }
 
 hipError_t e4m3_matmul(const E4m3ProductArgs& a, int y_dtype, hipStream_t s) {
-    return y_dtype == DL_F32 ? matmul_of<true, float>(a, s) : matmul_of<false, bf16>(a, s);
+    return y_dtype == DL_F32 ? matmul_of<ExactCodeMath, float>(a, s) : matmul_of<CodeMath, bf16>(a, s);
 }
 
 }  // namespace dlk

@@ -31,73 +31,65 @@ struct Part {
 
 // ---- forward -----------------------------------------------------------------
 
-__device__ __forceinline__ float across_groups(float v, bool largest) {
-    for (int k = 16; k < kWave; k *= 2) {
-        const float o = __shfl_xor(v, k);
-        v = largest ? fmaxf(v, o) : v + o;
-    }
-    return v;
-}
-
-struct StatsTile : NoSteps {
+struct StatsTile {
     Part* parts;                          // one row of `rows` for each wave's span
     int64_t rows;
     const int64_t* targets;               // or nullptr
     float* at_target;                     // the targets' logits
 
     template <int MT, int NT>
-    __device__ __forceinline__ void finish(const f32x4 (&acc)[MT][NT], const Place& at) const {
-        const int lane = threadIdx.x % kWave;
+    __device__ __forceinline__ void finish(const f32x16 (&acc)[MT][NT], const Place& at) const {
+        constexpr int kMine = MT * 16;                     // of a token's logits in this lane
+        const int lane = lane_here();
         const int64_t left = at.m - at.m0;                 // of the vocabulary from here on
         if (left <= 0) return;
-        const bool whole = left >= MT * 16;
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
-            const int64_t n = at.n0 + u * 16 + lane % 16;
-            float v[MT * 4];
-            for (int p = 0; p < MT / 2; ++p) eight(acc, p, u, v + 8 * p);
-            // element q of v is token m0 + 32 (q/8) + 8 (lane/16) + q%8
-            const int first = lane / 16 * 8;
-            if (!whole)
-                for (int q = 0; q < MT * 4; ++q)
-                    if (32 * (q / 8) + first + q % 8 >= left) v[q] = -__builtin_inff();
+            const int64_t n = at.n0 + u * kSquare + lane % kSquare;
+            float v[kMine];
+            for (int p = 0; p < 2 * MT; ++p) eight(acc, p, u, v + 8 * p);
+            // element q of v is token m0 + 32 (q/16) + 16 (lane/32) + q%16
+            const int first = lane / 32 * 16;
+            if (left < MT * 32)
+                for (int q = 0; q < kMine; ++q)
+                    if (q / 16 * 32 + first + q % 16 >= left) v[q] = -__builtin_inff();
             if (targets != nullptr) {
                 const int64_t t = n < at.n ? targets[n] - at.m0 : -1;
-                const bool mine = t >= 0 && t < MT * 16 && t < left && (t / 8) % 4 == lane / 16;
+                const bool mine = t >= 0 && t < MT * 32 && t < left && t / 16 % 2 == lane / 32;
                 if (__any(mine)) {
                     float l = 0;
-                    for (int q = 0; q < MT * 4; ++q)
-                        if (32 * (q / 8) + first + q % 8 == t) l = v[q];
+                    for (int q = 0; q < kMine; ++q)
+                        if (q / 16 * 32 + first + q % 16 == t) l = v[q];
                     if (mine) at_target[n] = l;
                 }
             }
             float m = v[0];
-            for (int q = 1; q < MT * 4; ++q) m = fmaxf(m, v[q]);
-            m = across_groups(m, true);
+            for (int q = 1; q < kMine; ++q) m = fmaxf(m, v[q]);
+            m = fmaxf(m, __shfl_xor(m, 32));
             const float from = m == -__builtin_inff() ? 0.0f : m;
             float s = 0, dot = 0;
-            for (int q = 0; q < MT * 4; ++q) {
+            for (int q = 0; q < kMine; ++q) {
                 const float d = v[q] - from, x = exp_of(d);
                 s += x;
                 dot += x > 0 ? x * d : (x != x ? x : 0.0f);
             }
-            s = across_groups(s, false);
-            dot = across_groups(dot, false);
+            s += __shfl_xor(s, 32);
+            dot += __shfl_xor(dot, 32);
             float rest = s - 1;
             // a nearly certain token: the others' sum by itself, with all its digits
             if (__any(s < 1.5f)) {
                 float r = 0, same = 0;
-                for (int q = 0; q < MT * 4; ++q) {
+                for (int q = 0; q < kMine; ++q) {
                     const bool top = v[q] == m;
                     same += top ? 1.0f : 0.0f;
                     r += top ? 0.0f : exp_of(v[q] - from);
                 }
-                r = across_groups(r, false);
-                same = across_groups(same, false);
+                r += __shfl_xor(r, 32);
+                same += __shfl_xor(same, 32);
                 if (s < 1.5f) rest = r + (same - 1);
             }
-            if (lane < 16 && n < at.n)
-                parts[at.m0 / (MT * 16) * rows + n] = Part{m, rest, dot};
+            if (lane < 32 && n < at.n)
+                parts[at.m0 / (MT * 32) * rows + n] = Part{m, rest, dot};
         }
     }
 };
@@ -257,37 +249,49 @@ template <typename T> __global__ __launch_bounds__(256) void k_gather(GatherArgs
 }
 
 // The gradient in the logits of a piece of the vocabulary.
-template <typename T, bool ENTROPY> struct GradTile : NoSteps {
+template <typename T, bool ENTROPY> struct GradTile {
     const RowTerms* terms;
     T* out;
     int64_t ld;
     int64_t first;                        // token that the piece begins with
 
     template <int MT, int NT>
-    __device__ __forceinline__ void finish(const f32x4 (&acc)[MT][NT], const Place& at) const {
-        const int lane = threadIdx.x % kWave;
+    __device__ __forceinline__ void finish(const f32x16 (&acc)[MT][NT], const Place& at) const {
+        const int lane = lane_here();
         if (at.m - at.m0 <= 0) return;
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
-            const int64_t n = at.n0 + u * 16 + lane % 16;
+            const int64_t n = at.n0 + u * kSquare + lane % kSquare;
             if (n >= at.n) continue;
             const RowTerms r = terms[n];
-            const int64_t t = r.target < 0 ? -1 : r.target - first - at.m0 - lane / 16 * 8;
-            const bool hot = t >= 0 && t < MT * 16 && t % 32 < 8;
+            const int64_t t = r.target < 0 ? -1 : r.target - first - at.m0;
+            const bool hot = t >= 0 && t < MT * 32 && t / 16 % 2 == lane / 32;
             // (a row of masked tokens only: their log probabilities are the logits)
             const float from = r.m == -__builtin_inff() ? 0.0f : r.m;
-            for (int p = 0; p < MT / 2; ++p) {
+            auto entropy_part = [&](float x, float lp) {
+                return ENTROPY && x > 0 ? r.b * x * (lp + r.entropy) : 0.0f;
+            };
+            float at_target = 0;
+#pragma unroll
+            for (int p = 0; p < 2 * MT; ++p) {
+                const int mine = eight_at(p, lane);
                 float v[8];
                 eight(acc, p, u, v);
                 for (int q = 0; q < 8; ++q) {
-                    const float lp = (v[q] - from) - r.log_s;
-                    const float x = exp_of(lp);
-                    float d = -r.a * x;
-                    const float h = ENTROPY ? (x > 0 ? r.b * x * (lp + r.entropy) : 0.0f) : 0.0f;
-                    if (hot && t == 32 * p + q) d = -r.a * expm1f(lp);
-                    v[q] = x != x ? x : d - h;
+                    const float lp = (v[q] - from) - r.log_s, x = exp_of(lp);
+                    if (t == mine + q) at_target = lp;
+                    v[q] = x != x ? x : -r.a * x - entropy_part(x, lp);
                 }
-                store8(out + n * ld, at.m0 + p * 32 + lane / 16 * 8, at.m, v);
+                // (zeros up to a multiple of 8: the next products read that far)
+                const int64_t c = at.m0 + mine;
+                if (c + 8 > at.m)
+                    for (int q = 0; q < 8; ++q) v[q] = c + q < at.m ? v[q] : 0.0f;
+                store8(out + n * ld, c, (at.m + 7) / 8 * 8, v);
+            }
+            if (hot && at.m0 + t < at.m) {
+                const float x = exp_of(at_target);
+                out[n * ld + at.m0 + t] = from_f32<T>(
+                    x != x ? x : -r.a * expm1f(at_target) - entropy_part(x, at_target));
             }
         }
     }
@@ -295,21 +299,22 @@ template <typename T, bool ENTROPY> struct GradTile : NoSteps {
 
 // Sums of dx in binary32, a matrix of rows x width for each slice of the vocabulary,
 // added up over its pieces.
-struct SumTile : NoSteps {
+struct SumTile {
     float* sums;
     int64_t rows, ld;
     bool first;
 
     template <int MT, int NT>
-    __device__ __forceinline__ void finish(const f32x4 (&acc)[MT][NT], const Place& at) const {
-        const int lane = threadIdx.x % kWave;
+    __device__ __forceinline__ void finish(const f32x16 (&acc)[MT][NT], const Place& at) const {
+        const int lane = lane_here();
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
-            const int64_t n = at.n0 + u * 16 + lane % 16;
+            const int64_t n = at.n0 + u * kSquare + lane % kSquare;
             if (n >= at.n) continue;
             float* row = sums + (at.slice * rows + n) * ld;
-            for (int p = 0; p < MT / 2; ++p) {
-                const int64_t c = at.m0 + p * 32 + lane / 16 * 8;
+#pragma unroll
+            for (int p = 0; p < 2 * MT; ++p) {
+                const int64_t c = at.m0 + eight_at(p, lane);
                 float v[8];
                 eight(acc, p, u, v);
                 if (!first) {
@@ -395,18 +400,23 @@ Backward backward_plan(int64_t rows, int64_t vocab, int64_t width, int64_t esize
     return b;
 }
 
-template <class Via, bool SA, bool SB, int TM, int TN, int WM, int WN, class E>
-hipError_t product(const ProductArgs& a, const E& e, hipStream_t s) {
-    const dim3 grid(product_grid(a.m, a.n, TM, TN, a.slices, kTileGroups)), block(kTileThreads);
-    k_product<Via, SA, SB, TM, TN, WM, WN, E><<<grid, block, 0, s>>>(a, e);
-    return hipGetLastError();
-}
-
-// bf16: 256 x 256 tiles; binary32, whose three planes fill the LDS: 256 x 128.
+// bf16: 256 x 256 tiles; binary32, whose three planes fill the LDS: 256 x 128.  `padded`: b
+// holds zeros from its end along k up to a multiple of 8.
 template <typename T, bool SA, bool SB, class E>
-hipError_t product_of(const ProductArgs& a, const E& e, hipStream_t s) {
-    if constexpr (sizeof(T) == 2) return product<ViaBf16, SA, SB, 256, 256, 2, 4>(a, e, s);
-    else return product<ViaSplit, SA, SB, 256, 128, 4, 2>(a, e, s);
+hipError_t product_of(const ProductArgs& a, const E& e, hipStream_t s, bool padded = false) {
+    const dim3 block(kTileThreads);
+    if constexpr (sizeof(T) == 2) {
+        const dim3 grid(product_grid(a.m, a.n, 256, 256, a.slices, kTileGroups));
+        if (direct(a.a, a.lda, 2, SA ? 0 : a.k) && direct(a.b, a.ldb, 2, SB || padded ? 0 : a.k))
+            k_product_direct<ViaBf16, SA, SB, 256, 256, 2, 4, E, Bf16Math>
+                <<<grid, block, 0, s>>>(a, e);
+        else
+            k_product<ViaBf16, SA, SB, 256, 256, 2, 4, E, Bf16Math><<<grid, block, 0, s>>>(a, e);
+    } else {
+        k_product<ViaSplit, SA, SB, 256, 128, 4, 2, E, SplitMath>
+            <<<dim3(product_grid(a.m, a.n, 256, 128, a.slices, kTileGroups)), block, 0, s>>>(a, e);
+    }
+    return hipGetLastError();
 }
 
 template <typename T> hipError_t forward(const HeadArgs& a, hipStream_t s) {
@@ -456,18 +466,18 @@ template <typename T> hipError_t backward(const HeadBackwardArgs& a, hipStream_t
         const T* embed = static_cast<const T*>(a.embed) + v0 * a.lde;
         const ProductArgs lp{embed, a.lde, x, b.ld_x, n, a.rows, a.width, 1, count, false};
         if (a.dentropy != nullptr) {
-            const GradTile<T, true> e{{}, terms, p, b.ld_p, v0};
+            const GradTile<T, true> e{terms, p, b.ld_p, v0};
             st = product_of<T, false, false>(lp, e, s);
         } else {
-            const GradTile<T, false> e{{}, terms, p, b.ld_p, v0};
+            const GradTile<T, false> e{terms, p, b.ld_p, v0};
             st = product_of<T, false, false>(lp, e, s);
         }
         if (st != hipSuccess) return st;
         if (a.dx != nullptr) {
             const ProductArgs dp{embed, a.lde, p, b.ld_p, a.width, a.rows, n, b.slices, count,
                                  false};
-            const SumTile e{{}, sums, a.rows, b.ld_s, i == 0};
-            if ((st = product_of<T, true, false>(dp, e, s)) != hipSuccess) return st;
+            const SumTile e{sums, a.rows, b.ld_s, i == 0};
+            if ((st = product_of<T, true, false>(dp, e, s, true)) != hipSuccess) return st;
         }
         if (a.dembed != nullptr) {
             const ProductArgs ep{x, b.ld_x, p, b.ld_p, a.width, n, a.rows, 1, count, true};

@@ -3,15 +3,10 @@
 //
 //   C[n][m] = sum over k of A(m, k) B(n, k),    m < M, n < N, k < K
 //
-// with the tile of sums handed to an epilogue while it is in registers.
-//
-// A workgroup of eight waves keeps TM x TN sums in registers and steps along k
-// by 128 bytes of an operand's row: the next step's 16-byte pieces are under
-// way from memory to registers while this step's products run, and are put
-// into the other one of two LDS buffers halfway through them, so that a step
-// costs one barrier and no wait for memory that its products do not cover.  The
-// pipeline runs on across tiles: a tile's epilogue has the next tile's first
-// step in LDS and its second under way.
+// with the tile of sums handed to an epilogue while it is in registers.  A
+// workgroup of eight waves keeps TM x TN sums (32 x 32 for each matrix
+// instruction) and steps along k; its way through its tiles is one pipeline, so
+// that a tile's epilogue has the next tile's first steps under way.
 //
 // An operand's rows are along k in memory (ACROSS false) or across it (true: k
 // is the slow index, and the LDS reads transpose).  Elements go through as they
@@ -32,7 +27,7 @@
 
 namespace dlk {
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -41,7 +36,7 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kTileThreads = 512;
 constexpr int kTileWaves = kTileThreads / kWave;
-constexpr int kStepBytes = 128;          // of an operand's row, a step
+constexpr int kSquare = 32;              // rows and columns of a matrix instruction's result
 
 struct ProductArgs {
     const void* a;
@@ -54,7 +49,7 @@ struct ProductArgs {
     bool count_is_k;
 };
 
-// ---- from memory to registers to LDS -----------------------------------------
+// ---- one operand -------------------------------------------------------------
 
 // 16 bytes of a row, at any element.
 template <typename T> struct Raw;
@@ -82,12 +77,12 @@ struct ViaCodes {                        // e4m3 codes
     static constexpr int kPlanes = 1;
 };
 
-// One operand's side of a step: ROWS rows (m or n) by kStep elements of k.
-// FIRST: operand A, whose rows a lane's sums run along (see a_row below).
-template <class Via, bool ACROSS, int ROWS, bool FIRST> struct Side {
+// One operand's side of a step: ROWS rows (m or n) by STEP_BYTES of each along k.
+// FIRST: operand A, whose rows a lane's sums run along (see m_row below).
+template <class Via, bool ACROSS, int ROWS, bool FIRST, int STEP_BYTES> struct Side {
     typedef typename Via::elem T;
     static constexpr int kPer = 16 / static_cast<int>(sizeof(T));
-    static constexpr int kStep = kStepBytes / static_cast<int>(sizeof(T));
+    static constexpr int kStep = STEP_BYTES / static_cast<int>(sizeof(T));
     static constexpr int kLine = (ACROSS ? ROWS : kStep) / kPer;     // pieces in a line of memory
     static constexpr int kLines = ACROSS ? kStep : ROWS;
     static constexpr int kMine = kLine * kLines / kTileThreads;
@@ -98,58 +93,61 @@ template <class Via, bool ACROSS, int ROWS, bool FIRST> struct Side {
     static constexpr int kBytes = kPlaneBytes * Via::kPlanes;
     static_assert(kMine >= 1 && kMine * kTileThreads == kLine * kLines, "");
 
-    u32x4 v[kMine];
+    // ---- through registers: any alignment, any element type
 
-    // Rows row0 .. row0 + ROWS - 1 and k from k0 on; 0 outside rows < rows, k < k1.
-    __device__ __forceinline__ void load(const void* p, int64_t ld, int64_t row0, int64_t rows,
-                                         int64_t k0, int64_t k1) {
+    u32x4 v[kMine];
+    const T* at;                                                     // this thread's first piece
+    int64_t ld, apart, lines, wide;                                  // (of what is left from here)
+
+    // Rows row0 .. row0 + ROWS - 1 of `rows`, and k from k0 up to k1.
+    __device__ __forceinline__ void enter(const void* p, int64_t ld_, int64_t row0, int64_t rows,
+                                          int64_t k0, int64_t k1) {
         const int c = threadIdx.x % kLine * kPer, l = threadIdx.x / kLine;
-        const int64_t lines = ACROSS ? k1 - k0 : rows - row0;
-        const int64_t wide = ACROSS ? rows - row0 : k1 - k0;
-        const T* at = static_cast<const T*>(p) + (ACROSS ? k0 * ld + row0 : row0 * ld + k0) +
-                      l * ld + c;
+        ld = ld_;
+        apart = kApart * ld;
+        lines = ACROSS ? k1 - k0 : rows - row0;
+        wide = ACROSS ? rows - row0 : k1 - k0;
+        at = static_cast<const T*>(p) + (ACROSS ? k0 * ld + row0 : row0 * ld + k0) + l * ld + c;
+    }
+    // The step's pieces (0 outside), and on to the next step.
+    __device__ __forceinline__ void load() {
+        const int c = threadIdx.x % kLine * kPer, l = threadIdx.x / kLine;
         if (lines >= kLines && wide >= kLine * kPer) {
             for (int j = 0; j < kMine; ++j)
-                v[j] = *reinterpret_cast<const typename Raw<T>::any*>(at + j * (kApart * ld));
+                v[j] = *reinterpret_cast<const typename Raw<T>::any*>(at + j * apart);
         } else {
             for (int j = 0; j < kMine; ++j) {
-                const T* q = at + j * (kApart * ld);
+                const T* q = at + j * apart;
                 v[j] = u32x4{};
                 if (l + j * kApart >= lines) continue;
                 if (c + kPer <= wide) {
                     v[j] = *reinterpret_cast<const typename Raw<T>::any*>(q);
                 } else if (c < wide) {
-                    T t[kPer] = {};
-                    for (int i = 0; i < kPer; ++i)
-                        if (c + i < wide) t[i] = q[i];
-                    __builtin_memcpy(&v[j], t, 16);
+                    const int n = static_cast<int>(wide) - c;
+#pragma unroll 1
+                    for (int i = 0; i < n; ++i) {
+                        constexpr int kIn = 4 / static_cast<int>(sizeof(T));
+                        uint32_t e = 0;
+                        __builtin_memcpy(&e, q + i, sizeof(T));
+                        e <<= i % kIn * 8 * static_cast<int>(sizeof(T)) % 32;
+                        for (int k = 0; k < 4; ++k) v[j][k] |= i / kIn == k ? e : 0;
+                    }
                 }
             }
         }
+        at += ACROSS ? kStep * ld : kStep;
+        (ACROSS ? lines : wide) -= kStep;
     }
-
-    // The 16-byte piece of row `row` that holds its piece c is at piece c ^ key(row).
-    // Eight lanes read the same piece of eight rows: neighbouring ones, or for A rows
-    // 0 1 2 3 8 9 10 11 of each 16.
-    static __device__ __forceinline__ int key(int row) {
-        if constexpr (kRowBytes == 128)
-            return FIRST ? (row & 3) | ((row >> 1) & 4) : row & 7;
-        else
-            return FIRST ? ((row >> 1) & 1) | ((row >> 2) & 2) : (row >> 1) & 3;
-    }
-    // Across k, four lines of 64 (A) or 32 (B) bytes are read together.
-    static __device__ __forceinline__ int key_across(int k) { return (k & 3) << (FIRST ? 6 : 5); }
-
     __device__ __forceinline__ void put(uint8_t* lds) const {
         const int c = threadIdx.x % kLine, l = threadIdx.x / kLine;
         for (int j = 0; j < kMine; ++j) {
             const int line = l + j * kApart;
             if constexpr (Via::kPlanes == 1) {
-                const int at = line * kRowBytes +
+                const int to = line * kRowBytes +
                                (ACROSS ? (c * 16) ^ key_across(line) : (c ^ key(line)) * 16);
-                *reinterpret_cast<u32x4*>(lds + at) = v[j];
+                *reinterpret_cast<u32x4*>(lds + to) = v[j];
             } else {
-                const int at = line * kRowBytes +
+                const int to = line * kRowBytes +
                                (ACROSS ? (c * 8) ^ key_across(line)
                                        : ((c >> 1) ^ key(line)) * 16 + (c & 1) * 8);
                 uint32_t q[3][2];
@@ -165,81 +163,196 @@ template <class Via, bool ACROSS, int ROWS, bool FIRST> struct Side {
                     }
                 }
                 for (int p = 0; p < 3; ++p)
-                    *reinterpret_cast<u32x2*>(lds + p * kPlaneBytes + at) = u32x2{q[p][0], q[p][1]};
+                    *reinterpret_cast<u32x2*>(lds + p * kPlaneBytes + to) = u32x2{q[p][0], q[p][1]};
             }
         }
     }
 
-    // The first operand's rows in the order that leaves a lane eight neighbouring sums of a
-    // pair of tiles: row r of tile t is row 32 (t/2) + 8 (r/4) + 4 (t%2) + r%4 of the wave's.
-    static __device__ __forceinline__ int a_row(int t, int r) {
-        return 32 * (t / 2) + 8 * (r / 4) + 4 * (t % 2) + r % 4;
+    // ---- straight into LDS: rows at multiples of 16 bytes, as far as `direct` below allows
+    //
+    // 64 lanes' pieces are neighbours in LDS: each lane asks for the piece that belongs in its
+    // place.  The buffer's bounds turn what lies outside into zeros without a branch, at the
+    // end of k by an offset past them; what a piece holds past the end of the other side
+    // belongs to rows of the result that nobody looks at.
+    struct Direct {
+        const uint8_t *matrix, *base;     // base: of the step, the same for all lanes
+        uint32_t offset[kMine];           // of this thread's pieces, in bytes
+        int64_t row_bytes;
+        int lines, wide, edge;            // what is left (edge: bytes of a line that is across k)
+
+        static __device__ __forceinline__ int piece() {
+            const int c = threadIdx.x % kLine, l = threadIdx.x / kLine;
+            static_assert(ACROSS ? kApart % 4 == 0 : kApart % 32 == 0, "one key for each j");
+            return c ^ (ACROSS ? key_across(l) / 16 : key(l));
+        }
+        __device__ __forceinline__ void start(const void* p, int64_t ld) {
+            matrix = base = static_cast<const uint8_t*>(p);
+            edge = 0;
+            row_bytes = ld * static_cast<int64_t>(sizeof(T));
+            for (int j = 0; j < kMine; ++j)
+                offset[j] = static_cast<uint32_t>((threadIdx.x / kLine + j * kApart) * row_bytes) +
+                            piece() * 16;
+        }
+        __device__ __forceinline__ void enter(int64_t row0, int64_t rows, int64_t k0, int64_t k1) {
+            const int64_t r = rows - row0 < ROWS ? rows - row0 : ROWS;
+            const int64_t k = k1 > k0 ? k1 - k0 : 0;
+            base = matrix +
+                   (ACROSS ? k0 * row_bytes + row0 * static_cast<int64_t>(sizeof(T))
+                           : row0 * row_bytes + k0 * static_cast<int64_t>(sizeof(T)));
+            lines = static_cast<int>(ACROSS ? k : r);
+            wide = static_cast<int>(k);
+            edge = static_cast<int>(r * static_cast<int64_t>(sizeof(T)) + 15) / 16 * 16;
+        }
+        // Nothing more to load: zeros from here on.
+        __device__ __forceinline__ void stop() { lines = wide = 0; }
+        __device__ __forceinline__ void load(uint8_t* lds) {
+            typedef __attribute__((address_space(3))) void lds_any;
+            uint8_t* to = lds + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * (kWave * 16);
+            // Bytes from the step's first to its last.
+            const int n = ACROSS ? (lines < kLines ? lines : kLines) : lines;
+            const int last = ACROSS ? edge : (wide < kStep ? wide : kStep) * static_cast<int>(sizeof(T));
+            const uint32_t bytes =
+                n <= 0 || last <= 0 ? 0 : static_cast<uint32_t>((n - 1) * row_bytes) + ((last + 15) & ~15);
+            __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<uint8_t*>(base), 0, bytes, 0x00020000);
+            for (int j = 0; j < kMine; ++j) {
+                uint32_t o = offset[j];
+                if constexpr (!ACROSS) o = piece() * kPer < wide ? o : 0xFFFFFFF0u;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_any*)(to + j * (kTileThreads * 16)),
+                                                         16, o, 0, 0, 0);
+            }
+            base += ACROSS ? kStep * row_bytes : kStep * static_cast<int64_t>(sizeof(T));
+            if (ACROSS) lines -= kStep;
+            else wide -= kStep;
+        }
+    };
+
+    // ---- in LDS
+
+    // The 16-byte piece of row `row` that holds its piece c is at piece c ^ key(row).  A
+    // 128-bit read takes 16 lanes at a time, 0-3 12-15 20-23 24-27 and 4-7 8-11 16-19 28-31 of
+    // each 32: with the keys, and with A's order of rows too, they meet 64 different banks.
+    static __device__ __forceinline__ int key(int row) {
+        return kRowBytes == 128 ? (row >> 1 & 1) | (row >> 3 & 3) << 1 : row >> 3 & 3;
+    }
+    // Across k, four lines of 64 (A) or 32 (B) bytes are read together.
+    static __device__ __forceinline__ int key_across(int k) { return (k & 3) << (FIRST ? 6 : 5); }
+
+    // The matrix instruction leaves a lane rows 8 i + 4 (lane/32) .. + 3 of its column.  The
+    // first operand's rows in the order that makes them 16 neighbours: row r is row
+    // 16 (r/4%2) + 4 (r/8) + r%4.
+    static __device__ __forceinline__ int m_row(int r) {
+        return FIRST ? 16 * (r / 4 % 2) + 4 * (r / 8) + r % 4 : r;
     }
 
-    // 8 elements of k for each lane: row `lane % 16` of 16-row tile t of the rows from row0
-    // on, k = 32 sub + 8 (lane / 16) .. + 7.
+    // 8 elements of k for each lane: row `lane % 32` of 32-row tile t of the rows from row0
+    // on, k = 16 sub + 8 (lane / 32) .. + 7.
     static __device__ __forceinline__ bf16x8 frag(const uint8_t* lds, int row0, int t, int sub) {
-        const int r = threadIdx.x % 16, g = threadIdx.x / 16 % 4;
+        const int lane = threadIdx.x % kWave;
         if constexpr (!ACROSS) {
-            const int row = row0 + (FIRST ? a_row(t, r) : t * 16 + r);
-            return *reinterpret_cast<const bf16x8*>(lds + row * kRowBytes +
-                                                    ((sub * 4 + g) ^ key(row)) * 16);
+            const int row = m_row(lane % 32);
+            return *reinterpret_cast<const bf16x8*>(
+                lds + (row0 + t * 32) * kRowBytes + row * kRowBytes +
+                ((sub * 2 + lane / 32) ^ key(row)) * 16);
         } else {
             // (lane 4 i + j of 16 gives the place of columns 4 j .. 4 j + 3 of line i, and gets
             // column 4 i + j of the four lines)
-            const int row = row0 + (FIRST ? a_row(t, 4 * (r % 4)) : t * 16 + 4 * (r % 4));
-            const int k = 32 * sub + 8 * g + r / 4;
-            const int at = k * kRowBytes + ((row * 2) ^ key_across(k));
+            const int row = row0 + t * 32 + m_row(lane / 16 % 2 * 16 + 4 * (lane % 4));
+            const int k = 16 * sub + 8 * (lane / 32) + lane % 16 / 4;
+            const int from = k * kRowBytes + ((row * 2) ^ key_across(k));
             typedef __attribute__((address_space(3))) i16x4 lds4;
             union {
                 i16x4 h[2];
                 bf16x8 all;
             } u;
-            u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(lds + at));
-            u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(lds + at + 4 * kRowBytes));
+            u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(lds + from));
+            u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(lds + from + 4 * kRowBytes));
             return u.all;
         }
     }
 
-    // 16 codes for each lane: pieces 4 half + (lane / 16) of its row.
-    static __device__ __forceinline__ u32x4 codes(const uint8_t* lds, int row0, int t, int half) {
-        const int r = threadIdx.x % 16, g = threadIdx.x / 16 % 4;
-        const int row = row0 + (FIRST ? a_row(t, r) : t * 16 + r);
-        return *reinterpret_cast<const u32x4*>(lds + row * kRowBytes +
-                                               ((half * 4 + g) ^ key(row)) * 16);
+    // Piece `c` of each lane's row of codes.
+    static __device__ __forceinline__ u32x4 codes(const uint8_t* lds, int row0, int t, int c) {
+        const int row = m_row(threadIdx.x % 32);
+        return *reinterpret_cast<const u32x4*>(lds + (row0 + t * 32) * kRowBytes + row * kRowBytes +
+                                               (c ^ key(row)) * 16);
     }
 };
+
+// What is the same for all lanes, as a scalar (divisions leave it in vector registers).
+__device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t scalar(int64_t v) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+    return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
 
 // ---- the order of the tiles --------------------------------------------------
 
 // Workgroups are dealt to the eight XCDs in turn.  Each XCD takes a run of
-// neighbouring items, whose operands its L2 then holds once: bands of up to
-// eight tiles of the shorter side, walked along the longer one.
+// neighbouring whole tiles, whose operands its L2 then holds once: bands of up to
+// eight tiles of the shorter side, walked along the longer one.  What is left of the
+// longer side past its last whole tile comes at the end, dealt over all XCDs, so that it
+// does not cost a whole turn more.  (Fewer than 2^31 items: 32 bits count them.)
 struct Items {
-    int64_t m_tiles, n_tiles, tiles, end, at, step;
+    int few, many, all, run, at, end, step;
+    bool n_short;
 
     __device__ Items(int64_t m, int64_t n, int tm, int tn, int slices) {
-        m_tiles = (m + tm - 1) / tm;
-        n_tiles = (n + tn - 1) / tn;
-        tiles = m_tiles * n_tiles;
-        const int64_t all = tiles * slices;
-        const int64_t run = (all + 7) / 8, x = blockIdx.x % 8;
+        const int m_tiles = static_cast<int>((m + tm - 1) / tm);
+        const int n_tiles = static_cast<int>((n + tn - 1) / tn);
+        n_short = n_tiles <= m_tiles;
+        few = n_short ? n_tiles : m_tiles;
+        many = static_cast<int>(n_short ? m / tm : n / tn);
+        all = few * many * slices;
+        const int edge = few * ((n_short ? m_tiles : n_tiles) - many) * slices;
+        const int x = blockIdx.x % 8;
+        const int each = (all + 7) / 8, from = each * x < all ? each * x : all;
+        run = all - from < each ? all - from : each;
         step = gridDim.x / 8;
-        end = run * (x + 1) < all ? run * (x + 1) : all;
-        at = run * x + blockIdx.x / 8;
+        at = blockIdx.x / 8;
+        end = run + (edge + 7 - x) / 8;
     }
     __device__ bool left() const { return at < end; }
     __device__ void next() { at += step; }
-    __device__ void place(int64_t* mt, int64_t* nt, int* slice) const {
-        *slice = static_cast<int>(at / tiles);
-        const int64_t t = at % tiles;
-        const bool n_short = n_tiles <= m_tiles;
-        const int64_t few = n_short ? n_tiles : m_tiles, many = n_short ? m_tiles : n_tiles;
-        const int64_t band = t / (8 * many), in = t % (8 * many);
-        const int64_t wide = few - band * 8 < 8 ? few - band * 8 : 8;
-        const int64_t s = band * 8 + in % wide, l = in / wide;
-        *mt = n_short ? l : s;
-        *nt = n_short ? s : l;
+    __device__ void place(int* mt, int* nt, int* slice) const {
+        const int x = blockIdx.x % 8;
+        int s, l;
+        if (at < run) {
+            const int each = (all + 7) / 8, i = each * x + at, tiles = few * many;
+            *slice = i / tiles;
+            const int t = i % tiles, band = t / (8 * many), in = t % (8 * many);
+            const int wide = few - band * 8 < 8 ? few - band * 8 : 8;
+            s = band * 8 + in % wide;
+            l = in / wide;
+        } else {
+            const int i = (at - run) * 8 + x;
+            *slice = i / few;
+            s = i % few;
+            l = many;
+        }
+        *slice = scalar(*slice);
+        *mt = scalar(n_short ? l : s);
+        *nt = scalar(n_short ? s : l);
+    }
+};
+
+// One workgroup's way through its items, `turns` steps of k each.
+struct Cursor {
+    Items items;
+    int mt, nt, slice, turns;
+    bool left;
+
+    __device__ void enter(int64_t k, int slices, int step) {
+        left = items.left();
+        if (!left) return;
+        items.place(&mt, &nt, &slice);
+        const int64_t len = length(k, slices, step), k0 = slice * len;
+        const int64_t n = k - k0 < len ? k - k0 : len;
+        turns = scalar(n <= step ? 1 : static_cast<int>((n + step - 1) / step));
+    }
+    static __device__ int64_t length(int64_t k, int slices, int step) {
+        return scalar(((k + slices - 1) / slices + step - 1) / step * step);
     }
 };
 
@@ -254,53 +367,125 @@ inline unsigned product_grid(int64_t m, int64_t n, int tm, int tn, int slices, i
 // ---- the product -------------------------------------------------------------
 
 // Where a wave's sums are: element i of acc[t][u] is C[n][m] with
-//   m = m0 + 32 (t/2) + 8 (lane/16) + 4 (t%2) + i,   n = n0 + 16 u + lane%16.
+//   m = m0 + 32 t + 16 (lane/32) + i,   n = n0 + 32 u + lane%32.
 struct Place {
     int64_t m0, n0;                       // of the wave
     int64_t m, n;                         // ends of the product
     int slice;
 };
 
-template <class Via, bool SA, bool SB, int TM, int TN, int WM, int WN, class Epilogue>
+template <int N> struct Count {
+    static constexpr int value = N;
+};
+
+// How a step's products are made: kSubs times, every row tile of A with all of B's.
+// A's pieces are read kAhead row tiles before their use, B's (into the next of kSlots) for
+// the next time round.
+template <class Epilogue, int MT, int NT, int SUBS> struct Bf16Math {
+    static constexpr int kSubs = SUBS, kAhead = 3, kSlots = 2;
+    typedef bf16x8 A;
+    struct B {
+        bf16x8 v[NT];
+    };
+    __device__ __forceinline__ void enter(const Epilogue&, const Place&) {}
+    __device__ __forceinline__ void step() {}
+    __device__ __forceinline__ void take(const B&) {}
+    template <class S> __device__ __forceinline__ A read_a(const uint8_t* l, int w, int t, int sub) {
+        return S::frag(l, w, t, sub);
+    }
+    template <class S> __device__ __forceinline__ B read_b(const uint8_t* l, int w, int sub) {
+        B b;
+        for (int u = 0; u < NT; ++u) b.v[u] = S::frag(l, w, u, sub);
+        return b;
+    }
+    __device__ __forceinline__ void multiply(const A& a, const B& b, f32x16 (&acc)[NT]) {
+        for (int u = 0; u < NT; ++u)
+            acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b.v[u], acc[u], 0, 0, 0);
+    }
+};
+
+template <class Epilogue, int MT, int NT, int SUBS> struct SplitMath {
+    static constexpr int kSubs = SUBS, kAhead = 1, kSlots = 2;
+    struct A {
+        bf16x8 p[3];
+    };
+    struct B {
+        bf16x8 v[3][NT];
+    };
+    __device__ __forceinline__ void enter(const Epilogue&, const Place&) {}
+    __device__ __forceinline__ void step() {}
+    __device__ __forceinline__ void take(const B&) {}
+    template <class S> __device__ __forceinline__ A read_a(const uint8_t* l, int w, int t, int sub) {
+        A a;
+        for (int p = 0; p < 3; ++p) a.p[p] = S::frag(l + p * S::kPlaneBytes, w, t, sub);
+        return a;
+    }
+    template <class S> __device__ __forceinline__ B read_b(const uint8_t* l, int w, int sub) {
+        B b;
+        for (int p = 0; p < 3; ++p)
+            for (int u = 0; u < NT; ++u) b.v[p][u] = S::frag(l + p * S::kPlaneBytes, w, u, sub);
+        return b;
+    }
+    __device__ __forceinline__ void multiply(const A& a, const B& b, f32x16 (&acc)[NT]) {
+        // the smallest products first
+        constexpr int pa[6] = {0, 2, 1, 0, 1, 0}, pb[6] = {2, 0, 1, 1, 0, 0};
+#pragma unroll
+        for (int q = 0; q < 6; ++q)
+            for (int u = 0; u < NT; ++u)
+                acc[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[pa[q]], b.v[pb[q]][u], acc[u],
+                                                                 0, 0, 0);
+    }
+};
+
+// Through registers.  The next step's 16-byte pieces are under way from memory to registers
+// while this step's products run, and are put into the other one of two LDS buffers halfway
+// through them: a step costs one barrier and no wait that its products do not cover.
+constexpr int kStepBytes = 128;
+
+template <class Via, bool SA, bool SB, int TM, int TN, int WM, int WN, class Epilogue,
+          template <class, int, int, int> class Math>
 __global__ __launch_bounds__(kTileThreads, 2) void k_product(ProductArgs a, Epilogue e) {
     static_assert(WM * WN == kTileWaves, "");
-    constexpr int kMT = TM / WM / 16, kNT = TN / WN / 16;
-    typedef Side<Via, SA, TM, true> SideA;
-    typedef Side<Via, SB, TN, false> SideB;
-    constexpr int kStep = SideA::kStep;
+    constexpr int kMT = TM / WM / kSquare, kNT = TN / WN / kSquare;
+    typedef Side<Via, SA, TM, true, kStepBytes> SideA;
+    typedef Side<Via, SB, TN, false, kStepBytes> SideB;
+    // (a sub-step is 32 bytes of what LDS holds)
+    typedef Math<Epilogue, kMT, kNT, SideA::kStep * SideA::kHeld / 32> Made;
+    constexpr int kStep = SideA::kStep, kGroups = Made::kSubs * kMT, kAhead = Made::kAhead;
+    static_assert(kMT >= 1 && kNT >= 1 && kGroups % (kAhead + 1) == 0 && kGroups > kAhead &&
+                      Made::kSubs % Made::kSlots == 0, "");
     __shared__ __attribute__((aligned(128))) uint8_t lds[2][SideA::kBytes + SideB::kBytes];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wm = wave / WN * (TM / WM), wn = wave % WN * (TN / WN);
-    if (a.count != nullptr) (a.count_is_k ? a.k : a.n) = *a.count;
-    const int64_t per_slice = ((a.k + a.slices - 1) / a.slices + kStep - 1) / kStep * kStep;
-
-    struct Cursor {
-        Items items;
-        int64_t mt, nt, k0, k1;
-        int slice;
-    };
-    auto enter = [&](Cursor& c) {
-        if (!c.items.left()) return;
-        c.items.place(&c.mt, &c.nt, &c.slice);
-        c.k0 = c.slice * per_slice;
-        c.k1 = c.k0 + per_slice < a.k ? c.k0 + per_slice : a.k;
-    };
-    Cursor in{Items(a.m, a.n, TM, TN, a.slices), 0, 0, 0, 0, 0};
-    enter(in);
+    if (a.count != nullptr) {
+        const int n = scalar(*a.count);
+        if (a.count_is_k) a.k = n;
+        else a.n = n;
+    }
+    Cursor in{Items(a.m, a.n, TM, TN, a.slices), 0, 0, 0, 0, false};
+    in.enter(a.k, a.slices, kStep);
     Cursor out = in;
     SideA sa;
     SideB sb;
+    auto aim = [&] {
+        if (!in.left) return;
+        const int64_t n = Cursor::length(a.k, a.slices, kStep), k0 = in.slice * n;
+        const int64_t k1 = k0 + n < a.k ? k0 + n : a.k;
+        sa.enter(a.a, a.lda, static_cast<int64_t>(in.mt) * TM, a.m, k0, k1);
+        sb.enter(a.b, a.ldb, static_cast<int64_t>(in.nt) * TN, a.n, k0, k1);
+    };
+    aim();
     // The step at `in` into registers; then on to the next one.
     bool held = false;
     auto fetch = [&] {
-        held = in.items.left();
+        held = in.left;
         if (!held) return;
-        sa.load(a.a, a.lda, in.mt * TM, a.m, in.k0, in.k1);
-        sb.load(a.b, a.ldb, in.nt * TN, a.n, in.k0, in.k1);
-        in.k0 += kStep;
-        if (in.k0 >= in.k1) {
+        sa.load();
+        sb.load();
+        if (--in.turns == 0) {
             in.items.next();
-            enter(in);
+            in.enter(a.k, a.slices, kStep);
+            aim();
         }
     };
     auto put = [&](uint8_t* to) {
@@ -313,100 +498,237 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product(ProductArgs a, Epil
     put(lds[0]);
     fetch();
     __syncthreads();
-    while (out.items.left()) {
-        f32x4 acc[kMT][kNT] = {};
-        typename Epilogue::template Steps<kNT> steps;
-        const Place at{out.mt * TM + wm, out.nt * TN + wn, a.m, a.n, out.slice};
-        steps.enter(e, at, out.k0);
+    while (out.left) {
+        f32x16 acc[kMT][kNT] = {};
+        const Place at{static_cast<int64_t>(out.mt) * TM + wm,
+                       static_cast<int64_t>(out.nt) * TN + wn, a.m, a.n, out.slice};
+        Made made;
+        made.enter(e, at);
+        typename Made::A va[kAhead + 1];
+        typename Made::B vb[Made::kSlots];
+        vb[0] = made.template read_b<SideB>(lds[buf] + SideA::kBytes, wn, 0);
+#pragma unroll
+        for (int g = 0; g < kAhead; ++g) va[g] = made.template read_a<SideA>(lds[buf], wm, g % kMT, g / kMT);
+        bool more;
+#pragma clang loop unroll(disable)
         do {
-            const uint8_t* la = lds[buf];
-            const uint8_t* lb = la + SideA::kBytes;
-            if constexpr (Via::kPlanes == 3) {
-                bf16x8 vb[3][kNT];
-                for (int p = 0; p < 3; ++p)
-                    for (int u = 0; u < kNT; ++u)
-                        vb[p][u] = SideB::frag(lb + p * SideB::kPlaneBytes, wn, u, 0);
+            const uint8_t *l = lds[buf], *next = lds[buf ^ 1];
+            more = --out.turns > 0;
+            made.step();
 #pragma unroll
-                for (int t = 0; t < kMT; ++t) {
-                    if (t == kMT / 2) {
-                        put(lds[buf ^ 1]);
-                        fetch();
-                    }
-                    bf16x8 va[3];
-                    for (int p = 0; p < 3; ++p)
-                        va[p] = SideA::frag(la + p * SideA::kPlaneBytes, wm, t, 0);
-                    // the smallest products first
-                    constexpr int pa[6] = {0, 2, 1, 0, 1, 0}, pb[6] = {2, 0, 1, 1, 0, 0};
-                    for (int q = 0; q < 6; ++q)
-                        for (int u = 0; u < kNT; ++u)
-                            acc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                va[pa[q]], vb[pb[q]][u], acc[t][u], 0, 0, 0);
-                }
-            } else if constexpr (sizeof(typename Via::elem) == 2) {
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    if (s == 1) {
-                        put(lds[buf ^ 1]);
-                        fetch();
-                    }
-                    bf16x8 vb[kNT];
-                    for (int u = 0; u < kNT; ++u) vb[u] = SideB::frag(lb, wn, u, s);
-#pragma unroll
-                    for (int t = 0; t < kMT; ++t) {
-                        const bf16x8 va = SideA::frag(la, wm, t, s);
-                        for (int u = 0; u < kNT; ++u)
-                            acc[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, vb[u],
-                                                                                acc[t][u], 0, 0, 0);
-                    }
-                }
-            } else {
-                steps.template product<SideA, SideB, kMT>(la, lb, wm, wn, acc, [&] {
+            for (int g = 0; g < kGroups; ++g) {
+                const int sub = g / kMT, h = g + kAhead;
+                if (g == kGroups / 2) {
                     put(lds[buf ^ 1]);
                     fetch();
-                });
+                }
+                if (g % kMT == 0) made.take(vb[sub % Made::kSlots]);
+                // All of this step has been read, and the next one is in LDS.  (After a
+                // tile's last step these are the next tile's, and not used.)
+                if (h == kGroups) __syncthreads();
+                if (h % kMT == 0)
+                    vb[h / kMT % Made::kSlots] = made.template read_b<SideB>(
+                        (h < kGroups ? l : next) + SideA::kBytes, wn, h / kMT % Made::kSubs);
+                va[h % (kAhead + 1)] = made.template read_a<SideA>(
+                    h < kGroups ? l : next, wm, h % kMT, h / kMT % Made::kSubs);
+                __builtin_amdgcn_sched_barrier(0);
+                made.multiply(va[g % (kAhead + 1)], vb[sub % Made::kSlots], acc[g % kMT]);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            __syncthreads();
             buf ^= 1;
-            out.k0 += kStep;
-        } while (out.k0 < out.k1);
+        } while (more);
         e.template finish<kMT, kNT>(acc, at);
         out.items.next();
-        enter(out);
+        out.enter(a.k, a.slices, kStep);
     }
 }
 
-// An epilogue whose operands need nothing at each step.
-struct NoSteps {
-    template <int NT> struct Steps {
-        template <class E> __device__ void enter(const E&, const Place&, int64_t) {}
-    };
-};
+// Straight to LDS, whole 128-byte lines of memory at a time (half lines cost as many
+// requests to L2, and were slower).  No registers are held meanwhile, and LDS holds five
+// units, one operand's 32 KB of a step each, in turn A B A B A: while a step's products run,
+// the next step's two are there or nearly so and A of the step after it is under way, and
+// when they are done their places take that step's B and the next A.  So A, which is
+// taken to be the operand that comes from far (weights), has the time of two to three steps to
+// come, B (tokens, read by many) that of one to two.  The loop has no branch but those to
+// the next tile, so that the compiler can count the reads that are under way.
+constexpr int kUnits = 5, kUnitBytes = 32768;
 
-// The eight neighbouring sums of pair p of tiles.
-template <int MT, int NT>
-__device__ __forceinline__ void eight(const f32x4 (&acc)[MT][NT], int p, int u, float* v) {
-    for (int i = 0; i < 4; ++i) {
-        v[i] = acc[2 * p][u][i];
-        v[4 + i] = acc[2 * p + 1][u][i];
+template <class Via, bool SA, bool SB, int TM, int TN, int WM, int WN, class Epilogue,
+          template <class, int, int, int> class Math>
+__global__ __launch_bounds__(kTileThreads, 2) void k_product_direct(ProductArgs a, Epilogue e) {
+    static_assert(WM * WN == kTileWaves, "");
+    constexpr int kMT = TM / WM / kSquare, kNT = TN / WN / kSquare;
+    typedef Side<Via, SA, TM, true, kStepBytes> SideA;
+    typedef Side<Via, SB, TN, false, kStepBytes> SideB;
+    typedef Math<Epilogue, kMT, kNT, 4> Made;
+    constexpr int kStep = SideA::kStep, kGroups = Made::kSubs * kMT, kAhead = Made::kAhead;
+    constexpr int kLoads = SideA::kMine;                             // of a unit, each thread's
+    static_assert(SideA::kBytes == kUnitBytes && SideB::kBytes == kUnitBytes, "");
+    static_assert(kGroups % (kAhead + 1) == 0 && kGroups > kAhead + 1 &&
+                      Made::kSubs % Made::kSlots == 0, "");
+    __shared__ __attribute__((aligned(128))) uint8_t lds[kUnits * kUnitBytes];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wm = wave / WN * (TM / WM), wn = wave % WN * (TN / WN);
+    if (a.count != nullptr) {
+        const int n = scalar(*a.count);
+        if (a.count_is_k) a.k = n;
+        else a.n = n;
     }
+    Cursor out{Items(a.m, a.n, TM, TN, a.slices), 0, 0, 0, 0, false};
+    out.enter(a.k, a.slices, kStep);
+    Cursor in_a = out, in_b = out;
+    typename SideA::Direct sa;
+    typename SideB::Direct sb;
+    sa.start(a.a, a.lda);
+    sb.start(a.b, a.ldb);
+    auto aim = [&](Cursor& in, auto& side, int tile, int64_t rows) {
+        if (in.left) {
+            const int64_t n = Cursor::length(a.k, a.slices, kStep), k0 = in.slice * n;
+            side.enter(static_cast<int64_t>(tile), rows, k0, k0 + n < a.k ? k0 + n : a.k);
+        } else {
+            side.stop();
+            in.turns = INT32_MAX;
+        }
+        // (so that the compiler knows of no scalar load under way in the loop below, beside
+        // which it could not count LDS reads)
+        __builtin_amdgcn_s_waitcnt(0xC07F);
+    };
+    aim(in_a, sa, in_a.mt * TM, a.m);
+    aim(in_b, sb, in_b.nt * TN, a.n);
+    // Sends for the next unit of an operand.
+    auto fetch_a = [&](int place) {
+        sa.load(lds + place);
+        if (--in_a.turns == 0) {
+            in_a.items.next();
+            in_a.enter(a.k, a.slices, kStep);
+            aim(in_a, sa, in_a.mt * TM, a.m);
+        }
+    };
+    auto fetch_b = [&](int place) {
+        sb.load(lds + place);
+        if (--in_b.turns == 0) {
+            in_b.items.next();
+            in_b.enter(a.k, a.slices, kStep);
+            aim(in_b, sb, in_b.nt * TN, a.n);
+        }
+    };
+    auto after = [](int place, int units) {
+        const int p = place + units * kUnitBytes;
+        return p >= kUnits * kUnitBytes ? p - kUnits * kUnitBytes : p;
+    };
+    // All but the last `late` units sent for are in LDS, for every wave, and what every wave
+    // has asked LDS for so far it has.
+    auto meet = [&](auto late) {
+        constexpr int n = decltype(late)::value * kLoads;
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt((n & 15) | (n >> 4 << 14) | 0x70);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+    fetch_a(0);
+    fetch_b(kUnitBytes);
+    fetch_a(2 * kUnitBytes);
+    fetch_b(3 * kUnitBytes);
+    fetch_a(4 * kUnitBytes);
+    meet(Count<3>{});
+    int at_a = 0, at_b = kUnitBytes;
+    while (out.left) {
+        f32x16 acc[kMT][kNT] = {};
+        const Place at{static_cast<int64_t>(out.mt) * TM + wm,
+                       static_cast<int64_t>(out.nt) * TN + wn, a.m, a.n, out.slice};
+        Made made;
+        made.enter(e, at);
+        typename Made::A va[kAhead + 1];
+        typename Made::B vb[Made::kSlots];
+        vb[0] = made.template read_b<SideB>(lds + at_b, wn, 0);
+#pragma unroll
+        for (int g = 0; g < kAhead; ++g)
+            va[g] = made.template read_a<SideA>(lds + at_a, wm, g % kMT, g / kMT);
+        // An epilogue's loads and stores are counted with the units: all have to be in.
+        bool fresh = true, more;
+#pragma clang loop unroll(disable)
+        do {
+            more = --out.turns > 0;
+            made.step();
+            const int next_a = after(at_a, 2), next_b = after(at_b, 2);
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+                const int sub = g / kMT, h = g + kAhead;
+                if (g % kMT == 0) made.take(vb[sub % Made::kSlots]);
+                if (h == kGroups) {
+                    if (fresh) {
+                        __builtin_amdgcn_s_waitcnt(0x0F70);
+                        fresh = false;
+                    }
+                    meet(Count<1>{});
+                }
+                // (after a tile's last step these are the next tile's, and not used)
+                if (h % kMT == 0)
+                    vb[h / kMT % Made::kSlots] = made.template read_b<SideB>(
+                        lds + (h < kGroups ? at_b : next_b), wn, h / kMT % Made::kSubs);
+                va[h % (kAhead + 1)] = made.template read_a<SideA>(
+                    lds + (h < kGroups ? at_a : next_a), wm, h % kMT, h / kMT % Made::kSubs);
+                __builtin_amdgcn_sched_barrier(0);
+                made.multiply(va[g % (kAhead + 1)], vb[sub % Made::kSlots], acc[g % kMT]);
+                __builtin_amdgcn_sched_barrier(0);
+                // this step has been read by all: its places are free
+                if (h == kGroups) fetch_b(at_a);
+                if (kAhead > 1 ? h == kGroups + 1 : h == kGroups) fetch_a(at_b);
+            }
+            at_a = next_a;
+            at_b = next_b;
+        } while (more);
+        e.template finish<kMT, kNT>(acc, at);
+        out.items.next();
+        out.enter(a.k, a.slices, kStep);
+    }
+    // (LDS is this workgroup's until all that was sent for has come)
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+}
+
+// Whether an operand can go straight to LDS: rows at multiples of 16 bytes, offsets within a
+// tile in 31 bits, and `along` k whole pieces.
+inline bool direct(const void* p, int64_t ld, int64_t esize, int64_t along) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * esize % 16 == 0 &&
+           along * esize % 16 == 0 && ld * esize < int64_t(1) << 23;
+}
+
+// ---- epilogues ---------------------------------------------------------------
+
+// The lane, worked out where it is asked for: what an epilogue derives from it would
+// otherwise be held in registers through the products.
+__device__ __forceinline__ int lane_here() {
+    int lane = static_cast<int>(threadIdx.x) % kWave;
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
+// A lane's sums as groups of eight neighbours: group p of 2 MT, from row eight_at(p) on.
+__device__ __forceinline__ int eight_at(int p, int lane) {
+    return p / 2 * 32 + lane / 32 * 16 + p % 2 * 8;
+}
+template <int MT, int NT>
+__device__ __forceinline__ void eight(const f32x16 (&acc)[MT][NT], int p, int u, float* v) {
+    for (int i = 0; i < 8; ++i) v[i] = acc[p / 2][u][p % 2 * 8 + i];
 }
 
 // C written out, a row of M for each n.
-template <typename Y> struct StoreTile : NoSteps {
+template <typename Y> struct StoreTile {
     Y* y;
     int64_t ld;
     StoreTile(void* to, int64_t l) : y(static_cast<Y*>(to)), ld(l) {}
     template <int MT, int NT>
-    __device__ __forceinline__ void finish(const f32x4 (&acc)[MT][NT], const Place& at) const {
-        const int lane = threadIdx.x % kWave;
+    __device__ __forceinline__ void finish(const f32x16 (&acc)[MT][NT], const Place& at) const {
+        const int lane = lane_here();
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
-            const int64_t n = at.n0 + u * 16 + lane % 16;
+            const int64_t n = at.n0 + u * kSquare + lane % kSquare;
             if (n >= at.n) continue;
-            for (int p = 0; p < MT / 2; ++p) {
+#pragma unroll
+            for (int p = 0; p < 2 * MT; ++p) {
                 float v[8];
                 eight(acc, p, u, v);
-                store8(y + n * ld, at.m0 + p * 32 + lane / 16 * 8, at.m, v);
+                store8(y + n * ld, at.m0 + eight_at(p, lane), at.m, v);
             }
         }
     }
