@@ -177,7 +177,7 @@ template <class Via, bool ACROSS, int ROWS, bool FIRST, int STEP_BYTES> struct S
     struct Direct {
         const uint8_t *matrix, *base;     // base: of the step, the same for all lanes
         uint32_t offset[kMine];           // of this thread's pieces, in bytes
-        int64_t row_bytes;
+        int row_bytes;
         int lines, wide, edge;            // what is left (edge: bytes of a line that is across k)
 
         static __device__ __forceinline__ int piece() {
@@ -188,9 +188,9 @@ template <class Via, bool ACROSS, int ROWS, bool FIRST, int STEP_BYTES> struct S
         __device__ __forceinline__ void start(const void* p, int64_t ld) {
             matrix = base = static_cast<const uint8_t*>(p);
             edge = 0;
-            row_bytes = ld * static_cast<int64_t>(sizeof(T));
+            row_bytes = static_cast<int>(ld * static_cast<int64_t>(sizeof(T)));
             for (int j = 0; j < kMine; ++j)
-                offset[j] = static_cast<uint32_t>((threadIdx.x / kLine + j * kApart) * row_bytes) +
+                offset[j] = (threadIdx.x / kLine + j * kApart) * static_cast<uint32_t>(row_bytes) +
                             piece() * 16;
         }
         __device__ __forceinline__ void enter(int64_t row0, int64_t rows, int64_t k0, int64_t k1) {
@@ -199,20 +199,26 @@ template <class Via, bool ACROSS, int ROWS, bool FIRST, int STEP_BYTES> struct S
             base = matrix +
                    (ACROSS ? k0 * row_bytes + row0 * static_cast<int64_t>(sizeof(T))
                            : row0 * row_bytes + k0 * static_cast<int64_t>(sizeof(T)));
+            // (edge is at most row_bytes)
             lines = static_cast<int>(ACROSS ? k : r);
             wide = static_cast<int>(k);
             edge = static_cast<int>(r * static_cast<int64_t>(sizeof(T)) + 15) / 16 * 16;
         }
         // Nothing more to load: zeros from here on.
-        __device__ __forceinline__ void stop() { lines = wide = 0; }
+        __device__ __forceinline__ void stop() {
+            lines = ACROSS ? 0 : 1;
+            wide = 0;
+        }
         __device__ __forceinline__ void load(uint8_t* lds) {
             typedef __attribute__((address_space(3))) void lds_any;
             uint8_t* to = lds + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * (kWave * 16);
-            // Bytes from the step's first to its last.
-            const int n = ACROSS ? (lines < kLines ? lines : kLines) : lines;
-            const int last = ACROSS ? edge : (wide < kStep ? wide : kStep) * static_cast<int>(sizeof(T));
+            // Bytes from the step's first to its last; 0 with no lines left.
+            constexpr int kSize = static_cast<int>(sizeof(T));
+            const int n = lines < kLines ? lines : kLines, w = wide < kStep ? wide : kStep;
+            const int across = (n - 1) * row_bytes + edge;
             const uint32_t bytes =
-                n <= 0 || last <= 0 ? 0 : static_cast<uint32_t>((n - 1) * row_bytes) + ((last + 15) & ~15);
+                ACROSS ? (across > 0 ? across : 0)
+                       : static_cast<uint32_t>(n - 1) * static_cast<uint32_t>(row_bytes) + (w * kSize + 15) / 16 * 16;
             __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
                 const_cast<uint8_t*>(base), 0, bytes, 0x00020000);
             for (int j = 0; j < kMine; ++j) {
@@ -221,7 +227,7 @@ template <class Via, bool ACROSS, int ROWS, bool FIRST, int STEP_BYTES> struct S
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_any*)(to + j * (kTileThreads * 16)),
                                                          16, o, 0, 0, 0);
             }
-            base += ACROSS ? kStep * row_bytes : kStep * static_cast<int64_t>(sizeof(T));
+            base += ACROSS ? kStep * static_cast<int64_t>(row_bytes) : kStep * kSize;
             if (ACROSS) lines -= kStep;
             else wide -= kStep;
         }
@@ -295,31 +301,30 @@ __device__ __forceinline__ int64_t scalar(int64_t v) {
 // longer side past its last whole tile comes at the end, dealt over all XCDs, so that it
 // does not cost a whole turn more.  (Fewer than 2^31 items: 32 bits count them.)
 struct Items {
-    int few, many, all, run, at, end, step;
+    int few, many, each, run, end, len;   // len: of k, a slice
     bool n_short;
 
-    __device__ Items(int64_t m, int64_t n, int tm, int tn, int slices) {
-        const int m_tiles = static_cast<int>((m + tm - 1) / tm);
-        const int n_tiles = static_cast<int>((n + tn - 1) / tn);
+    __device__ Items(int m, int n, int k, int tm, int tn, int slices, int step_k) {
+        const int m_tiles = (m + tm - 1) / tm, n_tiles = (n + tn - 1) / tn;
         n_short = n_tiles <= m_tiles;
         few = n_short ? n_tiles : m_tiles;
-        many = static_cast<int>(n_short ? m / tm : n / tn);
-        all = few * many * slices;
+        many = n_short ? m / tm : n / tn;
+        const int all = few * many * slices;
         const int edge = few * ((n_short ? m_tiles : n_tiles) - many) * slices;
         const int x = blockIdx.x % 8;
-        const int each = (all + 7) / 8, from = each * x < all ? each * x : all;
+        each = (all + 7) / 8;
+        const int from = each * x < all ? each * x : all;
         run = all - from < each ? all - from : each;
-        step = gridDim.x / 8;
-        at = blockIdx.x / 8;
         end = run + (edge + 7 - x) / 8;
+        len = scalar(((k + slices - 1) / slices + step_k - 1) / step_k * step_k);
     }
-    __device__ bool left() const { return at < end; }
-    __device__ void next() { at += step; }
-    __device__ void place(int* mt, int* nt, int* slice) const {
+    static __device__ int first() { return blockIdx.x / 8; }
+    static __device__ int step() { return gridDim.x / 8; }
+    __device__ void place(int at, int* mt, int* nt, int* slice) const {
         const int x = blockIdx.x % 8;
         int s, l;
         if (at < run) {
-            const int each = (all + 7) / 8, i = each * x + at, tiles = few * many;
+            const int i = each * x + at, tiles = few * many;
             *slice = i / tiles;
             const int t = i % tiles, band = t / (8 * many), in = t % (8 * many);
             const int wide = few - band * 8 < 8 ? few - band * 8 : 8;
@@ -335,24 +340,21 @@ struct Items {
         *mt = scalar(n_short ? l : s);
         *nt = scalar(n_short ? s : l);
     }
+    // Steps of k of a slice: one at least, whose sums are then zeros.
+    __device__ int turns(int k, int slice, int step_k) const {
+        const int64_t left = k - static_cast<int64_t>(slice) * len;
+        const int n = left < len ? static_cast<int>(left) : len;
+        return n <= step_k ? 1 : (n + step_k - 1) / step_k;
+    }
 };
 
-// One workgroup's way through its items, `turns` steps of k each.
-struct Cursor {
-    Items items;
-    int mt, nt, slice, turns;
-    bool left;
-
-    __device__ void enter(int64_t k, int slices, int step) {
-        left = items.left();
-        if (!left) return;
-        items.place(&mt, &nt, &slice);
-        const int64_t len = length(k, slices, step), k0 = slice * len;
-        const int64_t n = k - k0 < len ? k - k0 : len;
-        turns = scalar(n <= step ? 1 : static_cast<int>((n + step - 1) / step));
-    }
-    static __device__ int64_t length(int64_t k, int slices, int step) {
-        return scalar(((k + slices - 1) / slices + step - 1) / step * step);
+// What the products are of, in 32 bits where these are enough (fewer than 2^31 items, rows
+// and columns): the loops below have few scalar registers to spare.
+struct Extent {
+    int m, n, k;
+    __device__ explicit Extent(const ProductArgs& a)
+        : m(static_cast<int>(a.m)), n(static_cast<int>(a.n)), k(static_cast<int>(a.k)) {
+        if (a.count != nullptr) (a.count_is_k ? k : n) = scalar(*a.count);
     }
 };
 
@@ -457,34 +459,31 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product(ProductArgs a, Epil
     __shared__ __attribute__((aligned(128))) uint8_t lds[2][SideA::kBytes + SideB::kBytes];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wm = wave / WN * (TM / WM), wn = wave % WN * (TN / WN);
-    if (a.count != nullptr) {
-        const int n = scalar(*a.count);
-        if (a.count_is_k) a.k = n;
-        else a.n = n;
-    }
-    Cursor in{Items(a.m, a.n, TM, TN, a.slices), 0, 0, 0, 0, false};
-    in.enter(a.k, a.slices, kStep);
-    Cursor out = in;
+    const Extent x(a);
+    const Items items(x.m, x.n, x.k, TM, TN, a.slices, kStep);
+    int in_at = Items::first(), in_turns = 0;
     SideA sa;
     SideB sb;
     auto aim = [&] {
-        if (!in.left) return;
-        const int64_t n = Cursor::length(a.k, a.slices, kStep), k0 = in.slice * n;
-        const int64_t k1 = k0 + n < a.k ? k0 + n : a.k;
-        sa.enter(a.a, a.lda, static_cast<int64_t>(in.mt) * TM, a.m, k0, k1);
-        sb.enter(a.b, a.ldb, static_cast<int64_t>(in.nt) * TN, a.n, k0, k1);
+        if (in_at >= items.end) return;
+        int mt, nt, slice;
+        items.place(in_at, &mt, &nt, &slice);
+        in_turns = items.turns(x.k, slice, kStep);
+        const int64_t k0 = static_cast<int64_t>(slice) * items.len;
+        const int64_t k1 = k0 + items.len < x.k ? k0 + items.len : x.k;
+        sa.enter(a.a, a.lda, static_cast<int64_t>(mt) * TM, x.m, k0, k1);
+        sb.enter(a.b, a.ldb, static_cast<int64_t>(nt) * TN, x.n, k0, k1);
     };
     aim();
     // The step at `in` into registers; then on to the next one.
     bool held = false;
     auto fetch = [&] {
-        held = in.left;
+        held = in_at < items.end;
         if (!held) return;
         sa.load();
         sb.load();
-        if (--in.turns == 0) {
-            in.items.next();
-            in.enter(a.k, a.slices, kStep);
+        if (--in_turns == 0) {
+            in_at += Items::step();
             aim();
         }
     };
@@ -498,10 +497,13 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product(ProductArgs a, Epil
     put(lds[0]);
     fetch();
     __syncthreads();
-    while (out.left) {
+    for (int item = Items::first(); item < items.end; item += Items::step()) {
+        int mt, nt, slice;
+        items.place(item, &mt, &nt, &slice);
+        int turns = items.turns(x.k, slice, kStep);
         f32x16 acc[kMT][kNT] = {};
-        const Place at{static_cast<int64_t>(out.mt) * TM + wm,
-                       static_cast<int64_t>(out.nt) * TN + wn, a.m, a.n, out.slice};
+        const Place at{static_cast<int64_t>(mt) * TM + wm, static_cast<int64_t>(nt) * TN + wn, x.m,
+                       x.n, slice};
         Made made;
         made.enter(e, at);
         typename Made::A va[kAhead + 1];
@@ -509,11 +511,9 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product(ProductArgs a, Epil
         vb[0] = made.template read_b<SideB>(lds[buf] + SideA::kBytes, wn, 0);
 #pragma unroll
         for (int g = 0; g < kAhead; ++g) va[g] = made.template read_a<SideA>(lds[buf], wm, g % kMT, g / kMT);
-        bool more;
 #pragma clang loop unroll(disable)
         do {
             const uint8_t *l = lds[buf], *next = lds[buf ^ 1];
-            more = --out.turns > 0;
             made.step();
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) {
@@ -536,10 +536,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product(ProductArgs a, Epil
                 __builtin_amdgcn_sched_barrier(0);
             }
             buf ^= 1;
-        } while (more);
+        } while (--turns > 0);
         e.template finish<kMT, kNT>(acc, at);
-        out.items.next();
-        out.enter(a.k, a.slices, kStep);
     }
 }
 
@@ -569,48 +567,47 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_direct(ProductArgs 
     __shared__ __attribute__((aligned(128))) uint8_t lds[kUnits * kUnitBytes];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wm = wave / WN * (TM / WM), wn = wave % WN * (TN / WN);
-    if (a.count != nullptr) {
-        const int n = scalar(*a.count);
-        if (a.count_is_k) a.k = n;
-        else a.n = n;
-    }
-    Cursor out{Items(a.m, a.n, TM, TN, a.slices), 0, 0, 0, 0, false};
-    out.enter(a.k, a.slices, kStep);
-    Cursor in_a = out, in_b = out;
+    const Extent x(a);
+    const Items items(x.m, x.n, x.k, TM, TN, a.slices, kStep);
     typename SideA::Direct sa;
     typename SideB::Direct sb;
     sa.start(a.a, a.lda);
     sb.start(a.b, a.ldb);
-    auto aim = [&](Cursor& in, auto& side, int tile, int64_t rows) {
-        if (in.left) {
-            const int64_t n = Cursor::length(a.k, a.slices, kStep), k0 = in.slice * n;
-            side.enter(static_cast<int64_t>(tile), rows, k0, k0 + n < a.k ? k0 + n : a.k);
+    // To the item at `at`, for one side.
+    auto aim = [&](int at, auto& side, bool first) {
+        int turns = INT32_MAX;
+        if (at < items.end) {
+            int mt, nt, slice;
+            items.place(at, &mt, &nt, &slice);
+            turns = items.turns(x.k, slice, kStep);
+            const int64_t k0 = static_cast<int64_t>(slice) * items.len;
+            const int64_t k1 = k0 + items.len < x.k ? k0 + items.len : x.k;
+            if (first) side.enter(static_cast<int64_t>(mt) * TM, x.m, k0, k1);
+            else side.enter(static_cast<int64_t>(nt) * TN, x.n, k0, k1);
         } else {
             side.stop();
-            in.turns = INT32_MAX;
         }
         // (so that the compiler knows of no scalar load under way in the loop below, beside
         // which it could not count LDS reads)
         __builtin_amdgcn_s_waitcnt(0xC07F);
+        return turns;
     };
-    aim(in_a, sa, in_a.mt * TM, a.m);
-    aim(in_b, sb, in_b.nt * TN, a.n);
+    int a_at = Items::first(), b_at = a_at;
+    int a_turns = aim(a_at, sa, true), b_turns = aim(b_at, sb, false);
+    // On to the next items where that is due: before a step's products, whose block of
+    // instructions is then not cut.
+    auto onward = [&] {
+        if (a_turns == 0) a_turns = aim(a_at += Items::step(), sa, true);
+        if (b_turns == 0) b_turns = aim(b_at += Items::step(), sb, false);
+    };
     // Sends for the next unit of an operand.
     auto fetch_a = [&](int place) {
         sa.load(lds + place);
-        if (--in_a.turns == 0) {
-            in_a.items.next();
-            in_a.enter(a.k, a.slices, kStep);
-            aim(in_a, sa, in_a.mt * TM, a.m);
-        }
+        --a_turns;
     };
     auto fetch_b = [&](int place) {
         sb.load(lds + place);
-        if (--in_b.turns == 0) {
-            in_b.items.next();
-            in_b.enter(a.k, a.slices, kStep);
-            aim(in_b, sb, in_b.nt * TN, a.n);
-        }
+        --b_turns;
     };
     auto after = [](int place, int units) {
         const int p = place + units * kUnitBytes;
@@ -627,15 +624,20 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_direct(ProductArgs 
     };
     fetch_a(0);
     fetch_b(kUnitBytes);
+    onward();
     fetch_a(2 * kUnitBytes);
     fetch_b(3 * kUnitBytes);
+    onward();
     fetch_a(4 * kUnitBytes);
     meet(Count<3>{});
     int at_a = 0, at_b = kUnitBytes;
-    while (out.left) {
+    for (int item = Items::first(); item < items.end; item += Items::step()) {
+        int mt, nt, slice;
+        items.place(item, &mt, &nt, &slice);
+        int turns = items.turns(x.k, slice, kStep);
         f32x16 acc[kMT][kNT] = {};
-        const Place at{static_cast<int64_t>(out.mt) * TM + wm,
-                       static_cast<int64_t>(out.nt) * TN + wn, a.m, a.n, out.slice};
+        const Place at{static_cast<int64_t>(mt) * TM + wm, static_cast<int64_t>(nt) * TN + wn, x.m,
+                       x.n, slice};
         Made made;
         made.enter(e, at);
         typename Made::A va[kAhead + 1];
@@ -644,24 +646,17 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_direct(ProductArgs 
 #pragma unroll
         for (int g = 0; g < kAhead; ++g)
             va[g] = made.template read_a<SideA>(lds + at_a, wm, g % kMT, g / kMT);
-        // An epilogue's loads and stores are counted with the units: all have to be in.
-        bool fresh = true, more;
-#pragma clang loop unroll(disable)
-        do {
-            more = --out.turns > 0;
+        auto turn = [&](auto first) {
+            onward();
             made.step();
             const int next_a = after(at_a, 2), next_b = after(at_b, 2);
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) {
                 const int sub = g / kMT, h = g + kAhead;
                 if (g % kMT == 0) made.take(vb[sub % Made::kSlots]);
-                if (h == kGroups) {
-                    if (fresh) {
-                        __builtin_amdgcn_s_waitcnt(0x0F70);
-                        fresh = false;
-                    }
-                    meet(Count<1>{});
-                }
+                // An epilogue's loads and stores are counted with the units: the first time
+                // after it all have to be in.
+                if (h == kGroups) meet(Count<decltype(first)::value ? 0 : 1>{});
                 // (after a tile's last step these are the next tile's, and not used)
                 if (h % kMT == 0)
                     vb[h / kMT % Made::kSlots] = made.template read_b<SideB>(
@@ -677,10 +672,11 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_direct(ProductArgs 
             }
             at_a = next_a;
             at_b = next_b;
-        } while (more);
+        };
+        turn(Count<1>{});
+#pragma clang loop unroll(disable)
+        while (--turns > 0) turn(Count<0>{});
         e.template finish<kMT, kNT>(acc, at);
-        out.items.next();
-        out.enter(a.k, a.slices, kStep);
     }
     // (LDS is this workgroup's until all that was sent for has come)
     __builtin_amdgcn_s_waitcnt(0x0F70);
