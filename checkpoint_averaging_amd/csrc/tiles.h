@@ -178,7 +178,8 @@ template <class Via, bool ACROSS, int ROWS, bool FIRST, int STEP_BYTES> struct S
         const uint8_t *matrix, *base;     // base: of the step, the same for all lanes
         uint32_t offset[kMine];           // of this thread's pieces, in bytes
         int row_bytes;
-        int lines, wide, edge;            // what is left (edge: bytes of a line that is across k)
+        uint32_t bound;                   // bytes of all rows, or of a line that is across k
+        int lines, wide;                  // what is left
 
         static __device__ __forceinline__ int piece() {
             const int c = threadIdx.x % kLine, l = threadIdx.x / kLine;
@@ -187,7 +188,7 @@ template <class Via, bool ACROSS, int ROWS, bool FIRST, int STEP_BYTES> struct S
         }
         __device__ __forceinline__ void start(const void* p, int64_t ld) {
             matrix = base = static_cast<const uint8_t*>(p);
-            edge = 0;
+            bound = 0;
             row_bytes = static_cast<int>(ld * static_cast<int64_t>(sizeof(T)));
             for (int j = 0; j < kMine; ++j)
                 offset[j] = (threadIdx.x / kLine + j * kApart) * static_cast<uint32_t>(row_bytes) +
@@ -199,26 +200,24 @@ template <class Via, bool ACROSS, int ROWS, bool FIRST, int STEP_BYTES> struct S
             base = matrix +
                    (ACROSS ? k0 * row_bytes + row0 * static_cast<int64_t>(sizeof(T))
                            : row0 * row_bytes + k0 * static_cast<int64_t>(sizeof(T)));
-            // (edge is at most row_bytes)
             lines = static_cast<int>(ACROSS ? k : r);
             wide = static_cast<int>(k);
-            edge = static_cast<int>(r * static_cast<int64_t>(sizeof(T)) + 15) / 16 * 16;
+            // (a line's bytes, whole pieces, are at most row_bytes)
+            bound = ACROSS ? static_cast<uint32_t>(r * static_cast<int64_t>(sizeof(T)) + 15) / 16 * 16
+                           : static_cast<uint32_t>(r) * static_cast<uint32_t>(row_bytes);
         }
         // Nothing more to load: zeros from here on.
-        __device__ __forceinline__ void stop() {
-            lines = ACROSS ? 0 : 1;
-            wide = 0;
-        }
-        __device__ __forceinline__ void load(uint8_t* lds) {
+        __device__ __forceinline__ void stop() { lines = wide = 0; }
+        __device__ __forceinline__ void load(uint8_t* lds, int wave) {
             typedef __attribute__((address_space(3))) void lds_any;
-            uint8_t* to = lds + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * (kWave * 16);
-            // Bytes from the step's first to its last; 0 with no lines left.
-            constexpr int kSize = static_cast<int>(sizeof(T));
-            const int n = lines < kLines ? lines : kLines, w = wide < kStep ? wide : kStep;
-            const int across = (n - 1) * row_bytes + edge;
-            const uint32_t bytes =
-                ACROSS ? (across > 0 ? across : 0)
-                       : static_cast<uint32_t>(n - 1) * static_cast<uint32_t>(row_bytes) + (w * kSize + 15) / 16 * 16;
+            uint8_t* to = lds + wave * (kWave * 16);
+            // Bytes from the step's first to its last (along k, to the end of its last row: the
+            // offsets see to the end of k).
+            uint32_t bytes = bound;
+            if constexpr (ACROSS) {
+                const int n = __builtin_elementwise_min(lines, kLines);
+                bytes = __builtin_elementwise_max((n - 1) * row_bytes + static_cast<int>(bound), 0);
+            }
             __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
                 const_cast<uint8_t*>(base), 0, bytes, 0x00020000);
             for (int j = 0; j < kMine; ++j) {
@@ -227,7 +226,8 @@ template <class Via, bool ACROSS, int ROWS, bool FIRST, int STEP_BYTES> struct S
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_any*)(to + j * (kTileThreads * 16)),
                                                          16, o, 0, 0, 0);
             }
-            base += ACROSS ? kStep * static_cast<int64_t>(row_bytes) : kStep * kSize;
+            base += ACROSS ? kStep * static_cast<int64_t>(row_bytes)
+                           : kStep * static_cast<int64_t>(sizeof(T));
             if (ACROSS) lines -= kStep;
             else wide -= kStep;
         }
@@ -293,6 +293,13 @@ __device__ __forceinline__ int64_t scalar(int64_t v) {
     return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
 }
 
+// A scalar as if it were new: what is derived from it (a division's reciprocal) is worked
+// out here each time, rather than held in registers through the loops.
+__device__ __forceinline__ int afresh(int v) {
+    asm volatile("" : "+s"(v));
+    return v;
+}
+
 // ---- the order of the tiles --------------------------------------------------
 
 // Workgroups are dealt to the eight XCDs in turn.  Each XCD takes a run of
@@ -324,16 +331,16 @@ struct Items {
         const int x = blockIdx.x % 8;
         int s, l;
         if (at < run) {
-            const int i = each * x + at, tiles = few * many;
+            const int i = each * x + at, tiles = afresh(few * many), eight = afresh(8 * many);
             *slice = i / tiles;
-            const int t = i % tiles, band = t / (8 * many), in = t % (8 * many);
+            const int t = i % tiles, band = t / eight, in = t % eight;
             const int wide = few - band * 8 < 8 ? few - band * 8 : 8;
             s = band * 8 + in % wide;
             l = in / wide;
         } else {
-            const int i = (at - run) * 8 + x;
-            *slice = i / few;
-            s = i % few;
+            const int i = (at - run) * 8 + x, each_slice = afresh(few);
+            *slice = i / each_slice;
+            s = i % each_slice;
             l = many;
         }
         *slice = scalar(*slice);
@@ -602,11 +609,11 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_direct(ProductArgs 
     };
     // Sends for the next unit of an operand.
     auto fetch_a = [&](int place) {
-        sa.load(lds + place);
+        sa.load(lds + place, wave);
         --a_turns;
     };
     auto fetch_b = [&](int place) {
-        sb.load(lds + place);
+        sb.load(lds + place, wave);
         --b_turns;
     };
     auto after = [](int place, int units) {
