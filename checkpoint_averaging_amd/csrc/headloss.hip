@@ -47,19 +47,19 @@ struct StatsTile {
         for (int u = 0; u < NT; ++u) {
             const int64_t n = at.n0 + u * kSquare + lane % kSquare;
             float v[kMine];
-            for (int p = 0; p < 2 * MT; ++p) eight(acc, p, u, v + 8 * p);
-            // element q of v is token m0 + 32 (q/16) + 16 (lane/32) + q%16
-            const int first = lane / 32 * 16;
+            for (int q = 0; q < kMine; ++q) v[q] = in_run(acc, q / 32, u, q % 32);
+            // element q of v is token m0 + 64 (q/32) + 32 (lane/32) + q%32
+            const int first = lane / 32 * 32;
             if (left < MT * 32)
                 for (int q = 0; q < kMine; ++q)
-                    if (q / 16 * 32 + first + q % 16 >= left) v[q] = -__builtin_inff();
+                    if (q / 32 * 64 + first + q % 32 >= left) v[q] = -__builtin_inff();
             if (targets != nullptr) {
                 const int64_t t = n < at.n ? targets[n] - at.m0 : -1;
-                const bool mine = t >= 0 && t < MT * 32 && t < left && t / 16 % 2 == lane / 32;
+                const bool mine = t >= 0 && t < MT * 32 && t < left && t / 32 % 2 == lane / 32;
                 if (__any(mine)) {
                     float l = 0;
                     for (int q = 0; q < kMine; ++q)
-                        if (q / 16 * 32 + first + q % 16 == t) l = v[q];
+                        if (q / 32 * 64 + first + q % 32 == t) l = v[q];
                     if (mine) at_target[n] = l;
                 }
             }
@@ -221,6 +221,8 @@ struct GatherArgs {
     void* to;
     int64_t ldto;
     RowTerms* terms;
+    void* p;                              // dlogits of a piece, and where its last one's rows end
+    int64_t ldp, p_end;
 };
 
 template <typename T> __global__ __launch_bounds__(256) void k_gather(GatherArgs a) {
@@ -234,6 +236,9 @@ template <typename T> __global__ __launch_bounds__(256) void k_gather(GatherArgs
             load8(from, c, a.width, v);
             store8(to, c, a.width, v);
         }
+        // (zeros up to a multiple of 8: the products with dlogits read that far)
+        if (threadIdx.x < 8 && a.p_end + threadIdx.x < a.ldp)
+            static_cast<T*>(a.p)[j * a.ldp + a.p_end + threadIdx.x] = from_f32<T>(0.0f);
         if (threadIdx.x == 0) {
             const int64_t t = a.targets[row];
             RowTerms r{};
@@ -262,36 +267,30 @@ template <typename T, bool ENTROPY> struct GradTile {
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
             const int64_t n = at.n0 + u * kSquare + lane % kSquare;
-            if (n >= at.n) continue;
-            const RowTerms r = terms[n];
-            const int64_t t = r.target < 0 ? -1 : r.target - first - at.m0;
-            const bool hot = t >= 0 && t < MT * 32 && t / 16 % 2 == lane / 32;
+            const RowTerms r = terms[n < at.n ? n : at.n - 1];
+            const int64_t far = r.target - first - at.m0;
+            const int t = r.target < 0 || far < 0 || far >= MT * 32 ? -1 : static_cast<int>(far);
             // (a row of masked tokens only: their log probabilities are the logits)
             const float from = r.m == -__builtin_inff() ? 0.0f : r.m;
-            auto entropy_part = [&](float x, float lp) {
-                return ENTROPY && x > 0 ? r.b * x * (lp + r.entropy) : 0.0f;
+            auto gradient = [&](float l, bool target) {
+                const float lp = (l - from) - r.log_s, x = exp_of(lp);
+                const float h = ENTROPY && x > 0 ? r.b * x * (lp + r.entropy) : 0.0f;
+                // (1 - p of the target keeps its digits)
+                return x != x ? x : -r.a * (target ? expm1f(lp) : x) - h;
             };
-            float at_target = 0;
 #pragma unroll
-            for (int p = 0; p < 2 * MT; ++p) {
-                const int mine = eight_at(p, lane);
-                float v[8];
-                eight(acc, p, u, v);
-                for (int q = 0; q < 8; ++q) {
-                    const float lp = (v[q] - from) - r.log_s, x = exp_of(lp);
-                    if (t == mine + q) at_target = lp;
-                    v[q] = x != x ? x : -r.a * x - entropy_part(x, lp);
+            for (int p = 0; p < kRuns<MT>; ++p) {
+                const int mine = run_at<MT>(p, lane);
+                float of_target = 0;
+                if (__any(t >= mine && t < mine + 32)) {
+                    float l = 0;
+                    for (int i = 0; i < 32; ++i) l = t == mine + i ? in_run(acc, p, u, i) : l;
+                    of_target = gradient(l, true);
                 }
-                // (zeros up to a multiple of 8: the next products read that far)
-                const int64_t c = at.m0 + mine;
-                if (c + 8 > at.m)
-                    for (int q = 0; q < 8; ++q) v[q] = c + q < at.m ? v[q] : 0.0f;
-                store8(out + n * ld, c, (at.m + 7) / 8 * 8, v);
-            }
-            if (hot && at.m0 + t < at.m) {
-                const float x = exp_of(at_target);
-                out[n * ld + at.m0 + t] = from_f32<T>(
-                    x != x ? x : -r.a * expm1f(at_target) - entropy_part(x, at_target));
+                write_run<32, false>(out, ld, n, at.n, at.m0 + mine, at.m, lane, [&](int i) {
+                    const float d = gradient(in_run(acc, p, u, i), false);
+                    return t == mine + i ? of_target : d;
+                });
             }
         }
     }
@@ -307,24 +306,17 @@ struct SumTile {
     template <int MT, int NT>
     __device__ __forceinline__ void finish(const f32x16 (&acc)[MT][NT], const Place& at) const {
         const int lane = lane_here();
+        float* to = sums + at.slice * rows * ld;
 #pragma unroll
-        for (int u = 0; u < NT; ++u) {
-            const int64_t n = at.n0 + u * kSquare + lane % kSquare;
-            if (n >= at.n) continue;
-            float* row = sums + (at.slice * rows + n) * ld;
+        for (int u = 0; u < NT; ++u)
 #pragma unroll
-            for (int p = 0; p < 2 * MT; ++p) {
-                const int64_t c = at.m0 + eight_at(p, lane);
-                float v[8];
-                eight(acc, p, u, v);
-                if (!first) {
-                    float w[8];
-                    load8(row, c, at.m, w);
-                    for (int i = 0; i < 8; ++i) v[i] += w[i];
-                }
-                store8(row, c, at.m, v);
+            for (int p = 0; p < kRuns<MT>; ++p) {
+                const int64_t n = at.n0 + u * kSquare + lane % kSquare;
+                const int64_t m = at.m0 + run_at<MT>(p, lane);
+                auto value = [&](int i) { return in_run(acc, p, u, i); };
+                if (first) write_run<32, false>(to, ld, n, at.n, m, at.m, lane, value);
+                else write_run<32, true>(to, ld, n, at.n, m, at.m, lane, value);
             }
-        }
     }
 };
 
@@ -457,7 +449,8 @@ template <typename T> hipError_t backward(const HeadBackwardArgs& a, hipStream_t
     const unsigned walkers = static_cast<unsigned>(a.rows < 2048 ? a.rows : 2048);
     const GatherArgs g{a.x,       a.ldx,      a.rows, a.vocab, static_cast<int>(a.width),
                        a.targets, a.stats,    a.entropy, a.dlogprobs, a.dentropy,
-                       index,     count,      x,      b.ld_x,  terms};
+                       index,     count,      x,      b.ld_x,  terms,
+                       p,         b.ld_p,     a.vocab - (b.pieces - 1) * b.piece};
     k_gather<T><<<dim3(walkers), dim3(256), 0, s>>>(g);
     if ((st = hipGetLastError()) != hipSuccess) return st;
     for (int64_t i = 0; i < b.pieces; ++i) {

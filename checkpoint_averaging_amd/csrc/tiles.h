@@ -78,8 +78,8 @@ struct ViaCodes {                        // e4m3 codes
 };
 
 // One operand's side of a step: ROWS rows (m or n) by STEP_BYTES of each along k.
-// FIRST: operand A, whose rows a lane's sums run along (see m_row below).
-template <class Via, bool ACROSS, int ROWS, bool FIRST, int STEP_BYTES> struct Side {
+// FIRST: operand A, whose rows a lane's sums run along (see m_row below; PAIRS: over two tiles).
+template <class Via, bool ACROSS, int ROWS, bool FIRST, bool PAIRS, int STEP_BYTES> struct Side {
     typedef typename Via::elem T;
     static constexpr int kPer = 16 / static_cast<int>(sizeof(T));
     static constexpr int kStep = STEP_BYTES / static_cast<int>(sizeof(T));
@@ -237,18 +237,25 @@ template <class Via, bool ACROSS, int ROWS, bool FIRST, int STEP_BYTES> struct S
 
     // The 16-byte piece of row `row` that holds its piece c is at piece c ^ key(row).  A
     // 128-bit read takes 16 lanes at a time, 0-3 12-15 20-23 24-27 and 4-7 8-11 16-19 28-31 of
-    // each 32: with the keys, and with A's order of rows too, they meet 64 different banks.
+    // each 32: with the keys, and with A's orders of rows too, they meet 64 different banks.
     static __device__ __forceinline__ int key(int row) {
-        return kRowBytes == 128 ? (row >> 1 & 1) | (row >> 3 & 3) << 1 : row >> 3 & 3;
+        const int four = FIRST && PAIRS ? row >> 2 & 3 : row >> 3 & 3;
+        return kRowBytes == 128 ? (row >> 1 & 1) | four << 1 : four;
     }
-    // Across k, four lines of 64 (A) or 32 (B) bytes are read together.
-    static __device__ __forceinline__ int key_across(int k) { return (k & 3) << (FIRST ? 6 : 5); }
+    // Across k, 32 lanes read 8 bytes of four lines, two halves of a 64-byte window in each, or
+    // with PAIRS two of 32 bytes, 64 apart.
+    static __device__ __forceinline__ int key_across(int k) {
+        return FIRST && PAIRS ? (k & 1) << 5 | (k & 2) << 6 : (k & 3) << 6;
+    }
 
     // The matrix instruction leaves a lane rows 8 i + 4 (lane/32) .. + 3 of its column.  The
-    // first operand's rows in the order that makes them 16 neighbours: row r is row
-    // 16 (r/4%2) + 4 (r/8) + r%4.
-    static __device__ __forceinline__ int m_row(int r) {
-        return FIRST ? 16 * (r / 4 % 2) + 4 * (r / 8) + r % 4 : r;
+    // first operand's rows in the order that makes them 16 neighbours, or 32 in a pair of
+    // tiles: row r of tile t is this one of the wave's.
+    static __device__ __forceinline__ int m_row(int t, int r) {
+        if constexpr (!FIRST) return t * 32 + r;
+        if constexpr (PAIRS)
+            return t / 2 * 64 + t % 2 * 16 + r / 4 % 2 * 32 + 4 * (r / 8) + r % 4;
+        return t * 32 + r / 4 % 2 * 16 + 4 * (r / 8) + r % 4;
     }
 
     // 8 elements of k for each lane: row `lane % 32` of 32-row tile t of the rows from row0
@@ -256,14 +263,15 @@ template <class Via, bool ACROSS, int ROWS, bool FIRST, int STEP_BYTES> struct S
     static __device__ __forceinline__ bf16x8 frag(const uint8_t* lds, int row0, int t, int sub) {
         const int lane = threadIdx.x % kWave;
         if constexpr (!ACROSS) {
-            const int row = m_row(lane % 32);
+            // (the key is that of tile 0's row: 16, 32 or 64 rows further on it is the same)
+            const int row = m_row(0, lane % 32);
             return *reinterpret_cast<const bf16x8*>(
-                lds + (row0 + t * 32) * kRowBytes + row * kRowBytes +
+                lds + (row0 + m_row(t, 0)) * kRowBytes + row * kRowBytes +
                 ((sub * 2 + lane / 32) ^ key(row)) * 16);
         } else {
             // (lane 4 i + j of 16 gives the place of columns 4 j .. 4 j + 3 of line i, and gets
             // column 4 i + j of the four lines)
-            const int row = row0 + t * 32 + m_row(lane / 16 % 2 * 16 + 4 * (lane % 4));
+            const int row = row0 + m_row(t, lane / 16 % 2 * 16 + 4 * (lane % 4));
             const int k = 16 * sub + 8 * (lane / 32) + lane % 16 / 4;
             const int from = k * kRowBytes + ((row * 2) ^ key_across(k));
             typedef __attribute__((address_space(3))) i16x4 lds4;
@@ -279,9 +287,9 @@ template <class Via, bool ACROSS, int ROWS, bool FIRST, int STEP_BYTES> struct S
 
     // Piece `c` of each lane's row of codes.
     static __device__ __forceinline__ u32x4 codes(const uint8_t* lds, int row0, int t, int c) {
-        const int row = m_row(threadIdx.x % 32);
-        return *reinterpret_cast<const u32x4*>(lds + (row0 + t * 32) * kRowBytes + row * kRowBytes +
-                                               (c ^ key(row)) * 16);
+        const int row = m_row(0, threadIdx.x % 32);
+        return *reinterpret_cast<const u32x4*>(lds + (row0 + m_row(t, 0)) * kRowBytes +
+                                               row * kRowBytes + (c ^ key(row)) * 16);
     }
 };
 
@@ -375,8 +383,9 @@ inline unsigned product_grid(int64_t m, int64_t n, int tm, int tn, int slices, i
 
 // ---- the product -------------------------------------------------------------
 
-// Where a wave's sums are: element i of acc[t][u] is C[n][m] with
-//   m = m0 + 32 t + 16 (lane/32) + i,   n = n0 + 32 u + lane%32.
+// Where a wave's sums are: element i of acc[t][u] is C[n][m] with n = n0 + 32 u + lane%32 and
+//   m = m0 + 64 (t/2) + 32 (lane/32) + 16 (t%2) + i       (pairs of tiles), or
+//   m = m0 + 16 (lane/32) + i                             (one tile a wave).
 struct Place {
     int64_t m0, n0;                       // of the wave
     int64_t m, n;                         // ends of the product
@@ -456,8 +465,8 @@ template <class Via, bool SA, bool SB, int TM, int TN, int WM, int WN, class Epi
 __global__ __launch_bounds__(kTileThreads, 2) void k_product(ProductArgs a, Epilogue e) {
     static_assert(WM * WN == kTileWaves, "");
     constexpr int kMT = TM / WM / kSquare, kNT = TN / WN / kSquare;
-    typedef Side<Via, SA, TM, true, kStepBytes> SideA;
-    typedef Side<Via, SB, TN, false, kStepBytes> SideB;
+    typedef Side<Via, SA, TM, true, kMT % 2 == 0, kStepBytes> SideA;
+    typedef Side<Via, SB, TN, false, false, kStepBytes> SideB;
     // (a sub-step is 32 bytes of what LDS holds)
     typedef Math<Epilogue, kMT, kNT, SideA::kStep * SideA::kHeld / 32> Made;
     constexpr int kStep = SideA::kStep, kGroups = Made::kSubs * kMT, kAhead = Made::kAhead;
@@ -563,8 +572,8 @@ template <class Via, bool SA, bool SB, int TM, int TN, int WM, int WN, class Epi
 __global__ __launch_bounds__(kTileThreads, 2) void k_product_direct(ProductArgs a, Epilogue e) {
     static_assert(WM * WN == kTileWaves, "");
     constexpr int kMT = TM / WM / kSquare, kNT = TN / WN / kSquare;
-    typedef Side<Via, SA, TM, true, kStepBytes> SideA;
-    typedef Side<Via, SB, TN, false, kStepBytes> SideB;
+    typedef Side<Via, SA, TM, true, kMT % 2 == 0, kStepBytes> SideA;
+    typedef Side<Via, SB, TN, false, false, kStepBytes> SideB;
     typedef Math<Epilogue, kMT, kNT, 4> Made;
     constexpr int kStep = SideA::kStep, kGroups = Made::kSubs * kMT, kAhead = Made::kAhead;
     constexpr int kLoads = SideA::kMine;                             // of a unit, each thread's
@@ -706,13 +715,86 @@ __device__ __forceinline__ int lane_here() {
     return lane;
 }
 
-// A lane's sums as groups of eight neighbours: group p of 2 MT, from row eight_at(p) on.
-__device__ __forceinline__ int eight_at(int p, int lane) {
-    return p / 2 * 32 + lane / 32 * 16 + p % 2 * 8;
+// A lane's sums of column u as runs of neighbours: run p of MT/2 (32 each), or the one of 16,
+// from row run_at(p) on.
+template <int MT> constexpr int kRun = MT == 1 ? 16 : 32;
+template <int MT> constexpr int kRuns = MT == 1 ? 1 : MT / 2;
+template <int MT> __device__ __forceinline__ int run_at(int p, int lane) {
+    return MT == 1 ? lane / 32 * 16 : p * 64 + lane / 32 * 32;
 }
 template <int MT, int NT>
-__device__ __forceinline__ void eight(const f32x16 (&acc)[MT][NT], int p, int u, float* v) {
-    for (int i = 0; i < 8; ++i) v[i] = acc[p / 2][u][p % 2 * 8 + i];
+__device__ __forceinline__ float in_run(const f32x16 (&acc)[MT][NT], int p, int u, int i) {
+    return acc[p * 2 + i / 16][u][i % 16];
+}
+
+// Four 16-byte pieces of each of four neighbouring lanes, exchanged: lane j gets as its piece s
+// piece j of lane s.
+__device__ __forceinline__ void exchange(u32x4 (&c)[4], int lane) {
+    auto swap = [](u32x4& low, u32x4& high, bool upper, auto other) {
+        for (int d = 0; d < 4; ++d) {
+            const uint32_t t = other(upper ? low[d] : high[d]);
+            low[d] = upper ? t : low[d];
+            high[d] = upper ? high[d] : t;
+        }
+    };
+    auto next = [](uint32_t v) { return dpp<0xB1>(v); };                 // lanes 1 0 3 2
+    auto second = [](uint32_t v) { return dpp<0x4E>(v); };               // lanes 2 3 0 1
+    swap(c[0], c[1], lane & 1, next);
+    swap(c[2], c[3], lane & 1, next);
+    swap(c[0], c[2], lane & 2, second);
+    swap(c[1], c[3], lane & 2, second);
+}
+
+// A run of N of a lane's values, value(0) ..., into row n of C, from column m on.  Lanes hold a
+// row each, and 64 bytes of it are four lanes' business: they exchange pieces, so that each
+// store is of whole 64-byte segments (a lane's own 16 bytes at a time, four times the
+// requests, took up to a quarter of the products' time).  ADD: to what is there before.
+template <int N, bool ADD, typename Y, class Value>
+__device__ __forceinline__ void write_run(Y* y, int64_t ld, int64_t n, int64_t n_end, int64_t m,
+                                          int64_t m_end, int lane, Value value) {
+    constexpr int kPer = 16 / static_cast<int>(sizeof(Y));
+    if (N % (4 * kPer) == 0 && __all(m + N <= m_end)) {
+        Y* at = y + (n - lane % 4) * ld + m + lane % 4 * kPer;
+#pragma unroll
+        for (int q = 0; q < N / (4 * kPer); ++q) {
+            u32x4 c[4];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                float w[kPer];
+                for (int i = 0; i < kPer; ++i) w[i] = value((4 * q + s) * kPer + i);
+                c[s] = __builtin_bit_cast(u32x4, Vec<Y>::pack(w));
+                __builtin_amdgcn_sched_barrier(0);          // (few values at a time in registers)
+            }
+            exchange(c, lane);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                if (n - lane % 4 + s >= n_end) continue;
+                Y* to = at + s * ld + 4 * q * kPer;
+                if constexpr (ADD) {
+                    float a[kPer], b[kPer];
+                    Vec<Y>::unpack(Vec<Y>::load(to), a);
+                    Vec<Y>::unpack(__builtin_bit_cast(typename Vec<Y>::raw, c[s]), b);
+                    for (int i = 0; i < kPer; ++i) a[i] += b[i];
+                    Vec<Y>::store(to, Vec<Y>::pack(a));
+                } else {
+                    Vec<Y>::store(to, __builtin_bit_cast(typename Vec<Y>::raw, c[s]));
+                }
+            }
+        }
+        return;
+    }
+    if (n >= n_end) return;
+#pragma unroll
+    for (int i = 0; i < N; i += 8) {
+        float w[8];
+        for (int k = 0; k < 8; ++k) w[k] = value(i + k);
+        if (ADD) {
+            float a[8];
+            load8(y + n * ld, m + i, m_end, a);
+            for (int k = 0; k < 8; ++k) w[k] += a[k];
+        }
+        store8(y + n * ld, m + i, m_end, w);
+    }
 }
 
 // C written out, a row of M for each n.
@@ -724,16 +806,12 @@ template <typename Y> struct StoreTile {
     __device__ __forceinline__ void finish(const f32x16 (&acc)[MT][NT], const Place& at) const {
         const int lane = lane_here();
 #pragma unroll
-        for (int u = 0; u < NT; ++u) {
-            const int64_t n = at.n0 + u * kSquare + lane % kSquare;
-            if (n >= at.n) continue;
+        for (int u = 0; u < NT; ++u)
 #pragma unroll
-            for (int p = 0; p < 2 * MT; ++p) {
-                float v[8];
-                eight(acc, p, u, v);
-                store8(y + n * ld, at.m0 + eight_at(p, lane), at.m, v);
-            }
-        }
+            for (int p = 0; p < kRuns<MT>; ++p)
+                write_run<kRun<MT>, false>(y, ld, at.n0 + u * kSquare + lane % kSquare, at.n,
+                                           at.m0 + run_at<MT>(p, lane), at.m, lane,
+                                           [&](int i) { return in_run(acc, p, u, i); });
     }
 };
 
