@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include "dlhead.h"
+#include "few.h"
 #include "head.h"
 #include "head_device.h"
 #include "tiles.h"
@@ -232,11 +233,38 @@ template <class Epilogue, int MT, int NT, int SUBS> struct ExactCodeMath : Scale
     }
 };
 
+// A few tokens: each result written as it is.
+template <typename Y> struct StoreFew {
+    static constexpr bool kRowsFirst = true;
+    Y* y;
+    int64_t ld;
+    __device__ __forceinline__ void begin() {}
+    __device__ __forceinline__ void value(float c, int64_t row, int v) {
+        y[v * ld + row] = from_f32<Y>(c);
+    }
+    __device__ __forceinline__ void end(float*, int) {}
+};
+
+constexpr int kFewTokens = 32;
+
+template <typename Y> hipError_t few_tokens(const E4m3ProductArgs& a, hipStream_t s) {
+    const FewArgs f{a.w, a.ldw, a.rows, a.cols, a.x, a.ldx, static_cast<int>(a.count), a.w_scales,
+                    a.x_scales};
+    const StoreFew<Y> e{static_cast<Y*>(a.y), a.ldy};
+    // Two row tiles a wave keep more bytes under way; with few rows there are more workgroups
+    // with one.
+    const bool many = a.rows >= 8 * 1024;
+    if (a.count <= 16)
+        return many ? few<FewCodes<8>, 1, 2>(f, e, 512, s) : few<FewCodes<8>, 1, 1>(f, e, 512, s);
+    return many ? few<FewCodes<8>, 2, 2>(f, e, 256, s) : few<FewCodes<8>, 2, 1>(f, e, 256, s);
+}
+
 template <template <class, int, int, int> class Math, typename Y>
 hipError_t matmul_of(const E4m3ProductArgs& a, hipStream_t s) {
     typedef ProductTile<Y> E;
     const ProductArgs p{a.w, a.ldw, a.x, a.ldx, a.rows, a.count, a.cols, 1, nullptr, false};
     const E e{StoreTile<Y>(a.y, a.ldy), a.w_scales, a.x_scales, (a.cols + kBlock - 1) / kBlock};
+    if (a.count <= kFewTokens) return few_tokens<Y>(a, s);
     const dim3 block(kTileThreads);
     // Few tiles: smaller ones, so that more CUs have some.
     const int64_t big = (a.rows + 255) / 256 * ((a.count + 255) / 256);

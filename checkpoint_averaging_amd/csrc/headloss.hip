@@ -7,7 +7,10 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "dlhead.h"
+#include "few.h"
 #include "head.h"
 #include "head_device.h"
 #include "tiles.h"
@@ -91,6 +94,61 @@ struct StatsTile {
             if (lane < 32 && n < at.n)
                 parts[at.m0 / (MT * 32) * rows + n] = Part{m, rest, dot};
         }
+    }
+};
+
+// The same for a few tokens: a thread meets one token's logits, some rows of the vocabulary
+// in turn, and leaves a part for all of the workgroup's.
+struct StatsFew {
+    static constexpr bool kRowsFirst = false;
+    Part* parts;                          // one row of `rows` for each workgroup
+    int64_t rows;
+    const int64_t* targets;               // or nullptr
+    float* at_target;
+    float m, rest, dot;
+
+    __device__ __forceinline__ void begin() {
+        m = -__builtin_inff();
+        rest = dot = 0;
+    }
+    __device__ __forceinline__ void value(float l, int64_t row, int v) {
+        if (targets != nullptr && targets[v] == row) at_target[v] = l;
+        add(Part{l, 0, 0});
+    }
+    // Part p joined to this one's.
+    __device__ __forceinline__ void add(Part p) {
+        if (p.m == -__builtin_inff() && p.rest == p.rest) return;        // nothing there
+        if (m == -__builtin_inff() && rest == rest) {
+            m = p.m;
+            rest = p.rest;
+            dot = p.dot;
+            return;
+        }
+        if (p.m > m) {
+            const Part t{m, rest, dot};
+            m = p.m;
+            rest = p.rest;
+            dot = p.dot;
+            p = t;
+        }
+        const float d = p.m - m, w = exp_of(d);
+        rest += w * (1 + p.rest);
+        // (w is 0 where d is -infinity)
+        dot += w > 0 || w != w ? w * (p.dot + d * (1 + p.rest)) : 0.0f;
+    }
+    __device__ __forceinline__ void end(float* lds, int count) {
+        const int tokens = count <= 16 ? 16 : 32;
+        Part* all = reinterpret_cast<Part*>(lds);
+        __syncthreads();
+        all[threadIdx.x] = Part{m, rest, dot};
+        for (int n = kFewThreads / 2; n >= tokens; n /= 2) {
+            __syncthreads();
+            if (static_cast<int>(threadIdx.x) < n) {
+                add(all[threadIdx.x + n]);
+                all[threadIdx.x] = Part{m, rest, dot};
+            }
+        }
+        if (static_cast<int>(threadIdx.x) < count) parts[blockIdx.x * rows + threadIdx.x] = Part{m, rest, dot};
     }
 };
 
@@ -411,20 +469,33 @@ hipError_t product_of(const ProductArgs& a, const E& e, hipStream_t s, bool padd
     return hipGetLastError();
 }
 
+constexpr int kFewTokens = 32, kFewGroups = 256;
+
 template <typename T> hipError_t forward(const HeadArgs& a, hipStream_t s) {
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-    const int parts = static_cast<int>((a.vocab + span_of<T>() - 1) / span_of<T>());
-    StatsTile e{};
-    e.at_target = reinterpret_cast<float*>(ws);
-    e.parts = reinterpret_cast<Part*>(ws + up(4 * a.rows, 256));
-    e.rows = a.rows;
-    e.targets = a.targets;
-    const ProductArgs p{a.embed, a.lde, a.x, a.ldx, a.vocab, a.rows, a.width, 1, nullptr, false};
-    const hipError_t st = product_of<T, false, false>(p, e, s);
+    float* at_target = reinterpret_cast<float*>(ws);
+    Part* parts = reinterpret_cast<Part*>(ws + up(4 * a.rows, 256));
+    int n_parts = 0;
+    hipError_t st;
+    if (a.rows <= kFewTokens) {
+        const FewArgs f{a.embed, a.lde, a.vocab, a.width, a.x, a.ldx, static_cast<int>(a.rows),
+                        nullptr, nullptr};
+        const StatsFew e{parts, a.rows, a.targets, at_target, 0, 0, 0};
+        constexpr bool kHalf = sizeof(T) == 2;
+        typedef std::conditional_t<kHalf, FewBf16<8>, FewSplit<4>> Src;
+        st = a.rows <= 16 ? few<Src, 1, kHalf ? 2 : 1>(f, e, kFewGroups, s, &n_parts)
+                          : few<Src, 2, 1>(f, e, kFewGroups, s, &n_parts);
+    } else {
+        const StatsTile e{parts, a.rows, a.targets, at_target};
+        const ProductArgs p{a.embed, a.lde, a.x, a.ldx, a.vocab, a.rows, a.width, 1, nullptr,
+                            false};
+        n_parts = static_cast<int>((a.vocab + span_of<T>() - 1) / span_of<T>());
+        st = product_of<T, false, false>(p, e, s);
+    }
     if (st != hipSuccess) return st;
     k_join<<<dim3(static_cast<unsigned>((a.rows + kJoinRows - 1) / kJoinRows)),
-             dim3(kJoinRows * kJoinParts), 0, s>>>(e.parts, parts, a.rows, a.vocab, a.targets,
-                                                   e.at_target, a.logprobs, a.entropy, a.stats);
+             dim3(kJoinRows * kJoinParts), 0, s>>>(parts, n_parts, a.rows, a.vocab, a.targets,
+                                                   at_target, a.logprobs, a.entropy, a.stats);
     return hipGetLastError();
 }
 
@@ -490,8 +561,9 @@ template <typename T> hipError_t backward(const HeadBackwardArgs& a, hipStream_t
 int64_t head_workspace_bytes(int64_t rows, int64_t vocab, int64_t width, int dtype,
                              bool with_backward) {
     const int64_t span = dtype == DL_BF16 ? kSpan : kSpanSplit;
-    const int64_t fwd = up(4 * rows, 256) +
-                        up((vocab + span - 1) / span * rows * static_cast<int64_t>(sizeof(Part)), 256);
+    const int64_t parts = rows <= kFewTokens ? kFewGroups : (vocab + span - 1) / span;
+    const int64_t fwd =
+        up(4 * rows, 256) + up(parts * rows * static_cast<int64_t>(sizeof(Part)), 256);
     if (!with_backward) return fwd;
     const int64_t bwd = backward_plan(rows, vocab, width, dtype == DL_BF16 ? 2 : 4).bytes;
     return fwd > bwd ? fwd : bwd;
