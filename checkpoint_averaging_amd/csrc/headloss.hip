@@ -237,18 +237,36 @@ struct __attribute__((aligned(16))) RowTerms {
 };
 
 // The rows that have a part in the gradients, in order: those with a target, or all
-// if there is a gradient of the entropies.  One workgroup.
+// if there is a gradient of the entropies.  And their largest weight: what the products
+// multiply is dlogits in units of it, so that where all weights are one (a mean's), a
+// target's 1 - p is near 1 and not rounded from a number that none of bf16's is near to.
+// One workgroup.
 constexpr int kSelectThreads = 1024;
 
-__global__ __launch_bounds__(kSelectThreads) void k_select(const int64_t* targets, bool all,
-                                                           int64_t rows, int* index, int* where,
-                                                           int* count) {
+struct Selected {
+    int count;
+    float unit;
+};
+
+__global__ __launch_bounds__(kSelectThreads) void k_select(const int64_t* targets,
+                                                           const float* dlogprobs,
+                                                           const float* dentropy, int64_t rows,
+                                                           int* index, int* where, Selected* to) {
     __shared__ int waves[2][kSelectThreads / kWave];
+    __shared__ uint32_t most[kSelectThreads / kWave];
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
     int before = 0;
+    uint32_t unit = 0;
     for (int64_t r0 = 0, turn = 0; r0 < rows; r0 += kSelectThreads, ++turn) {
         const int64_t row = r0 + threadIdx.x;
-        const bool in = row < rows && (all || targets[row] >= 0);
+        const bool has = row < rows && targets[row] >= 0;
+        const bool in = has || (row < rows && dentropy != nullptr);
+        auto weigh = [&](float w) {
+            const uint32_t b = abs_bits(w);
+            unit = b < 0x7F800000u ? Max{}(unit, b) : unit;
+        };
+        if (has) weigh(dlogprobs[row]);
+        if (in && dentropy != nullptr) weigh(dentropy[row]);
         const uint64_t votes = __ballot(in);
         if (lane == 0) waves[turn % 2][wave] = __popcll(votes);
         __syncthreads();
@@ -262,7 +280,14 @@ __global__ __launch_bounds__(kSelectThreads) void k_select(const int64_t* target
         if (in) index[at] = static_cast<int>(row);
         if (row < rows) where[row] = in ? at : -1;
     }
-    if (threadIdx.x == 0) *count = before;
+    unit = wave_reduce(unit, Max{});
+    if (lane == 0) most[wave] = unit;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int w = 0; w < kSelectThreads / kWave; ++w) unit = Max{}(unit, most[w]);
+    // (one below 2^-100, whose quotients might not be numbers, is no unit)
+    const float u = __uint_as_float(unit);
+    *to = Selected{before, u >= 0x1p-100f ? u : 1.0f};
 }
 
 struct GatherArgs {
@@ -275,7 +300,7 @@ struct GatherArgs {
     const float* dlogprobs;
     const float* dentropy;                // or nullptr
     const int* index;
-    const int* count;
+    const Selected* selected;
     void* to;
     int64_t ldto;
     RowTerms* terms;
@@ -284,7 +309,8 @@ struct GatherArgs {
 };
 
 template <typename T> __global__ __launch_bounds__(256) void k_gather(GatherArgs a) {
-    const int n = *a.count;
+    const int n = a.selected->count;
+    const float unit = a.selected->unit;
     for (int64_t j = blockIdx.x; j < n; j += gridDim.x) {
         const int64_t row = a.index[j];
         const T* from = static_cast<const T*>(a.x) + row * a.ldx;
@@ -302,8 +328,8 @@ template <typename T> __global__ __launch_bounds__(256) void k_gather(GatherArgs
             RowTerms r{};
             r.m = a.stats[2 * row];
             r.log_s = a.stats[2 * row + 1];
-            r.a = t < 0 ? 0.0f : t >= a.vocab ? __uint_as_float(0x7FC00000u) : a.dlogprobs[row];
-            r.b = a.dentropy != nullptr ? a.dentropy[row] : 0.0f;
+            r.a = t < 0 ? 0.0f : t >= a.vocab ? __uint_as_float(0x7FC00000u) : a.dlogprobs[row] / unit;
+            r.b = a.dentropy != nullptr ? a.dentropy[row] / unit : 0.0f;
             r.entropy = a.dentropy != nullptr ? a.entropy[row] : 0.0f;
             r.target = t < 0 || t >= a.vocab ? -1 : static_cast<int32_t>(t);
             a.terms[j] = r;
@@ -378,26 +404,52 @@ struct SumTile {
     }
 };
 
+// The slices' sums together, in the inputs' units: row i of out from row where[i] of the sums
+// (0 if that is -1), or with no `where` from row i.
 template <typename T>
-__global__ __launch_bounds__(256) void k_dx(const float* sums, int slices, int64_t rows,
-                                            int64_t lds, int width, const int* where, T* dx,
-                                            int64_t lddx) {
-    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-        const int at = where[row];
-        for (int c = threadIdx.x * 8; c < width; c += 256 * 8) {
-            float v[8] = {};
-            if (at >= 0) {
-                load8(sums + at * lds, c, width, v);
-                for (int s = 1; s < slices; ++s) {
-                    float w[8];
-                    load8(sums + (s * rows + at) * lds, c, width, w);
-                    for (int i = 0; i < 8; ++i) v[i] += w[i];
-                }
+__global__ __launch_bounds__(256) void k_join_slices(const float* sums, int slices, int64_t apart,
+                                                     int64_t lds, int64_t rows, int width,
+                                                     const int* where, const Selected* selected,
+                                                     T* out, int64_t ldo) {
+    const float unit = selected->unit;
+    const int per = (width + 7) / 8;                       // groups of eight columns
+    const int64_t all = rows * per;
+    for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < all; i += gridDim.x * int64_t(256)) {
+        const int64_t row = i / per, c = i % per * 8;
+        const int64_t at = where != nullptr ? where[row] : row;
+        float v[8] = {};
+        if (at >= 0) {
+            load8(sums + at * lds, c, width, v);
+            for (int s = 1; s < slices; ++s) {
+                float w[8];
+                load8(sums + (s * apart + at) * lds, c, width, w);
+                for (int k = 0; k < 8; ++k) v[k] += w[k];
             }
-            store8(dx + row * lddx, c, width, v);
+            for (int k = 0; k < 8; ++k) v[k] *= unit;
         }
+        store8(out + row * ldo, c, width, v);
     }
 }
+
+// C written out in the inputs' units.
+template <typename T> struct UnitTile {
+    T* y;
+    int64_t ld;
+    const Selected* selected;             // or nullptr
+
+    template <int MT, int NT>
+    __device__ __forceinline__ void finish(const f32x16 (&acc)[MT][NT], const Place& at) const {
+        const int lane = lane_here();
+        const float unit = selected != nullptr ? selected->unit : 1.0f;
+#pragma unroll
+        for (int u = 0; u < NT; ++u)
+#pragma unroll
+            for (int p = 0; p < kRuns<MT>; ++p)
+                write_run<32, false>(y, ld, at.n0 + u * kSquare + lane % kSquare, at.n,
+                                     at.m0 + run_at<MT>(p, lane), at.m, lane,
+                                     [&](int i) { return in_run(acc, p, u, i) * unit; });
+    }
+};
 
 // ---- plans -------------------------------------------------------------------
 
@@ -411,8 +463,9 @@ template <typename T> constexpr int span_of() { return sizeof(T) == 2 ? kSpan : 
 struct Backward {
     int64_t piece, pieces;                // of the vocabulary; the last takes the rest
     int64_t ld_p, ld_x, ld_s;
-    int slices;
-    int64_t index, where, count, terms, x, p, sums, bytes;      // places in the workspace
+    int slices, slices_e;                 // of the vocabulary for dx, of the rows for dembed
+    int64_t widest;                       // piece
+    int64_t index, where, selected, terms, x, p, sums, sums_e, bytes;      // places in the workspace
 };
 
 constexpr int64_t kPieceBytes = int64_t(128) << 20;
@@ -427,12 +480,16 @@ Backward backward_plan(int64_t rows, int64_t vocab, int64_t width, int64_t esize
         b.piece = vocab;
         b.pieces = 1;
     }
-    const int64_t widest = vocab - (b.pieces - 1) * b.piece;
-    b.ld_p = up(widest, 8);
+    b.widest = vocab - (b.pieces - 1) * b.piece;
+    b.ld_p = up(b.widest, 8);
     b.ld_x = up(width, 8);
     b.ld_s = up(width, 4);
-    const int64_t tiles = up(width, 256) / 256 * (up(rows, 256) / 256);
-    b.slices = static_cast<int>(tiles >= 256 ? 1 : 256 / tiles > 16 ? 16 : 256 / tiles);
+    // Products of few tiles are cut along k, so that every CU has some.
+    auto cut = [](int64_t tiles) {
+        return static_cast<int>(tiles > 128 ? 1 : 256 / tiles > 16 ? 16 : 256 / tiles);
+    };
+    b.slices = cut(up(width, 256) / 256 * (up(rows, 256) / 256));
+    b.slices_e = cut(up(width, 256) / 256 * (up(b.widest, 256) / 256));
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t here = at;
@@ -441,11 +498,12 @@ Backward backward_plan(int64_t rows, int64_t vocab, int64_t width, int64_t esize
     };
     b.index = take(4 * rows);
     b.where = take(4 * rows);
-    b.count = take(4);
+    b.selected = take(sizeof(Selected));
     b.terms = take(static_cast<int64_t>(sizeof(RowTerms)) * rows);
     b.x = take(rows * b.ld_x * esize);
     b.p = take(rows * b.ld_p * esize);
     b.sums = take(b.slices * rows * b.ld_s * 4);
+    b.sums_e = b.slices_e == 1 ? at : take(b.slices_e * b.widest * b.ld_s * 4);
     b.bytes = at;
     return b;
 }
@@ -499,29 +557,42 @@ template <typename T> hipError_t forward(const HeadArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <typename T>
+hipError_t join_slices(const float* sums, int slices, int64_t apart, int64_t lds, int64_t rows,
+                       int64_t width, const int* where, const Selected* selected, T* out,
+                       int64_t ldo, hipStream_t s) {
+    const int64_t blocks = (rows * ((width + 7) / 8) + 255) / 256;
+    k_join_slices<T><<<dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s>>>(
+        sums, slices, apart, lds, rows, static_cast<int>(width), where, selected, out, ldo);
+    return hipGetLastError();
+}
+
 template <typename T> hipError_t backward(const HeadBackwardArgs& a, hipStream_t s) {
     if (a.rows == 0) {
         const ProductArgs none{nullptr, 0, nullptr, 0, a.width, a.vocab, 0, 1, nullptr, false};
-        return product_of<T, true, true>(none, StoreTile<T>(a.dembed, a.ldde), s);
+        return product_of<T, true, true>(
+            none, UnitTile<T>{static_cast<T*>(a.dembed), a.ldde, nullptr}, s);
     }
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     const Backward b = backward_plan(a.rows, a.vocab, a.width, sizeof(T));
     int* index = reinterpret_cast<int*>(ws + b.index);
     int* where = reinterpret_cast<int*>(ws + b.where);
-    int* count = reinterpret_cast<int*>(ws + b.count);
+    Selected* selected = reinterpret_cast<Selected*>(ws + b.selected);
+    const int* count = &selected->count;
     RowTerms* terms = reinterpret_cast<RowTerms*>(ws + b.terms);
     T* x = reinterpret_cast<T*>(ws + b.x);
     T* p = reinterpret_cast<T*>(ws + b.p);
     float* sums = reinterpret_cast<float*>(ws + b.sums);
-    k_select<<<dim3(1), dim3(kSelectThreads), 0, s>>>(a.targets, a.dentropy != nullptr, a.rows,
-                                                      index, where, count);
+    float* sums_e = reinterpret_cast<float*>(ws + b.sums_e);
+    k_select<<<dim3(1), dim3(kSelectThreads), 0, s>>>(a.targets, a.dlogprobs, a.dentropy, a.rows,
+                                                      index, where, selected);
     hipError_t st = hipGetLastError();
     if (st != hipSuccess) return st;
     const unsigned walkers = static_cast<unsigned>(a.rows < 2048 ? a.rows : 2048);
     const GatherArgs g{a.x,       a.ldx,      a.rows, a.vocab, static_cast<int>(a.width),
                        a.targets, a.stats,    a.entropy, a.dlogprobs, a.dentropy,
-                       index,     count,      x,      b.ld_x,  terms,
-                       p,         b.ld_p,     a.vocab - (b.pieces - 1) * b.piece};
+                       index,     selected,   x,      b.ld_x,  terms,
+                       p,         b.ld_p,     b.widest};
     k_gather<T><<<dim3(walkers), dim3(256), 0, s>>>(g);
     if ((st = hipGetLastError()) != hipSuccess) return st;
     for (int64_t i = 0; i < b.pieces; ++i) {
@@ -544,16 +615,24 @@ template <typename T> hipError_t backward(const HeadBackwardArgs& a, hipStream_t
             if ((st = product_of<T, true, false>(dp, e, s, true)) != hipSuccess) return st;
         }
         if (a.dembed != nullptr) {
-            const ProductArgs ep{x, b.ld_x, p, b.ld_p, a.width, n, a.rows, 1, count, true};
-            const StoreTile<T> e(static_cast<T*>(a.dembed) + v0 * a.ldde, a.ldde);
-            if ((st = product_of<T, true, true>(ep, e, s)) != hipSuccess) return st;
+            T* to = static_cast<T*>(a.dembed) + v0 * a.ldde;
+            const ProductArgs ep{x, b.ld_x, p, b.ld_p, a.width, n, a.rows, b.slices_e, count, true};
+            if (b.slices_e == 1) {
+                const UnitTile<T> e{to, a.ldde, selected};
+                st = product_of<T, true, true>(ep, e, s);
+            } else {
+                const SumTile e{sums_e, n, b.ld_s, true};
+                st = product_of<T, true, true>(ep, e, s);
+                if (st == hipSuccess)
+                    st = join_slices<T>(sums_e, b.slices_e, n, b.ld_s, n, a.width, nullptr, selected,
+                                        to, a.ldde, s);
+            }
+            if (st != hipSuccess) return st;
         }
     }
     if (a.dx == nullptr) return hipSuccess;
-    k_dx<T><<<dim3(walkers), dim3(256), 0, s>>>(sums, b.slices, a.rows, b.ld_s,
-                                                static_cast<int>(a.width), where,
-                                                static_cast<T*>(a.dx), a.lddx);
-    return hipGetLastError();
+    return join_slices<T>(sums, b.slices, a.rows, b.ld_s, a.rows, a.width, where, selected,
+                          static_cast<T*>(a.dx), a.lddx, s);
 }
 
 }  // namespace
