@@ -17,6 +17,9 @@ using dlk::check_device_span;
 using dlk::span_of;
 
 constexpr int64_t kMaxDim = INT32_MAX;
+// Of the tiled products, whose kernels count rows and columns, past a last tile too, and
+// tiles in 32 bits.
+constexpr int64_t kMaxTiled = int64_t(1) << 30, kMaxProduct = int64_t(1) << 43;
 
 int64_t esize_of(int dtype) { return dtype == DL_F32 ? 4 : dtype == DL_BF16 ? 2 : 1; }
 
@@ -344,7 +347,7 @@ int dl_head_workspace_bytes(int64_t rows, int64_t vocab, int64_t width, int dtyp
     if (bytes == nullptr || !float_type(dtype) || !dim(rows, 0) || !dim(vocab, 1) || width < 1 ||
         width > DL_MAX_NORM_COLS)
         return DL_E_INVAL;
-    if (rows > 0 && vocab + width > (int64_t(1) << 50) / rows) return DL_E_INVAL;
+    if (rows > kMaxTiled || vocab > kMaxTiled || rows * vocab > kMaxProduct) return DL_E_INVAL;
     *bytes = rows == 0 ? 0 : dlk::head_workspace_bytes(rows, vocab, width, dtype, backward != 0);
     return DL_OK;
 }
@@ -432,6 +435,8 @@ int dl_e4m3_matmul(const uint8_t* w, int64_t ldw, const uint8_t* w_scales, int64
                    int64_t cols, const uint8_t* x, int64_t ldx, const uint8_t* x_scales,
                    int64_t count, void* y, int64_t ldy, int y_dtype, void* stream) {
     if (!float_type(y_dtype) || !dim(rows, 0) || !dim(cols, 1) || !dim(count, 0))
+        return DL_E_INVAL;
+    if (rows > kMaxTiled || cols > kMaxTiled || count > kMaxTiled || rows * count > kMaxProduct)
         return DL_E_INVAL;
     if (rows == 0 || count == 0) return DL_OK;
     const int64_t ye = esize_of(y_dtype);

@@ -14,6 +14,14 @@ layers below it, which give the residual stream, are the caller's.
     a = head.score(x, residual, targets)         # from the fp32 embedding
     head.publish()                               # lay the embedding out in 4 bits
     a = head.answer(x, residual, top_k=8)        # from the published one
+    head.publish(bits=8)                         # or in 8: for whole probes at once
+
+``LossHead`` is the same stage where only the log probabilities are wanted, and
+their gradients: it holds no logits.
+
+    loss = LossHead.of(synth.DIFFUREFILL_1B, global_, max_rows=16384)
+    a = loss.score(x, residual, targets, sum_=s)
+    loss.backward(s, targets, dlogprobs, dx, dembed, dweight)
 
 Results are views of the head's buffers: the next call on it writes over them.
 All buffers, workspaces included, are taken when the head is built and the
@@ -42,6 +50,28 @@ class Answer(NamedTuple):
     top_logprobs: Optional[torch.Tensor]       # rows x top_k
 
 
+class Loss(NamedTuple):
+    logprobs: Optional[torch.Tensor]           # rows (None without targets)
+    entropy: torch.Tensor                      # rows
+    stats: torch.Tensor                        # rows x 2: largest logit, log of the sum
+
+
+def _views(layout: synth.Layout, flat: torch.Tensor):
+    """(final norm weight, tied embedding) in a flat fp32 parameter vector."""
+    names = dict(layout.tensors)
+    if "final_norm.weight" not in names or "embed" not in names:
+        raise ValueError(f"{layout.name}: no RMS norm and tied embedding at its end")
+    if (flat.dtype != torch.float32 or flat.numel() != layout.n_params or
+            not flat.is_contiguous()):
+        raise ValueError("flat: the layout's parameters in float32 required, contiguous")
+    flat = flat.view(-1)
+    width = names["final_norm.weight"]
+    off = layout.offset_of("final_norm.weight")
+    weight = flat[off:off + width]
+    off = layout.offset_of("embed")
+    return weight, flat[off:off + names["embed"]].view(names["embed"] // width, width)
+
+
 class Head:
     """Final RMS norm and tied embedding of one candidate, for up to max_rows
     tokens a call.  `flat` is the candidate's fp32 parameter vector; the views
@@ -50,24 +80,14 @@ class Head:
 
     def __init__(self, layout: synth.Layout, flat: torch.Tensor, max_rows: int,
                  eps: float = 1e-5):
-        names = dict(layout.tensors)
-        if "final_norm.weight" not in names or "embed" not in names:
-            raise ValueError(f"{layout.name}: no RMS norm and tied embedding at its end")
-        if (flat.dtype != torch.float32 or flat.numel() != layout.n_params or
-                not flat.is_contiguous()):
-            raise ValueError("flat: the layout's parameters in float32 required, contiguous")
-        flat = flat.view(-1)
+        self.weight, self.embed = _views(layout, flat)
         if max_rows < 1:
             raise ValueError("max_rows must be at least 1")
-        self.width = names["final_norm.weight"]
-        self.vocab = names["embed"] // self.width
-        off = layout.offset_of("final_norm.weight")
-        self.weight = flat[off:off + self.width]
-        off = layout.offset_of("embed")
-        self.embed = flat[off:off + names["embed"]].view(self.vocab, self.width)
+        self.vocab, self.width = self.embed.shape
         self.eps, self.max_rows, dev = eps, max_rows, flat.device
         self._blocks = (self.width + 31) // 32
-        self._packed = self._scales = None
+        self._packed = self._scales = self._codes = self._code_scales = None
+        self._bits = 0                           # of the published form
 
         def new(*shape, dtype=torch.float32):
             return torch.empty(*shape, dtype=dtype, device=dev)
@@ -75,6 +95,7 @@ class Head:
         self._h = new(max_rows, self.width)
         self._h8 = new(max_rows, self.width, dtype=torch.float8_e4m3fn)
         self._h8_scales = new(max_rows, self._blocks, dtype=torch.uint8)
+        self._h8_scales128 = new(max_rows, (self.width + 127) // 128, dtype=torch.uint8)
         self._inv = new(max_rows)
         self._logits = new(max_rows, self.vocab)
         self._logprobs, self._entropy, self._stats = new(max_rows), new(max_rows), new(max_rows, 2)
@@ -89,14 +110,28 @@ class Head:
                    for r in range(1, max_rows + 1))
         self._product_ws = new(max(need, 256), dtype=torch.uint8)
 
-    def publish(self) -> None:
-        """Lays the embedding, as it is now, out in 4 bits."""
-        if self._packed is None:
-            packed, scales = dh.dl_w4_bytes(self.vocab, self.width)
-            dev = self.embed.device
-            self._packed = torch.empty(packed, dtype=torch.uint8, device=dev)
-            self._scales = torch.empty(scales, dtype=torch.uint8, device=dev)
-        dh.dl_w4_quantize(self.embed, self.vocab, self.width, self._packed, self._scales)
+    def publish(self, bits: int = 4) -> None:
+        """Lays the embedding, as it is now, out in 4 bits (with a scale for each
+        32 weights) or in 8 (for each 128 x 128): what answer() then goes by."""
+        dev = self.embed.device
+        if bits == 4:
+            if self._packed is None:
+                packed, scales = dh.dl_w4_bytes(self.vocab, self.width)
+                self._packed = torch.empty(packed, dtype=torch.uint8, device=dev)
+                self._scales = torch.empty(scales, dtype=torch.uint8, device=dev)
+            dh.dl_w4_quantize(self.embed, self.vocab, self.width, self._packed, self._scales)
+        elif bits == 8:
+            if self._codes is None:
+                self._codes = torch.empty(self.vocab, self.width, dtype=torch.float8_e4m3fn,
+                                          device=dev)
+                self._code_scales = torch.empty((self.vocab + 127) // 128,
+                                                (self.width + 127) // 128, dtype=torch.uint8,
+                                                device=dev)
+            dh.dl_e4m3_quantize(self.embed, self.vocab, self.width, self._codes,
+                                self._code_scales, dh.DL_SCALE_TILE128)
+        else:
+            raise ValueError(f"bits: 4 or 8 required, got {bits}")
+        self._bits = bits
 
     def _rows(self, x: torch.Tensor, top_k: int = 0) -> int:
         if not 0 <= top_k <= min(dh.DL_MAX_TOP, self.vocab):
@@ -109,20 +144,28 @@ class Head:
     def answer(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
                targets: Optional[torch.Tensor] = None, top_k: int = 0) -> Answer:
         """The published head's answer for the residual stream x (+ residual),
-        in bf16 or fp32: norm in 8 bits with block scales, 4-bit product
-        (DL_MAX_VECTORS tokens a pass), log probabilities.  (With more bits in
-        the stream: dl_rmsnorm to bf16 and dl_w4_matvec.)"""
-        if self._packed is None:
+        in bf16 or fp32.  In 4 bits: norm in 8 bits with block scales, 4-bit
+        product (DL_MAX_VECTORS tokens a pass), log probabilities.  In 8: norm in
+        8 bits with a scale for each 128, one product for all tokens.  (With more
+        bits in the stream: dl_rmsnorm to bf16 and dl_w4_matvec.)"""
+        if self._bits == 0:
             raise RuntimeError("publish() first")
         rows = self._rows(x, top_k)
+        four = self._bits == 4
         dh.dl_rmsnorm(x, rows, self.width, self.weight, self._h8, eps=self.eps,
-                      residual=residual, scales=self._h8_scales,
-                      scale_kind=dh.DL_SCALE_BLOCK32)
-        for r in range(0, rows, dh.DL_MAX_VECTORS):
-            n = min(dh.DL_MAX_VECTORS, rows - r)
-            dh.dl_w4_matvec(self._packed, self._scales, self.vocab, self.width, self._h8[r:r + n],
-                            n, self._logits[r:r + n], x_scales=self._h8_scales[r:r + n],
-                            x_scale_kind=dh.DL_SCALE_BLOCK32)
+                      residual=residual,
+                      scales=self._h8_scales if four else self._h8_scales128,
+                      scale_kind=dh.DL_SCALE_BLOCK32 if four else dh.DL_SCALE_BLOCK128)
+        if four:
+            for r in range(0, rows, dh.DL_MAX_VECTORS):
+                n = min(dh.DL_MAX_VECTORS, rows - r)
+                dh.dl_w4_matvec(self._packed, self._scales, self.vocab, self.width,
+                                self._h8[r:r + n], n, self._logits[r:r + n],
+                                x_scales=self._h8_scales[r:r + n],
+                                x_scale_kind=dh.DL_SCALE_BLOCK32)
+        else:
+            dh.dl_e4m3_matmul(self._codes, self._code_scales, self.vocab, self.width, self._h8,
+                              self._h8_scales128, rows, self._logits)
         return self._read(rows, targets, top_k)
 
     def score(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
@@ -175,3 +218,80 @@ class Head:
         rows = self._rows(sum_)
         dh.dl_rmsnorm_backward(dy, sum_, rows, self.width, self.weight, self._inv, dx,
                                dweight=dweight, workspace=workspace)
+
+
+class LossHead:
+    """Final RMS norm and embedding where the logits themselves are not wanted: a
+    long probe's log probabilities, a training step's loss and gradients, for up to
+    max_rows tokens a call.  weight: width fp32; embed: vocab x width in fp32 or bf16
+    (products are then of bf16 numbers, the norm's output rounded to them), a view of
+    the caller's parameters that the head follows."""
+
+    def __init__(self, weight: torch.Tensor, embed: torch.Tensor, max_rows: int,
+                 eps: float = 1e-5):
+        if embed.dim() != 2 or embed.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError("embed: a matrix in float32 or bfloat16 required")
+        self.vocab, self.width = embed.shape
+        if weight.shape != (self.width,) or weight.dtype != torch.float32:
+            raise ValueError(f"weight: {self.width} elements in float32 required")
+        if max_rows < 1:
+            raise ValueError("max_rows must be at least 1")
+        self.weight, self.embed, self.eps, self.max_rows = weight, embed, eps, max_rows
+        dev = embed.device
+
+        def new(*shape, dtype=torch.float32):
+            return torch.empty(*shape, dtype=dtype, device=dev)
+
+        self._h = new(max_rows, self.width, dtype=embed.dtype)
+        self._dh = new(max_rows, self.width, dtype=embed.dtype)
+        self._inv = new(max_rows)
+        self._logprobs, self._entropy, self._stats = new(max_rows), new(max_rows), new(max_rows, 2)
+        need = max(dh.dl_head_workspace_bytes(r, self.vocab, self.width, embed.dtype, True)
+                   for r in range(1, max_rows + 1))
+        self._ws = new(max(need, 256), dtype=torch.uint8)
+        need = dh.dl_rmsnorm_workspace_bytes(max_rows, self.width)      # (fewer rows need no more)
+        self._norm_ws = new(max(need, 256), dtype=torch.uint8)
+
+    @classmethod
+    def of(cls, layout: synth.Layout, flat: torch.Tensor, max_rows: int, eps: float = 1e-5):
+        """A candidate's, over its flat fp32 parameter vector."""
+        return cls(*_views(layout, flat), max_rows, eps)
+
+    def _rows(self, x: torch.Tensor, name: str) -> int:
+        if x.dim() != 2 or x.shape[1] != self.width or x.shape[0] > self.max_rows:
+            raise ValueError(f"{name}: at most {self.max_rows} x {self.width} required, got "
+                             f"{tuple(x.shape)}")
+        return x.shape[0]
+
+    def score(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
+              targets: Optional[torch.Tensor] = None,
+              sum_: Optional[torch.Tensor] = None) -> Loss:
+        """Log probabilities of the targets and entropies for the residual stream x (+
+        residual), in fp32 or bf16; sum_, if given, receives x + residual (backward()
+        wants it)."""
+        rows = self._rows(x, "x")
+        dh.dl_rmsnorm(x, rows, self.width, self.weight, self._h, eps=self.eps, residual=residual,
+                      sum_=sum_, inv_rms=self._inv)
+        logprobs = None if targets is None else self._logprobs[:rows]
+        dh.dl_head_logprobs(self._h, self.embed, rows, self.vocab, self.width, targets, logprobs,
+                            entropy=self._entropy, stats=self._stats, workspace=self._ws)
+        return Loss(logprobs, self._entropy[:rows], self._stats[:rows])
+
+    def backward(self, sum_: torch.Tensor, targets: torch.Tensor, dlogprobs: torch.Tensor,
+                 dx: torch.Tensor, dembed: Optional[torch.Tensor] = None,
+                 dweight: Optional[torch.Tensor] = None,
+                 dentropy: Optional[torch.Tensor] = None,
+                 dsum: Optional[torch.Tensor] = None) -> None:
+        """The gradients of sum(dlogprobs * logprobs) + sum(dentropy * entropy) (and of
+        what gave dsum), after the score() of these targets that left sum_ (or took it
+        as x): dx in the stream, dembed, dweight, each written.  The stream has to be of
+        the embedding's type."""
+        rows = self._rows(sum_, "sum")
+        if sum_.dtype != self.embed.dtype:
+            raise ValueError(f"sum: {sum_.dtype}, and the embedding {self.embed.dtype}")
+        dh.dl_head_logprobs_backward(self._h, self.embed, rows, self.vocab, self.width, targets,
+                                     self._stats, dlogprobs, dx=self._dh, dembed=dembed,
+                                     entropy=None if dentropy is None else self._entropy,
+                                     dentropy=dentropy, workspace=self._ws)
+        dh.dl_rmsnorm_backward(self._dh, sum_, rows, self.width, self.weight, self._inv, dx,
+                               dsum=dsum, dweight=dweight, workspace=self._norm_ws)

@@ -248,8 +248,8 @@ int dl_logprobs_backward(const void *logits, int64_t ldl, int dtype, int64_t row
  *
  * workspace: dl_head_workspace_bytes bytes; `backward` nonzero asks for what the
  * gradients need too (never less than without).  rows = 0 is a no-op.
- * 1 <= vocab <= 2^31 - 1, 1 <= width <= DL_MAX_NORM_COLS, and rows x (vocab
- * + width) at most 2^50.
+ * 1 <= vocab, 1 <= width <= DL_MAX_NORM_COLS; rows and vocab at most 2^30, their
+ * product at most 2^43.
  */
 int dl_head_workspace_bytes(int64_t rows, int64_t vocab, int64_t width, int dtype, int backward,
                             int64_t *bytes);
@@ -265,7 +265,8 @@ int dl_head_logprobs(const void *x, int64_t ldx, const void *embed, int64_t lde,
  * stats and entropy are the forward call's (entropy is needed with dentropy,
  * else NULL).  dx: rows x width, dembed: vocab x width of dtype, each written (not
  * added to); either may be NULL.  The logits are formed again piece by piece;
- * dlogits is rounded to dtype, and its products summed in binary32.
+ * dlogits, in units of the largest magnitude among the dlogprobs and dentropy that
+ * take part, is rounded to dtype, and its products summed in binary32.
  *
  * Without dentropy, a row without a target has no part: its dx is 0 and it adds
  * nothing to dembed, whatever its x, stats and dlogprobs hold.  A row with target
@@ -311,7 +312,7 @@ int dl_e4m3_quantize(const void *x, int64_t ldx, int dtype, int64_t rows, int64_
  *             bf16's rounding.
  *
  * Any code and scale byte is accepted.  rows = 0 and count = 0 are no-ops;
- * 1 <= cols, all at most 2^31 - 1.
+ * 1 <= cols, all at most 2^30, rows x count at most 2^43.
  */
 int dl_e4m3_matmul(const uint8_t *w, int64_t ldw, const uint8_t *w_scales, int64_t rows,
                    int64_t cols, const uint8_t *x, int64_t ldx, const uint8_t *x_scales,
