@@ -109,62 +109,67 @@ template <class Via, bool ACROSS, int ROWS, bool FIRST, bool PAIRS, int STEP_BYT
         wide = ACROSS ? rows - row0 : k1 - k0;
         at = static_cast<const T*>(p) + (ACROSS ? k0 * ld + row0 : row0 * ld + k0) + l * ld + c;
     }
-    // The step's pieces (0 outside), and on to the next step.
+    // Whether all of the step's pieces are inside.
+    __device__ __forceinline__ bool whole() const { return lines >= kLines && wide >= kLine * kPer; }
     __device__ __forceinline__ void load() {
+        for (int j = 0; j < kMine; ++j)
+            v[j] = *reinterpret_cast<const typename Raw<T>::any*>(at + j * apart);
+    }
+    // The pieces of a step that is not whole: 0 outside.
+    __device__ __forceinline__ void load_some() {
         const int c = threadIdx.x % kLine * kPer, l = threadIdx.x / kLine;
-        if (lines >= kLines && wide >= kLine * kPer) {
-            for (int j = 0; j < kMine; ++j)
-                v[j] = *reinterpret_cast<const typename Raw<T>::any*>(at + j * apart);
-        } else {
-            for (int j = 0; j < kMine; ++j) {
-                const T* q = at + j * apart;
-                v[j] = u32x4{};
-                if (l + j * kApart >= lines) continue;
-                if (c + kPer <= wide) {
-                    v[j] = *reinterpret_cast<const typename Raw<T>::any*>(q);
-                } else if (c < wide) {
-                    const int n = static_cast<int>(wide) - c;
+        for (int j = 0; j < kMine; ++j) {
+            const T* q = at + j * apart;
+            v[j] = u32x4{};
+            if (l + j * kApart >= lines) continue;
+            if (c + kPer <= wide) {
+                v[j] = *reinterpret_cast<const typename Raw<T>::any*>(q);
+            } else if (c < wide) {
+                const int n = static_cast<int>(wide) - c;
 #pragma unroll 1
-                    for (int i = 0; i < n; ++i) {
-                        constexpr int kIn = 4 / static_cast<int>(sizeof(T));
-                        uint32_t e = 0;
-                        __builtin_memcpy(&e, q + i, sizeof(T));
-                        e <<= i % kIn * 8 * static_cast<int>(sizeof(T)) % 32;
-                        for (int k = 0; k < 4; ++k) v[j][k] |= i / kIn == k ? e : 0;
-                    }
+                for (int i = 0; i < n; ++i) {
+                    constexpr int kIn = 4 / static_cast<int>(sizeof(T));
+                    uint32_t e = 0;
+                    __builtin_memcpy(&e, q + i, sizeof(T));
+                    e <<= i % kIn * 8 * static_cast<int>(sizeof(T)) % 32;
+                    for (int k = 0; k < 4; ++k) v[j][k] |= i / kIn == k ? e : 0;
                 }
             }
         }
+    }
+    // On to the next step.
+    __device__ __forceinline__ void onward() {
         at += ACROSS ? kStep * ld : kStep;
         (ACROSS ? lines : wide) -= kStep;
     }
-    __device__ __forceinline__ void put(uint8_t* lds) const {
-        const int c = threadIdx.x % kLine, l = threadIdx.x / kLine;
-        for (int j = 0; j < kMine; ++j) {
-            const int line = l + j * kApart;
-            if constexpr (Via::kPlanes == 1) {
-                const int to = line * kRowBytes +
-                               (ACROSS ? (c * 16) ^ key_across(line) : (c ^ key(line)) * 16);
-                *reinterpret_cast<u32x4*>(lds + to) = v[j];
-            } else {
-                const int to = line * kRowBytes +
-                               (ACROSS ? (c * 8) ^ key_across(line)
-                                       : ((c >> 1) ^ key(line)) * 16 + (c & 1) * 8);
-                uint32_t q[3][2];
-                for (int i = 0; i < 2; ++i) {
-                    float x = __uint_as_float(v[j][2 * i]), y = __uint_as_float(v[j][2 * i + 1]);
-                    for (int p = 0; p < 3; ++p) {
-                        typedef float f32x2 __attribute__((ext_vector_type(2)));
-                        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-                        q[p][i] = __builtin_bit_cast(
-                            uint32_t, __builtin_convertvector((f32x2{x, y}), bf16x2));
-                        x -= __uint_as_float(q[p][i] << 16);
-                        y -= __uint_as_float(q[p][i] & 0xFFFF0000u);
-                    }
+    // The pieces p, which a step's load() left, to LDS.
+    __device__ __forceinline__ void put(uint8_t* lds, const u32x4 (&p)[kMine]) const {
+        for (int j = 0; j < kMine; ++j) put(lds, j, p[j]);
+    }
+    __device__ __forceinline__ void put(uint8_t* lds, int j, const u32x4& p) const {
+        const int c = threadIdx.x % kLine, line = threadIdx.x / kLine + j * kApart;
+        if constexpr (Via::kPlanes == 1) {
+            const int to = line * kRowBytes +
+                           (ACROSS ? (c * 16) ^ key_across(line) : (c ^ key(line)) * 16);
+            *reinterpret_cast<u32x4*>(lds + to) = p;
+        } else {
+            const int to = line * kRowBytes +
+                           (ACROSS ? (c * 8) ^ key_across(line)
+                                   : ((c >> 1) ^ key(line)) * 16 + (c & 1) * 8);
+            uint32_t q[3][2];
+            for (int i = 0; i < 2; ++i) {
+                float x = __uint_as_float(p[2 * i]), y = __uint_as_float(p[2 * i + 1]);
+                for (int h = 0; h < 3; ++h) {
+                    typedef float f32x2 __attribute__((ext_vector_type(2)));
+                    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+                    q[h][i] = __builtin_bit_cast(
+                        uint32_t, __builtin_convertvector((f32x2{x, y}), bf16x2));
+                    x -= __uint_as_float(q[h][i] << 16);
+                    y -= __uint_as_float(q[h][i] & 0xFFFF0000u);
                 }
-                for (int p = 0; p < 3; ++p)
-                    *reinterpret_cast<u32x2*>(lds + p * kPlaneBytes + to) = u32x2{q[p][0], q[p][1]};
             }
+            for (int h = 0; h < 3; ++h)
+                *reinterpret_cast<u32x2*>(lds + h * kPlaneBytes + to) = u32x2{q[h][0], q[h][1]};
         }
     }
 
@@ -456,8 +461,13 @@ template <class Epilogue, int MT, int NT, int SUBS> struct SplitMath {
 };
 
 // Through registers.  The next step's 16-byte pieces are under way from memory to registers
-// while this step's products run, and are put into the other one of two LDS buffers halfway
-// through them: a step costs one barrier and no wait that its products do not cover.
+// while this step's products run, and are put into the other one of two LDS buffers beside
+// them: a step costs one barrier and no wait that its products do not cover.  Binary32's way
+// to LDS has some 35 vector instructions a piece (its three planes): these are spread between
+// the products, five after each, from copies of the pieces, whose registers take the step
+// after at once (all of a step's at a time, halfway through its products: 3.85 ms for 2048 x
+// 73760 x 2048, so 3.40; of which the conversions are 0.27).  Other types' pieces, whose
+// products leave no registers for copies, go halfway.
 constexpr int kStepBytes = 128;
 
 template <class Via, bool SA, bool SB, int TM, int TN, int WM, int WN, class Epilogue,
@@ -467,6 +477,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product(ProductArgs a, Epil
     constexpr int kMT = TM / WM / kSquare, kNT = TN / WN / kSquare;
     typedef Side<Via, SA, TM, true, kMT % 2 == 0, kStepBytes> SideA;
     typedef Side<Via, SB, TN, false, false, kStepBytes> SideB;
+    constexpr bool kSpread = Via::kPlanes == 3;
     // (a sub-step is 32 bytes of what LDS holds)
     typedef Math<Epilogue, kMT, kNT, SideA::kStep * SideA::kHeld / 32> Made;
     constexpr int kStep = SideA::kStep, kGroups = Made::kSubs * kMT, kAhead = Made::kAhead;
@@ -496,8 +507,17 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product(ProductArgs a, Epil
     auto fetch = [&] {
         held = in_at < items.end;
         if (!held) return;
-        sa.load();
-        sb.load();
+        // (one branch for both: where ways join, the compiler waits for all that either has
+        // under way before it uses a register of theirs again)
+        if (sa.whole() && sb.whole()) {
+            sa.load();
+            sb.load();
+        } else {
+            sa.load_some();
+            sb.load_some();
+        }
+        sa.onward();
+        sb.onward();
         if (--in_turns == 0) {
             in_at += Items::step();
             aim();
@@ -505,8 +525,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product(ProductArgs a, Epil
     };
     auto put = [&](uint8_t* to) {
         if (!held) return;
-        sa.put(to);
-        sb.put(to + SideA::kBytes);
+        sa.put(to, sa.v);
+        sb.put(to + SideA::kBytes, sb.v);
     };
     int buf = 0;
     fetch();
@@ -531,10 +551,17 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product(ProductArgs a, Epil
         do {
             const uint8_t *l = lds[buf], *next = lds[buf ^ 1];
             made.step();
+            u32x4 pa[SideA::kMine], pb[SideB::kMine];
+            if constexpr (kSpread) {
+                for (int j = 0; j < SideA::kMine; ++j) pa[j] = sa.v[j];
+                for (int j = 0; j < SideB::kMine; ++j) pb[j] = sb.v[j];
+                fetch();
+                __builtin_amdgcn_sched_barrier(0);
+            }
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) {
                 const int sub = g / kMT, h = g + kAhead;
-                if (g == kGroups / 2) {
+                if (!kSpread && g == kGroups / 2) {
                     put(lds[buf ^ 1]);
                     fetch();
                 }
@@ -549,6 +576,23 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product(ProductArgs a, Epil
                     h < kGroups ? l : next, wm, h % kMT, h / kMT % Made::kSubs);
                 __builtin_amdgcn_sched_barrier(0);
                 made.multiply(va[g % (kAhead + 1)], vb[sub % Made::kSlots], acc[g % kMT]);
+                if constexpr (kSpread) {
+                    // (a step that is not there leaves what nobody reads)
+                    constexpr int kOver = kGroups - kAhead, kA = SideA::kMine, kAll = kA + SideB::kMine;
+#pragma unroll
+                    for (int q = 0; q < kAll; ++q) {
+                        if (q * kOver / kAll != g) continue;
+                        if (q < kA) sa.put(lds[buf ^ 1], q, pa[q]);
+                        else sb.put(lds[buf ^ 1] + SideA::kBytes, q - kA, pb[q - kA]);
+                    }
+                    // one product, then what the vector unit does while it runs
+#pragma unroll
+                    for (int i = 0; i < 6 * kNT; ++i) {
+                        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+                    }
+                }
                 __builtin_amdgcn_sched_barrier(0);
             }
             buf ^= 1;
