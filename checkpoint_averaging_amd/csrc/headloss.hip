@@ -13,6 +13,7 @@
 #include "few.h"
 #include "head.h"
 #include "head_device.h"
+#include "narrow.h"
 #include "tiles.h"
 
 #pragma clang fp contract(off)
@@ -74,7 +75,8 @@ struct StatsTile {
             for (int q = 0; q < kMine; ++q) {
                 const float d = v[q] - from, x = exp_of(d);
                 s += x;
-                dot += x > 0 ? x * d : (x != x ? x : 0.0f);
+                // (a masked token's d is -infinity and its x 0, of which the product is to be 0)
+                dot = __builtin_fmaf(x, fmaxf(d, -0x1.fffffep+127f), dot);
             }
             s += __shfl_xor(s, 32);
             dot += __shfl_xor(dot, 32);
@@ -303,7 +305,8 @@ struct GatherArgs {
     const Selected* selected;
     void* to;
     int64_t ldto;
-    RowTerms* terms;
+    RowTerms* terms;                      // or nullptr: narrow ones, kNarrowTerms x rows
+    float* narrow;
     void* p;                              // dlogits of a piece, and where its last one's rows end
     int64_t ldp, p_end;
 };
@@ -321,7 +324,7 @@ template <typename T> __global__ __launch_bounds__(256) void k_gather(GatherArgs
             store8(to, c, a.width, v);
         }
         // (zeros up to a multiple of 8: the products with dlogits read that far)
-        if (threadIdx.x < 8 && a.p_end + threadIdx.x < a.ldp)
+        if (a.terms != nullptr && threadIdx.x < 8 && a.p_end + threadIdx.x < a.ldp)
             static_cast<T*>(a.p)[j * a.ldp + a.p_end + threadIdx.x] = from_f32<T>(0.0f);
         if (threadIdx.x == 0) {
             const int64_t t = a.targets[row];
@@ -332,7 +335,16 @@ template <typename T> __global__ __launch_bounds__(256) void k_gather(GatherArgs
             r.b = a.dentropy != nullptr ? a.dentropy[row] / unit : 0.0f;
             r.entropy = a.dentropy != nullptr ? a.entropy[row] : 0.0f;
             r.target = t < 0 || t >= a.vocab ? -1 : static_cast<int32_t>(t);
-            a.terms[j] = r;
+            if (a.terms != nullptr) {
+                a.terms[j] = r;
+            } else {
+                const float m = r.m == -__builtin_inff() ? 0.0f : r.m;
+                a.narrow[j] = (m + r.log_s) * kLog2e;
+                a.narrow[a.rows + j] = -r.a;
+                a.narrow[2 * a.rows + j] = __int_as_float(r.target);
+                a.narrow[3 * a.rows + j] = m;
+                a.narrow[4 * a.rows + j] = r.log_s;
+            }
         }
     }
 }
@@ -468,7 +480,7 @@ struct Backward {
     int64_t index, where, selected, terms, x, p, sums, sums_e, bytes;      // places in the workspace
 };
 
-constexpr int64_t kPieceBytes = int64_t(128) << 20;
+constexpr int64_t kPieceBytes = int64_t(128) << 20, kNarrowPiece = int64_t(1) << 18;
 
 Backward backward_plan(int64_t rows, int64_t vocab, int64_t width, int64_t esize) {
     Backward b{};
@@ -504,6 +516,42 @@ Backward backward_plan(int64_t rows, int64_t vocab, int64_t width, int64_t esize
     b.p = take(rows * b.ld_p * esize);
     b.sums = take(b.slices * rows * b.ld_s * 4);
     b.sums_e = b.slices_e == 1 ? at : take(b.slices_e * b.widest * b.ld_s * 4);
+    b.bytes = at;
+    return b;
+}
+
+// The same for rows of 128 numbers at most, whose products take no more time than the gradient
+// in the logits takes to be written and read twice.
+struct Narrow {
+    int64_t ld_x, ld_s, piece;            // of the vocabulary, for dembed
+    int slices, slices_e;                 // of the vocabulary for dx, of the rows for dembed
+    int64_t index, where, selected, terms, x, sums, bytes;
+};
+
+Narrow narrow_plan(int64_t rows, int64_t vocab, int64_t width) {
+    Narrow b{};
+    b.ld_x = up(width, 8);
+    b.ld_s = up(width, 4);
+    b.piece = vocab < kNarrowPiece ? vocab : kNarrowPiece;
+    auto cut = [](int64_t still) {
+        const int64_t tiles = (still + kNarrowStill - 1) / kNarrowStill;
+        return static_cast<int>(tiles > 128 ? 1 : 256 / tiles > 64 ? 64 : 256 / tiles);
+    };
+    b.slices = cut(rows);
+    b.slices_e = cut(b.piece);
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += up(bytes, 256);
+        return here;
+    };
+    b.index = take(4 * rows);
+    b.where = take(4 * rows);
+    b.selected = take(sizeof(Selected));
+    b.terms = take(4 * kNarrowTerms * rows);
+    b.x = take(2 * rows * b.ld_x);
+    const int64_t of_x = b.slices * rows, of_e = b.slices_e * b.piece;
+    b.sums = take((of_x > of_e ? of_x : of_e) * b.ld_s * 4);
     b.bytes = at;
     return b;
 }
@@ -567,12 +615,68 @@ hipError_t join_slices(const float* sums, int slices, int64_t apart, int64_t lds
     return hipGetLastError();
 }
 
+// The rows that take part, and the largest weight; then their inputs and terms.
+template <typename T> hipError_t collect(const HeadBackwardArgs& a, const GatherArgs& g, int* index,
+                                         int* where, Selected* selected, hipStream_t s) {
+    k_select<<<dim3(1), dim3(kSelectThreads), 0, s>>>(a.targets, a.dlogprobs, a.dentropy, a.rows,
+                                                      index, where, selected);
+    if (const hipError_t st = hipGetLastError(); st != hipSuccess) return st;
+    const unsigned walkers = static_cast<unsigned>(a.rows < 2048 ? a.rows : 2048);
+    k_gather<T><<<dim3(walkers), dim3(256), 0, s>>>(g);
+    return hipGetLastError();
+}
+
+hipError_t narrow_backward(const HeadBackwardArgs& a, hipStream_t s) {
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    const Narrow b = narrow_plan(a.rows, a.vocab, a.width);
+    int* index = reinterpret_cast<int*>(ws + b.index);
+    int* where = reinterpret_cast<int*>(ws + b.where);
+    Selected* selected = reinterpret_cast<Selected*>(ws + b.selected);
+    float* terms = reinterpret_cast<float*>(ws + b.terms);
+    bf16* x = reinterpret_cast<bf16*>(ws + b.x);
+    float* sums = reinterpret_cast<float*>(ws + b.sums);
+    const int width = static_cast<int>(a.width);
+    const GatherArgs g{a.x,     a.ldx,     a.rows,      a.vocab,    width, a.targets,
+                       a.stats, nullptr,   a.dlogprobs, nullptr,    index, selected,
+                       x,       b.ld_x,    nullptr,     terms,      nullptr, 0, 0};
+    hipError_t st = collect<bf16>(a, g, index, where, selected, s);
+    if (st != hipSuccess) return st;
+    const bf16* embed = static_cast<const bf16*>(a.embed);
+    auto tiles = [](int64_t still) { return (still + kNarrowStill - 1) / kNarrowStill; };
+    if (a.dx != nullptr) {
+        const NarrowArgs k{x,        b.ld_x,   a.rows,           embed, a.lde, a.vocab, width,
+                           b.slices, &selected->count, 0, {terms, a.rows}, sums, b.ld_s};
+        k_narrow<true><<<dim3(static_cast<unsigned>(tiles(a.rows) * b.slices)), dim3(kTileThreads), 0,
+                         s>>>(k);
+        if ((st = hipGetLastError()) != hipSuccess) return st;
+        st = join_slices<bf16>(sums, b.slices, a.rows, b.ld_s, a.rows, a.width, where, selected,
+                               static_cast<bf16*>(a.dx), a.lddx, s);
+        if (st != hipSuccess) return st;
+    }
+    if (a.dembed == nullptr) return hipSuccess;
+    for (int64_t v0 = 0; v0 < a.vocab; v0 += b.piece) {
+        const int64_t n = a.vocab - v0 < b.piece ? a.vocab - v0 : b.piece;
+        const NarrowArgs k{embed + v0 * a.lde, a.lde, n, x, b.ld_x, a.rows, width,
+                           b.slices_e, &selected->count, v0, {terms, a.rows}, sums, b.ld_s};
+        k_narrow<false><<<dim3(static_cast<unsigned>(tiles(n) * b.slices_e)), dim3(kTileThreads), 0,
+                          s>>>(k);
+        if ((st = hipGetLastError()) != hipSuccess) return st;
+        st = join_slices<bf16>(sums, b.slices_e, n, b.ld_s, n, a.width, nullptr, selected,
+                               static_cast<bf16*>(a.dembed) + v0 * a.ldde, a.ldde, s);
+        if (st != hipSuccess) return st;
+    }
+    return hipSuccess;
+}
+
 template <typename T> hipError_t backward(const HeadBackwardArgs& a, hipStream_t s) {
     if (a.rows == 0) {
         const ProductArgs none{nullptr, 0, nullptr, 0, a.width, a.vocab, 0, 1, nullptr, false};
         return product_of<T, true, true>(
             none, UnitTile<T>{static_cast<T*>(a.dembed), a.ldde, nullptr}, s);
     }
+    if constexpr (sizeof(T) == 2)
+        if (a.width <= kNarrow && a.dentropy == nullptr && direct(a.embed, a.lde, 2, a.width))
+            return narrow_backward(a, s);
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     const Backward b = backward_plan(a.rows, a.vocab, a.width, sizeof(T));
     int* index = reinterpret_cast<int*>(ws + b.index);
@@ -584,17 +688,12 @@ template <typename T> hipError_t backward(const HeadBackwardArgs& a, hipStream_t
     T* p = reinterpret_cast<T*>(ws + b.p);
     float* sums = reinterpret_cast<float*>(ws + b.sums);
     float* sums_e = reinterpret_cast<float*>(ws + b.sums_e);
-    k_select<<<dim3(1), dim3(kSelectThreads), 0, s>>>(a.targets, a.dlogprobs, a.dentropy, a.rows,
-                                                      index, where, selected);
-    hipError_t st = hipGetLastError();
-    if (st != hipSuccess) return st;
-    const unsigned walkers = static_cast<unsigned>(a.rows < 2048 ? a.rows : 2048);
     const GatherArgs g{a.x,       a.ldx,      a.rows, a.vocab, static_cast<int>(a.width),
                        a.targets, a.stats,    a.entropy, a.dlogprobs, a.dentropy,
-                       index,     selected,   x,      b.ld_x,  terms,
+                       index,     selected,   x,      b.ld_x,  terms, nullptr,
                        p,         b.ld_p,     b.widest};
-    k_gather<T><<<dim3(walkers), dim3(256), 0, s>>>(g);
-    if ((st = hipGetLastError()) != hipSuccess) return st;
+    hipError_t st = collect<T>(a, g, index, where, selected, s);
+    if (st != hipSuccess) return st;
     for (int64_t i = 0; i < b.pieces; ++i) {
         const int64_t v0 = i * b.piece;
         const int64_t n = i + 1 < b.pieces ? b.piece : a.vocab - v0;
@@ -644,7 +743,11 @@ int64_t head_workspace_bytes(int64_t rows, int64_t vocab, int64_t width, int dty
     const int64_t fwd =
         up(4 * rows, 256) + up(parts * rows * static_cast<int64_t>(sizeof(Part)), 256);
     if (!with_backward) return fwd;
-    const int64_t bwd = backward_plan(rows, vocab, width, dtype == DL_BF16 ? 2 : 4).bytes;
+    int64_t bwd = backward_plan(rows, vocab, width, dtype == DL_BF16 ? 2 : 4).bytes;
+    if (dtype == DL_BF16 && width <= kNarrow) {
+        const int64_t narrow = narrow_plan(rows, vocab, width).bytes;
+        bwd = bwd > narrow ? bwd : narrow;
+    }
     return fwd > bwd ? fwd : bwd;
 }
 
