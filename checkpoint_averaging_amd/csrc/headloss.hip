@@ -4,6 +4,21 @@
 //   l = x E^T ; m = max l ; S = sum exp(l - m)
 //   log p_t = (l_t - m) - log S ;  H = log S - sum exp(l - m)(l - m) / S
 //   d = a (delta_t - p) - b p (log p + H) ;  dx = d E ;  dE = d^T x
+//
+// Forward: E's product with x tile by tile (tiles.h), from whose registers a wave leaves the
+// m, S and sum of a span of the vocabulary for each token, joined by a second launch.  2048
+// tokens x 73760 x 2048 in bf16: 0.54 ms, 1.14 PFLOP/s, of which 13 us join the parts; the
+// matrix cores' power bounds it (a loop of nothing but these instructions reaches 1.8).  In
+// fp32, six bf16 products for one: 3.3 ms, 187 TFLOP/s.  Up to 32 tokens read E once, straight
+// into registers (few.h): one token 69 us, 4.4 TB/s; 33 tokens in a tile of 256 take 103.
+//
+// Backward: the rows that have a part are gathered first, so that a product has as many
+// columns as there are of them (a masked-token loss has a target at some 15 in 100 positions);
+// then the logits again, piece by piece of the vocabulary (128 MB of d at a time: with 72 the
+// products' last tiles cost 0.6 in 100 more, with 48 17 in 100; with 256 3 in 100 more here,
+// and 8 less at a width of 128), d in memory, and its two products.  2048 rows x 73760 x 2048
+// in bf16: 2.23 ms for 1.86 TFLOP.  Rows of at most 128 numbers keep d in registers
+// (narrow.h).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -22,7 +37,7 @@ namespace dlk {
 
 namespace {
 
-constexpr float kLog2e = 0x1.715476p+0f;
+constexpr float kLog2e = 0x1.715476p+0f, kLn2 = 0x1.62e43p-1f;
 
 __device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
 
@@ -310,6 +325,8 @@ template <typename T> __global__ __launch_bounds__(256) void k_gather(GatherArgs
                 a.narrow[2 * a.rows + j] = __int_as_float(r.target);
                 a.narrow[3 * a.rows + j] = m;
                 a.narrow[4 * a.rows + j] = r.log_s;
+                a.narrow[5 * a.rows + j] = -r.a - r.b * r.entropy;
+                a.narrow[6 * a.rows + j] = -r.b * kLn2;
             }
         }
     }
@@ -603,7 +620,7 @@ hipError_t narrow_backward(const HeadBackwardArgs& a, hipStream_t s) {
     float* sums = reinterpret_cast<float*>(ws + b.sums);
     const int width = static_cast<int>(a.width);
     const GatherArgs g{a.x,     a.ldx,     a.rows,      a.vocab,    width, a.targets,
-                       a.stats, nullptr,   a.dlogprobs, nullptr,    index, selected,
+                       a.stats, a.entropy, a.dlogprobs, a.dentropy, index, selected,
                        x,       b.ld_x,    nullptr,     terms,      nullptr, 0, 0};
     hipError_t st = collect<bf16>(a, g, index, where, selected, s);
     if (st != hipSuccess) return st;
@@ -612,8 +629,8 @@ hipError_t narrow_backward(const HeadBackwardArgs& a, hipStream_t s) {
     if (a.dx != nullptr) {
         const NarrowArgs k{x,        b.ld_x,   a.rows,           embed, a.lde, a.vocab, width,
                            b.slices, &selected->count, 0, {terms, a.rows}, sums, b.ld_s};
-        k_narrow<true><<<dim3(static_cast<unsigned>(tiles(a.rows) * b.slices)), dim3(kTileThreads), 0,
-                         s>>>(k);
+        (a.dentropy != nullptr ? k_narrow<true, true> : k_narrow<true, false>)
+            <<<dim3(static_cast<unsigned>(tiles(a.rows) * b.slices)), dim3(kTileThreads), 0, s>>>(k);
         if ((st = hipGetLastError()) != hipSuccess) return st;
         st = join_slices<bf16>(sums, b.slices, a.rows, b.ld_s, a.rows, a.width, where, selected,
                                static_cast<bf16*>(a.dx), a.lddx, s);
@@ -624,8 +641,8 @@ hipError_t narrow_backward(const HeadBackwardArgs& a, hipStream_t s) {
         const int64_t n = a.vocab - v0 < b.piece ? a.vocab - v0 : b.piece;
         const NarrowArgs k{embed + v0 * a.lde, a.lde, n, x, b.ld_x, a.rows, width,
                            b.slices_e, &selected->count, v0, {terms, a.rows}, sums, b.ld_s};
-        k_narrow<false><<<dim3(static_cast<unsigned>(tiles(n) * b.slices_e)), dim3(kTileThreads), 0,
-                          s>>>(k);
+        (a.dentropy != nullptr ? k_narrow<false, true> : k_narrow<false, false>)
+            <<<dim3(static_cast<unsigned>(tiles(n) * b.slices_e)), dim3(kTileThreads), 0, s>>>(k);
         if ((st = hipGetLastError()) != hipSuccess) return st;
         st = join_slices<bf16>(sums, b.slices_e, n, b.ld_s, n, a.width, nullptr, selected,
                                static_cast<bf16*>(a.dembed) + v0 * a.ldde, a.ldde, s);
@@ -641,10 +658,10 @@ template <typename T> hipError_t backward(const HeadBackwardArgs& a, hipStream_t
             none, UnitTile<T>{static_cast<T*>(a.dembed), a.ldde, nullptr}, s);
     }
     if constexpr (sizeof(T) == 2)
-        // (in time against the general form's: 0.56 to 1.21 ms for 8191 tokens x 50304 x 128,
-        // 0.48 to 1.04 with a width of 16, 0.079 to 0.149 for 100 tokens; 0.077 to 0.067 for 100
-        // x 1000, whose time is their launches')
-        if (a.width <= kNarrow && a.dentropy == nullptr && direct(a.embed, a.lde, 2, a.width))
+        // (0.56 ms against the general form's 1.21 for 8191 tokens x 50304 x 128, 0.48 against
+        // 1.04 with a width of 16, 0.079 against 0.149 for 100 tokens; 0.077 against 0.067 for
+        // 100 x 1000, whose time is launches)
+        if (a.width <= kNarrow && direct(a.embed, a.lde, 2, a.width))
             return narrow_backward(a, s);
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     const Backward b = backward_plan(a.rows, a.vocab, a.width, sizeof(T));

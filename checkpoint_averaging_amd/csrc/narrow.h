@@ -2,7 +2,7 @@
 // the logits goes from the registers that hold the logits straight into its product, and no
 // part of it through memory.
 //
-//   l = still . moving ;  p = exp(l - m - log S) ;  d = -a (p - delta_t)
+//   l = still . moving ;  p = exp(l - m - log S) ;  d = -a (p - delta_t) - b p (log p + H)
 //   sums = sum over the moving rows of d times them
 //
 // for dx (tokens still, the vocabulary moving past them) and for dembed (the other way
@@ -10,7 +10,13 @@
 // LDS has units of 128, four in turn, sent for three units ahead; each is read along its
 // rows for the logits and across them for the sums.  The first product leaves a lane 16 of
 // 32 moving rows in its column, which is what the second one takes of its own operand if the
-// rows are counted in that order.
+// rows are counted in that order.  d is rounded to bf16 for it, as the general form's is.
+//
+// 8191 tokens x 50304 x 128: dx 0.21 ms, dembed 0.28 (with an entropy's gradient 0.22 and
+// 0.29), 0.21 TFLOP each: 0.75 to 1 PFLOP/s, which the exponentials and conversions between
+// the products bound (some 8 vector instructions an element beside its two matrix
+// instructions' share).  Through memory the gradient in the logits was 824 MB written and
+// twice read, and the two and its own product took 1.1 ms.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -24,10 +30,11 @@ namespace dlk {
 constexpr int kNarrow = 128;             // elements of a row, with zeros from its width on
 constexpr int kNarrowStill = kTileWaves * kSquare, kNarrowUnit = 128;
 constexpr int kNarrowRing = 4, kNarrowBytes = kNarrowUnit * kNarrow * 2;
-constexpr int kNarrowTerms = 5;
+constexpr int kNarrowTerms = 7;
 
 // A row's terms, an array of `rows` for each: (m + log S) log2(e), -a, its target (or -1),
-// m (0 if that is -infinity), log S.
+// m (0 if that is -infinity), log S; and, with a gradient b of the entropies, -a - b H and
+// -b log(2): d = p (one + other log2(p)) + a delta_t.
 struct NarrowTerms {
     const float* of;
     int64_t rows;
@@ -54,7 +61,7 @@ struct NarrowArgs {
 // rows, meet all banks.
 __device__ __forceinline__ int narrow_key(int row) { return (row & 3) << 2 | (row >> 2 & 3); }
 
-template <bool TOKENS_STILL>
+template <bool TOKENS_STILL, bool ENTROPY>
 __global__ __launch_bounds__(kTileThreads, 2) void k_narrow(NarrowArgs a) {
     constexpr float kLog2e = 0x1.715476p+0f;
     constexpr int kSubs = kNarrow / 16, kWide = kNarrow / kSquare, kMine = kNarrowBytes / 16 / kTileThreads;
@@ -89,7 +96,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_narrow(NarrowArgs a) {
                           static_cast<int64_t>(from) * row_bytes;
     const float* term_base = a.terms.of + from;
     const uint32_t term_offset = static_cast<uint32_t>(threadIdx.x % kNarrowUnit) * 4;
-    // (a wave's places are of half of a term; of terms 5 to 7, which there are not, zeros)
+    // (a wave's places are of half of a term)
     const float* term_of = term_base + wave / 2 * a.terms.rows;
     int left = rows;                      // not sent for yet
     auto fetch = [&](int slot) {
@@ -108,7 +115,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_narrow(NarrowArgs a) {
                 const_cast<float*>(term_of), 0, have * 4, 0x00020000);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(t, (lds_any*)to, 4, term_offset, 0, 0, 0);
             t = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(term_of + 4 * a.terms.rows), 0,
-                                                  wave < 2 ? have * 4 : 0, 0x00020000);
+                                                  wave < (ENTROPY ? 6 : 2) ? have * 4 : 0, 0x00020000);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(t, (lds_any*)(to + 4 * kNarrowUnit), 4,
                                                      term_offset, 0, 0, 0);
             term_of += kNarrowUnit;
@@ -125,7 +132,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_narrow(NarrowArgs a) {
             v = *reinterpret_cast<const u32x4*>(a.still + n * a.ld_still + k);
         still[s] = __builtin_bit_cast(bf16x8, v);
     }
-    float base2 = 0, mine = 0, top = 0, log_s = 0;
+    float base2 = 0, mine = 0, top = 0, log_s = 0, one = 0, other = 0;
     int target = -1;
     if constexpr (TOKENS_STILL) {
         if (there) {
@@ -134,10 +141,22 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_narrow(NarrowArgs a) {
             target = __float_as_int(a.terms.get(2, n)) - from;
             top = a.terms.get(3, n);
             log_s = a.terms.get(4, n);
+            if constexpr (ENTROPY) {
+                one = a.terms.get(5, n);
+                other = a.terms.get(6, n);
+            }
         }
     }
     const int id = static_cast<int>(a.first) + n;             // of this lane's row of the vocabulary
     __builtin_amdgcn_s_waitcnt(0x0070);                       // (none of these counts below)
+
+    // log2(p) of a logit, and what p is multiplied by in d.  (A still token's -a alone is a
+    // factor of its sums.)
+    auto power = [&](float l, float base) { return __builtin_fmaf(l, kLog2e, -base); };
+    // (log2(p) is -infinity where p is 0)
+    auto weight = [](float log2p, float f0, float f1) {
+        return __builtin_fmaf(f1, fmaxf(log2p, -0x1p+100f), f0);
+    };
 
     // Moving row `row` of a slot along its width, and four of them across it: columns of tile w.
     auto along = [&](const uint8_t* l, int row, int sub) {
@@ -175,13 +194,24 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_narrow(NarrowArgs a) {
                 // element i is of row row0 + 8 (i / 4) + 4 half + i % 4
                 float v[16];
                 if constexpr (TOKENS_STILL) {
-                    for (int i = 0; i < 16; ++i)
-                        v[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i], kLog2e, -base2));
+                    for (int i = 0; i < 16; ++i) {
+                        const float e = power(s[t][i], base2);
+                        v[i] = __builtin_amdgcn_exp2f(e);
+                        if constexpr (ENTROPY) v[i] *= weight(e, one, other);
+                    }
                     const int at = target - u * kNarrowUnit - row0;
                     if (__any(at >= 0 && at < 32)) {
                         for (int i = 0; i < 16; ++i)
-                            if (at == 8 * (i / 4) + 4 * half + i % 4)
-                                v[i] = expm1f((s[t][i] - top) - log_s);
+                            if (at == 8 * (i / 4) + 4 * half + i % 4) {
+                                const float less = expm1f((s[t][i] - top) - log_s);
+                                if constexpr (ENTROPY) {
+                                    const float e = power(s[t][i], base2);
+                                    v[i] = mine * less + __builtin_amdgcn_exp2f(e) *
+                                                             weight(e, one - mine, other);
+                                } else {
+                                    v[i] = less;
+                                }
+                            }
                     }
                 } else {
                     const auto& terms = lds_terms[slot];
@@ -189,32 +219,47 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_narrow(NarrowArgs a) {
                     for (int q = 0; q < 4; ++q) {
                         const int r = row0 + 8 * q + 4 * half;
                         const f32x4 b = *reinterpret_cast<const f32x4*>(&terms[0][r]);
-                        w[q] = *reinterpret_cast<const f32x4*>(&terms[1][r]);
-                        for (int j = 0; j < 4; ++j)
-                            v[4 * q + j] = __builtin_amdgcn_exp2f(
-                                __builtin_fmaf(s[t][4 * q + j], kLog2e, -b[j]));
+                        w[q] = *reinterpret_cast<const f32x4*>(&terms[ENTROPY ? 5 : 1][r]);
+                        f32x4 f{};
+                        if constexpr (ENTROPY) f = *reinterpret_cast<const f32x4*>(&terms[6][r]);
+                        for (int j = 0; j < 4; ++j) {
+                            const float e = power(s[t][4 * q + j], b[j]);
+                            v[4 * q + j] = __builtin_amdgcn_exp2f(e);
+                            if constexpr (ENTROPY) w[q][j] = weight(e, w[q][j], f[j]);
+                        }
                     }
+                    // -a of the targets more; where p is near 1, and little is left of both, the
+                    // two by themselves
                     const int near = __float_as_int(terms[2][row0 + lane % 32]) - (id - lane % 32);
-                    if (__any(near >= 0 && near < 32)) {
-                        // p - 1 of the targets; near 1, where it has few digits left, by itself
-                        uint32_t hits = 0;
-                        bool certain = false;
+                    const bool hits = __any(near >= 0 && near < 32);
+                    uint32_t certain = 0;
+                    if (hits) {
                         for (int i = 0; i < 16; ++i) {
                             const int r = row0 + 8 * (i / 4) + 4 * half + i % 4;
                             const bool hit = __float_as_int(terms[2][r]) == id;
-                            certain |= hit && v[i] > 1 - 0x1p-6f;
-                            hits |= hit ? 1u << i : 0;
-                            v[i] -= hit ? 1.0f : 0.0f;
-                        }
-                        if (__any(certain)) {
-                            for (int i = 0; i < 16; ++i) {
-                                const int r = row0 + 8 * (i / 4) + 4 * half + i % 4;
-                                if (hits >> i & 1)
-                                    v[i] = expm1f((s[t][i] - terms[3][r]) - terms[4][r]);
+                            certain |= hit && v[i] > 1 - 0x1p-6f ? 1u << i : 0;
+                            if constexpr (ENTROPY) {
+                                v[i] = __builtin_fmaf(v[i], w[i / 4][i % 4], hit ? -terms[1][r] : 0);
+                            } else {
+                                v[i] = (v[i] - (hit ? 1.0f : 0.0f)) * w[i / 4][i % 4];
                             }
                         }
+                        if (__any(certain != 0)) {
+                            for (int i = 0; i < 16; ++i) {
+                                const int r = row0 + 8 * (i / 4) + 4 * half + i % 4;
+                                if (!(certain >> i & 1)) continue;
+                                v[i] = terms[1][r] *
+                                       expm1f((s[t][i] - terms[3][r]) - terms[4][r]);
+                                if constexpr (ENTROPY) {
+                                    const float e = power(s[t][i], terms[0][r]);
+                                    v[i] += __builtin_amdgcn_exp2f(e) *
+                                            weight(e, terms[5][r] - terms[1][r], terms[6][r]);
+                                }
+                            }
+                        }
+                    } else {
+                        for (int i = 0; i < 16; ++i) v[i] *= w[i / 4][i % 4];
                     }
-                    for (int i = 0; i < 16; ++i) v[i] *= w[i / 4][i % 4];
                 }
                 // (zeros stand for rows past the end, but what becomes of them need not be finite)
                 const int end = rows - u * kNarrowUnit - row0;
@@ -247,7 +292,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_narrow(NarrowArgs a) {
             const int c = w * kSquare + 8 * q + 4 * half;
             if (c >= a.width) continue;
             f32x4 v;
-            for (int j = 0; j < 4; ++j) v[j] = acc[w][4 * q + j] * (TOKENS_STILL ? mine : 1.0f);
+            for (int j = 0; j < 4; ++j) v[j] = acc[w][4 * q + j] * (TOKENS_STILL && !ENTROPY ? mine : 1.0f);
             *reinterpret_cast<f32x4*>(to + c) = v;
         }
 }

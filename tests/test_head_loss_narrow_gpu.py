@@ -18,12 +18,13 @@ DEV = "cuda"
 @pytest.mark.parametrize("rows,vocab,width", [
     (2, 31, 8), (127, 33, 128), (128, 128, 128), (129, 257, 120), (255, 65, 16),
     (256, 256, 64), (257, 1025, 128), (513, 40, 104), (31, 5000, 128), (1500, 3001, 128)])
-def test_sizes_about_its_tiles(rows, vocab, width):
+@pytest.mark.parametrize("entropy", [False, True])
+def test_sizes_about_its_tiles(rows, vocab, width, entropy):
     rng = np.random.default_rng(rows + vocab)
     x, e, t = lg.inputs(rng, rows, vocab, width)
     t[:min(rows, 4)] = np.array([0, vocab - 1, vocab // 2, min(31, vocab - 1)])[:min(rows, 4)]
-    a, _ = lg.weights(rng, rows, False)
-    lg.Case(x, e, t, "bf16", 0, None, a).forward().backward().check_backward()
+    a, b = lg.weights(rng, rows, entropy)
+    lg.Case(x, e, t, "bf16", 0, b, a).forward().backward().check_backward()
 
 
 @pytest.mark.parametrize("pad", [8, 24])
@@ -37,8 +38,9 @@ def test_rows_apart(pad):
     c.backward(3, de=False).check_backward(de=False)
 
 
+@pytest.mark.parametrize("entropy", [False, True])
 @pytest.mark.parametrize("same", [False, True])
-def test_certain_tokens_keep_their_digits(same):
+def test_certain_tokens_keep_their_digits(same, entropy):
     """Rows that give their targets nearly all: 1 - p is far below p's last place."""
     rng = np.random.default_rng(3)
     rows, vocab, width = 150, 300, 128
@@ -46,11 +48,13 @@ def test_certain_tokens_keep_their_digits(same):
     t = np.full(rows, 77) if same else rng.integers(0, vocab, rows)
     lean = np.linspace(2, 30, rows)[:, None]
     x = (0.1 * x + lean * e[t] / (e[t] ** 2).sum(1, keepdims=True)).astype(np.float32)
-    a, _ = lg.weights(rng, rows, False)
-    c = lg.Case(x, e, t, "bf16", 0, None, a).forward().backward()
+    a, b = lg.weights(rng, rows, entropy)
+    c = lg.Case(x, e, t, "bf16", 0, b, a).forward().backward()
     p = np.exp(c.lp[np.arange(rows), t])
     assert (1 - p < 2.0 ** -12).sum() > 20 and (p < 0.9).sum() > 5
     c.check_backward()
+    if entropy:
+        return
     # one row at a time: relative to that row's own gradient, whose terms all have the size of
     # 1 - p; and a logit's own error moves log(1 - p) by as much
     for r in np.flatnonzero(1 - p < 2.0 ** -12)[::7]:
@@ -60,7 +64,8 @@ def test_certain_tokens_keep_their_digits(same):
         hg.within(hg.host(c.dx)[r:r + 1], d @ c.ev.astype(np.float64), off * mag + 1e-38, "dx")
 
 
-def test_logits_far_from_zero():
+@pytest.mark.parametrize("entropy", [False, True])
+def test_logits_far_from_zero(entropy):
     """Logits of -300 and less, and of 300: the rows' largest are subtracted before anything
     is raised, also for what lies past the vocabulary's or the tokens' end."""
     rng = np.random.default_rng(8)
@@ -69,27 +74,28 @@ def test_logits_far_from_zero():
     x[:, 0] = 0
     x[::2, 0], x[1::2, 0] = 300, -300
     e[:, 0] = 1
-    a, _ = lg.weights(rng, rows, False)
-    lg.Case(x, e, t, "bf16", 0, None, a).forward().backward().check_backward()
+    a, b = lg.weights(rng, rows, entropy)
+    lg.Case(x, e, t, "bf16", 0, b, a).forward().backward().check_backward()
 
 
-def test_masked_tokens_have_no_gradient():
+@pytest.mark.parametrize("entropy", [False, True])
+def test_masked_tokens_have_no_gradient(entropy):
     """Logits of -infinity: an embedding's row that holds it, where x is positive."""
     rng = np.random.default_rng(9)
     x, e, t = lg.inputs(rng, 70, 200, 64)
     x[:, 5] = np.abs(x[:, 5]) + 0.01
     masked = np.arange(3, 200, 11)
     t = np.where(np.isin(t, masked), 0, t)
-    a, _ = lg.weights(rng, 70, False)
+    a, b = lg.weights(rng, 70, entropy)
     plain = e.copy()
     e[masked, 5] = -np.inf
     with np.errstate(invalid="ignore"):
-        c = lg.Case(x, e, t, "bf16", 0, None, a)
+        c = lg.Case(x, e, t, "bf16", 0, b, a)
     c.forward().backward(dx=False)
     # p is 0 there, and the others' are those of a vocabulary without them
     keep = np.setdiff1d(np.arange(200), masked)
     at = np.searchsorted(keep, t)
-    w = lg.Case(x, plain[keep], at, "bf16", 0, None, a)
+    w = lg.Case(x, plain[keep], at, "bf16", 0, b, a)
     w.err = lg.logit_error(w.xv, w.ev, "bf16")
     w.de = c.de[torch.from_numpy(keep).to(DEV)]
     w.check_backward(dx=False)
@@ -122,23 +128,31 @@ def test_vocabulary_in_pieces():
 def test_the_other_form_in_pieces():
     """The general form over several pieces of the vocabulary, in bf16."""
     rng = np.random.default_rng(12)
-    rows, vocab, width = 9000, 16_000, 32
+    rows, vocab, width = 9000, 16_000, 136
     x, e, t = lg.inputs(rng, rows, vocab, width)
     a, b = lg.weights(rng, rows, True)
     lg.Case(x, e, t, "bf16", 0, b, a).forward().backward().check_backward()
 
 
 def test_both_forms_agree():
-    """Weights of zero for the entropies take the general form: the same gradients, but for
-    the roundings of each."""
+    """Rows apart by an odd distance take the general form: the same gradients, but for the
+    roundings of each."""
     rng = np.random.default_rng(13)
     x, e, t = lg.inputs(rng, 300, 1200, 128)
-    a, _ = lg.weights(rng, 300, False)
-    c = lg.Case(x, e, t, "bf16", 0, None, a).forward().backward().check_backward()
-    g = lg.Case(x, e, t, "bf16", 0, np.zeros(300), a).forward().backward()
-    g.b = None
-    g.check_backward()
-    assert c.dx.shape == g.dx.shape
+    a, b = lg.weights(rng, 300, True)
+    lg.Case(x, e, t, "bf16", 0, b, a).forward().backward().check_backward()
+    lg.Case(x, e, t, "bf16", 1, b, a).forward().backward().check_backward()
+
+
+@pytest.mark.parametrize("width", [72, 128])
+def test_entropies_alone(width):
+    """Rows without a target, and weights of zero for the targets, beside others."""
+    rng = np.random.default_rng(width)
+    x, e, t = lg.inputs(rng, 140, 900, width)
+    a, b = lg.weights(rng, 140, True)
+    t[::2] = -1
+    a[1::4] = 0
+    lg.Case(x, e, t, "bf16", 0, b, a).forward().backward().check_backward()
 
 
 def test_graphs_replay_it_and_calls_repeat():
