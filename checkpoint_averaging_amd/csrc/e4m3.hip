@@ -16,6 +16,11 @@ namespace dlk {
 namespace {
 
 // ---- the layout --------------------------------------------------------------
+//
+// Bound by memory: an element is read once, its block's largest magnitude is found by a
+// reduction over lanes (and LDS, where a block has 128 rows), and its code and value are
+// written from the registers that held it.  73,760 x 2048 fp32 with values: 258 us (1.36 GB, 5.3
+// TB/s); 16,383 x 2048 bf16 in blocks of a row, with values: 32 us (5.3 TB/s).
 
 constexpr int kBlock = 128;
 constexpr int kThreads = 256;
@@ -119,6 +124,12 @@ template <typename T> __global__ __launch_bounds__(kThreads) void k_e4m3_tiles(Q
 // to 2.5e-5 of the result in the 2-norm whatever its width: little beside bf16's own rounding
 // (1.7e-3), too much for a binary32 result.  That one takes codes as bf16 numbers, which
 // they are exactly with their scales, at half the rate.
+//
+// 73,760 x 2048 with 2048 tokens: 0.58 ms in fp32 (1.06 PFLOP/s, as a bf16 product reaches), 0.35
+// in bf16 (1.76); 5632 x 2048 with 8191 tokens in bf16: 94 us, 2.0 PFLOP/s.  The power that the
+// matrix cores may take bounds the large ones: clocks fall from 2.4 GHz to 1.9.  Up to 32
+// tokens (few.h) read W once: one token 29 us, 5.2 TB/s; 32 tokens 37 against the tiles' 33 to
+// 40, and with 2048 rows, whose tiles are few, 19 against 33.
 
 template <typename Y> struct ProductTile : StoreTile<Y> {
     const uint8_t* w_scales;
@@ -266,9 +277,13 @@ hipError_t matmul_of(const E4m3ProductArgs& a, hipStream_t s) {
     const E e{StoreTile<Y>(a.y, a.ldy), a.w_scales, a.x_scales, (a.cols + kBlock - 1) / kBlock};
     if (a.count <= kFewTokens) return few_tokens<Y>(a, s);
     const dim3 block(kTileThreads);
-    // Few tiles: smaller ones, so that more CUs have some.
+    // Few tiles: smaller ones, so that more CUs have some (5632 rows x 2048, bf16 out: 512
+    // tokens 19.6 us against 28.4, 1024 31.8 against 30.3, 1600 47.8 against 32.5).  And while
+    // half of a large tile's tokens or more would be none (73,760 rows x 2048: 64 tokens 38 us
+    // against 98 in fp32; 128 tokens 52 against 57 and 160 63 against 58 in bf16, 192 89 against
+    // 106 and 256 126 against 111 in fp32, whose products take longer).
     const int64_t big = (a.rows + 255) / 256 * ((a.count + 255) / 256);
-    if (big >= 128) {
+    if (big >= 128 && a.count > (sizeof(Y) == 4 ? 192 : 128)) {
         const dim3 grid(product_grid(a.rows, a.count, 256, 256, 1, kTileGroups));
         if (direct(a.w, a.ldw, 1, a.cols) && direct(a.x, a.ldx, 1, a.cols))
             k_product_direct<ViaCodes, false, false, 256, 256, 2, 4, E, Math>
