@@ -13,7 +13,7 @@
 // into registers (few.h): one token 69 us, 4.4 TB/s; 33 tokens in a tile of 256 take 103.
 //
 // Backward: the rows that have a part are gathered first, so that a product has as many
-// columns as there are of them (a masked-token loss has a target at some 15 in 100 positions);
+// columns as there are of them (a masked-token loss has targets at its masked positions only);
 // then the logits again, piece by piece of the vocabulary (128 MB of d at a time: with 72 the
 // products' last tiles cost 0.6 in 100 more, with 48 17 in 100; with 256 3 in 100 more here,
 // and 8 less at a width of 128), d in memory, and its two products.  2048 rows x 73760 x 2048
@@ -379,13 +379,13 @@ template <typename T, bool ENTROPY> struct GradTile {
 // added up over its pieces.
 struct SumTile {
     float* sums;
-    int64_t rows, ld;
+    int64_t ld;
     bool first;
 
     template <int MT, int NT>
     __device__ __forceinline__ void finish(const f32x16 (&acc)[MT][NT], const Place& at) const {
         const int lane = lane_here();
-        float* to = sums + at.slice * rows * ld;
+        float* to = sums + at.slice * at.n * ld;
 #pragma unroll
         for (int u = 0; u < NT; ++u)
 #pragma unroll
@@ -400,13 +400,24 @@ struct SumTile {
 };
 
 // The slices' sums together, in the inputs' units: row i of out from row where[i] of the sums
-// (0 if that is -1), or with no `where` from row i.
+// (0 if that is -1), or with no `where` from row i.  With `where`, slices are as many as
+// cut_of gives for the selected rows' tiles, m_tiles for each 256 of them.
+struct Slices {
+    const float* sums;
+    int64_t ld;
+    int number, items, most, m_tiles;
+};
+
 template <typename T>
-__global__ __launch_bounds__(256) void k_join_slices(const float* sums, int slices, int64_t apart,
-                                                     int64_t lds, int64_t rows, int width,
+__global__ __launch_bounds__(256) void k_join_slices(Slices a, int64_t rows, int width,
                                                      const int* where, const Selected* selected,
                                                      T* out, int64_t ldo) {
     const float unit = selected->unit;
+    const float* sums = a.sums;
+    const int64_t lds = a.ld, apart = where != nullptr ? selected->count : rows;
+    const int slices = where != nullptr
+                           ? cut_of(tiles_of(selected->count) * a.m_tiles, a.items, a.most)
+                           : a.number;
     const int per = (width + 7) / 8;                       // groups of eight columns
     const int64_t all = rows * per;
     for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < all; i += gridDim.x * int64_t(256)) {
@@ -458,10 +469,19 @@ template <typename T> constexpr int span_of() { return sizeof(T) == 2 ? kSpan : 
 struct Backward {
     int64_t piece, pieces;                // of the vocabulary; the last takes the rest
     int64_t ld_p, ld_x, ld_s;
-    int slices, slices_e;                 // of the vocabulary for dx, of the rows for dembed
+    int items, slices;                    // of the vocabulary for dx (of all rows: fewer have more)
+    int slices_e;                         // of the rows for dembed
     int64_t widest;                       // piece
     int64_t index, where, selected, terms, x, p, sums, sums_e, bytes;      // places in the workspace
 };
+
+int items_of(int64_t tiles) { return static_cast<int>(tiles > 128 ? tiles : 256); }
+
+// Rows of sums that the slices of up to `rows` rows need.
+int64_t slice_rows(int64_t rows, int items, int most, int64_t m_tiles) {
+    const int64_t all = items / m_tiles, cut = most * tiles_of(rows);
+    return 256 * (all < cut ? all : cut);
+}
 
 constexpr int64_t kPieceBytes = int64_t(128) << 20, kNarrowPiece = int64_t(1) << 18;
 
@@ -479,12 +499,13 @@ Backward backward_plan(int64_t rows, int64_t vocab, int64_t width, int64_t esize
     b.ld_p = up(b.widest, 8);
     b.ld_x = up(width, 8);
     b.ld_s = up(width, 4);
-    // Products of few tiles are cut along k, so that every CU has some.
-    auto cut = [](int64_t tiles) {
-        return static_cast<int>(tiles > 128 ? 1 : 256 / tiles > 16 ? 16 : 256 / tiles);
-    };
-    b.slices = cut(up(width, 256) / 256 * (up(rows, 256) / 256));
-    b.slices_e = cut(up(width, 256) / 256 * (up(b.widest, 256) / 256));
+    // Products of few tiles are cut along k, so that every CU has some (333 rows x 73,760 x 2048
+    // in bf16: 2.60 ms whole, 0.62 so).
+    const int64_t m_tiles = tiles_of(width), tiles = m_tiles * tiles_of(rows);
+    b.items = items_of(tiles);
+    b.slices = cut_of(tiles, b.items, kMostSlices);
+    const int64_t tiles_e = m_tiles * tiles_of(b.widest);
+    b.slices_e = cut_of(tiles_e, items_of(tiles_e), kMostSlices);
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t here = at;
@@ -497,7 +518,7 @@ Backward backward_plan(int64_t rows, int64_t vocab, int64_t width, int64_t esize
     b.terms = take(static_cast<int64_t>(sizeof(RowTerms)) * rows);
     b.x = take(rows * b.ld_x * esize);
     b.p = take(rows * b.ld_p * esize);
-    b.sums = take(b.slices * rows * b.ld_s * 4);
+    b.sums = take(slice_rows(rows, b.items, kMostSlices, m_tiles) * b.ld_s * 4);
     b.sums_e = b.slices_e == 1 ? at : take(b.slices_e * b.widest * b.ld_s * 4);
     b.bytes = at;
     return b;
@@ -507,7 +528,7 @@ Backward backward_plan(int64_t rows, int64_t vocab, int64_t width, int64_t esize
 // in the logits takes to be written and read twice.
 struct Narrow {
     int64_t ld_x, ld_s, piece;            // of the vocabulary, for dembed
-    int slices, slices_e;                 // of the vocabulary for dx, of the rows for dembed
+    int items, slices, slices_e;          // as above
     int64_t index, where, selected, terms, x, sums, bytes;
 };
 
@@ -516,12 +537,9 @@ Narrow narrow_plan(int64_t rows, int64_t vocab, int64_t width) {
     b.ld_x = up(width, 8);
     b.ld_s = up(width, 4);
     b.piece = vocab < kNarrowPiece ? vocab : kNarrowPiece;
-    auto cut = [](int64_t still) {
-        const int64_t tiles = (still + kNarrowStill - 1) / kNarrowStill;
-        return static_cast<int>(tiles > 128 ? 1 : 256 / tiles > 64 ? 64 : 256 / tiles);
-    };
-    b.slices = cut(rows);
-    b.slices_e = cut(b.piece);
+    b.items = items_of(tiles_of(rows));
+    b.slices = cut_of(tiles_of(rows), b.items, kNarrowSlices);
+    b.slices_e = cut_of(tiles_of(b.piece), items_of(tiles_of(b.piece)), kNarrowSlices);
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t here = at;
@@ -533,7 +551,7 @@ Narrow narrow_plan(int64_t rows, int64_t vocab, int64_t width) {
     b.selected = take(sizeof(Selected));
     b.terms = take(4 * kNarrowTerms * rows);
     b.x = take(2 * rows * b.ld_x);
-    const int64_t of_x = b.slices * rows, of_e = b.slices_e * b.piece;
+    const int64_t of_x = slice_rows(rows, b.items, kNarrowSlices, 1), of_e = b.slices_e * b.piece;
     b.sums = take((of_x > of_e ? of_x : of_e) * b.ld_s * 4);
     b.bytes = at;
     return b;
@@ -577,7 +595,7 @@ template <typename T> hipError_t forward(const HeadArgs& a, hipStream_t s) {
     } else {
         const StatsTile e{parts, a.rows, a.targets, at_target};
         const ProductArgs p{a.embed, a.lde, a.x, a.ldx, a.vocab, a.rows, a.width, 1, nullptr,
-                            false};
+                            false, 0};
         n_parts = static_cast<int>((a.vocab + span_of<T>() - 1) / span_of<T>());
         st = product_of<T, false, false>(p, e, s);
     }
@@ -589,12 +607,11 @@ template <typename T> hipError_t forward(const HeadArgs& a, hipStream_t s) {
 }
 
 template <typename T>
-hipError_t join_slices(const float* sums, int slices, int64_t apart, int64_t lds, int64_t rows,
-                       int64_t width, const int* where, const Selected* selected, T* out,
-                       int64_t ldo, hipStream_t s) {
+hipError_t join_slices(const Slices& a, int64_t rows, int64_t width, const int* where,
+                       const Selected* selected, T* out, int64_t ldo, hipStream_t s) {
     const int64_t blocks = (rows * ((width + 7) / 8) + 255) / 256;
     k_join_slices<T><<<dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s>>>(
-        sums, slices, apart, lds, rows, static_cast<int>(width), where, selected, out, ldo);
+        a, rows, static_cast<int>(width), where, selected, out, ldo);
     return hipGetLastError();
 }
 
@@ -625,15 +642,16 @@ hipError_t narrow_backward(const HeadBackwardArgs& a, hipStream_t s) {
     hipError_t st = collect<bf16>(a, g, index, where, selected, s);
     if (st != hipSuccess) return st;
     const bf16* embed = static_cast<const bf16*>(a.embed);
-    auto tiles = [](int64_t still) { return (still + kNarrowStill - 1) / kNarrowStill; };
+    static_assert(kNarrowStill == 256, "tiles_of counts them");
     if (a.dx != nullptr) {
-        const NarrowArgs k{x,        b.ld_x,   a.rows,           embed, a.lde, a.vocab, width,
-                           b.slices, &selected->count, 0, {terms, a.rows}, sums, b.ld_s};
+        const NarrowArgs k{x,       b.ld_x,           a.rows, embed,           a.lde, a.vocab, width,
+                           b.items, &selected->count, 0,      {terms, a.rows}, sums,  b.ld_s};
         (a.dentropy != nullptr ? k_narrow<true, true> : k_narrow<true, false>)
-            <<<dim3(static_cast<unsigned>(tiles(a.rows) * b.slices)), dim3(kTileThreads), 0, s>>>(k);
+            <<<dim3(static_cast<unsigned>(slice_rows(a.rows, b.items, kNarrowSlices, 1) / 256)),
+               dim3(kTileThreads), 0, s>>>(k);
         if ((st = hipGetLastError()) != hipSuccess) return st;
-        st = join_slices<bf16>(sums, b.slices, a.rows, b.ld_s, a.rows, a.width, where, selected,
-                               static_cast<bf16*>(a.dx), a.lddx, s);
+        st = join_slices<bf16>({sums, b.ld_s, 0, b.items, kNarrowSlices, 1}, a.rows, a.width, where,
+                               selected, static_cast<bf16*>(a.dx), a.lddx, s);
         if (st != hipSuccess) return st;
     }
     if (a.dembed == nullptr) return hipSuccess;
@@ -642,9 +660,9 @@ hipError_t narrow_backward(const HeadBackwardArgs& a, hipStream_t s) {
         const NarrowArgs k{embed + v0 * a.lde, a.lde, n, x, b.ld_x, a.rows, width,
                            b.slices_e, &selected->count, v0, {terms, a.rows}, sums, b.ld_s};
         (a.dentropy != nullptr ? k_narrow<false, true> : k_narrow<false, false>)
-            <<<dim3(static_cast<unsigned>(tiles(n) * b.slices_e)), dim3(kTileThreads), 0, s>>>(k);
+            <<<dim3(static_cast<unsigned>(tiles_of(n) * b.slices_e)), dim3(kTileThreads), 0, s>>>(k);
         if ((st = hipGetLastError()) != hipSuccess) return st;
-        st = join_slices<bf16>(sums, b.slices_e, n, b.ld_s, n, a.width, nullptr, selected,
+        st = join_slices<bf16>({sums, b.ld_s, b.slices_e, 0, 0, 0}, n, a.width, nullptr, selected,
                                static_cast<bf16*>(a.dembed) + v0 * a.ldde, a.ldde, s);
         if (st != hipSuccess) return st;
     }
@@ -653,7 +671,7 @@ hipError_t narrow_backward(const HeadBackwardArgs& a, hipStream_t s) {
 
 template <typename T> hipError_t backward(const HeadBackwardArgs& a, hipStream_t s) {
     if (a.rows == 0) {
-        const ProductArgs none{nullptr, 0, nullptr, 0, a.width, a.vocab, 0, 1, nullptr, false};
+        const ProductArgs none{nullptr, 0, nullptr, 0, a.width, a.vocab, 0, 1, nullptr, false, 0};
         return product_of<T, true, true>(
             none, UnitTile<T>{static_cast<T*>(a.dembed), a.ldde, nullptr}, s);
     }
@@ -684,7 +702,7 @@ template <typename T> hipError_t backward(const HeadBackwardArgs& a, hipStream_t
         const int64_t v0 = i * b.piece;
         const int64_t n = i + 1 < b.pieces ? b.piece : a.vocab - v0;
         const T* embed = static_cast<const T*>(a.embed) + v0 * a.lde;
-        const ProductArgs lp{embed, a.lde, x, b.ld_x, n, a.rows, a.width, 1, count, false};
+        const ProductArgs lp{embed, a.lde, x, b.ld_x, n, a.rows, a.width, 1, count, false, 0};
         if (a.dentropy != nullptr) {
             const GradTile<T, true> e{terms, p, b.ld_p, v0};
             st = product_of<T, false, false>(lp, e, s);
@@ -695,29 +713,30 @@ template <typename T> hipError_t backward(const HeadBackwardArgs& a, hipStream_t
         if (st != hipSuccess) return st;
         if (a.dx != nullptr) {
             const ProductArgs dp{embed, a.lde, p, b.ld_p, a.width, a.rows, n, b.slices, count,
-                                 false};
-            const SumTile e{sums, a.rows, b.ld_s, i == 0};
+                                 false, b.items};
+            const SumTile e{sums, b.ld_s, i == 0};
             if ((st = product_of<T, true, false>(dp, e, s, true)) != hipSuccess) return st;
         }
         if (a.dembed != nullptr) {
             T* to = static_cast<T*>(a.dembed) + v0 * a.ldde;
-            const ProductArgs ep{x, b.ld_x, p, b.ld_p, a.width, n, a.rows, b.slices_e, count, true};
+            const ProductArgs ep{x, b.ld_x, p, b.ld_p, a.width, n, a.rows, b.slices_e, count, true, 0};
             if (b.slices_e == 1) {
                 const UnitTile<T> e{to, a.ldde, selected};
                 st = product_of<T, true, true>(ep, e, s);
             } else {
-                const SumTile e{sums_e, n, b.ld_s, true};
+                const SumTile e{sums_e, b.ld_s, true};
                 st = product_of<T, true, true>(ep, e, s);
                 if (st == hipSuccess)
-                    st = join_slices<T>(sums_e, b.slices_e, n, b.ld_s, n, a.width, nullptr, selected,
-                                        to, a.ldde, s);
+                    st = join_slices<T>({sums_e, b.ld_s, b.slices_e, 0, 0, 0}, n, a.width, nullptr,
+                                        selected, to, a.ldde, s);
             }
             if (st != hipSuccess) return st;
         }
     }
     if (a.dx == nullptr) return hipSuccess;
-    return join_slices<T>(sums, b.slices, a.rows, b.ld_s, a.rows, a.width, where, selected,
-                          static_cast<T*>(a.dx), a.lddx, s);
+    return join_slices<T>(
+        {sums, b.ld_s, 0, b.items, kMostSlices, static_cast<int>(tiles_of(a.width))}, a.rows, a.width,
+        where, selected, static_cast<T*>(a.dx), a.lddx, s);
 }
 
 }  // namespace

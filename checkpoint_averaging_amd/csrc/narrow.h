@@ -30,7 +30,7 @@ namespace dlk {
 constexpr int kNarrow = 128;             // elements of a row, with zeros from its width on
 constexpr int kNarrowStill = kTileWaves * kSquare, kNarrowUnit = 128;
 constexpr int kNarrowRing = 4, kNarrowBytes = kNarrowUnit * kNarrow * 2;
-constexpr int kNarrowTerms = 7;
+constexpr int kNarrowTerms = 7, kNarrowSlices = 64;
 
 // A row's terms, an array of `rows` for each: (m + log S) log2(e), -a, its target (or -1),
 // m (0 if that is -infinity), log S; and, with a gradient b of the entropies, -a - b H and
@@ -48,7 +48,8 @@ struct NarrowArgs {
     int64_t ld_still, still_rows;
     const bf16* moving;
     int64_t ld_moving, moving_rows;
-    int width, slices;                    // of the moving rows
+    int width;
+    int slices;                           // of the moving rows; with tokens still: cut_of's items
     const int* count;                     // of the tokens
     int64_t first;                        // token id of the vocabulary's first row here
     NarrowTerms terms;
@@ -70,13 +71,16 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_narrow(NarrowArgs a) {
     __shared__ float lds_terms[TOKENS_STILL ? 1 : kNarrowRing][8][kNarrowUnit];
     const int lane = threadIdx.x % kWave, half = lane / 32;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int slice = static_cast<int>(blockIdx.x % a.slices);
     const int count = *a.count;
+    const int slices = scalar(TOKENS_STILL ? cut_of(tiles_of(count), a.slices, kNarrowSlices)
+                                           : a.slices);
+    const int slice = scalar(static_cast<int>(blockIdx.x) % slices);
     const int still_rows = TOKENS_STILL ? count : static_cast<int>(a.still_rows);
     const int moving_rows = TOKENS_STILL ? static_cast<int>(a.moving_rows) : count;
-    const int n0 = static_cast<int>(blockIdx.x / a.slices) * kNarrowStill;
+    const int n0 = scalar(static_cast<int>(blockIdx.x) / slices) * kNarrowStill;
     if (n0 >= still_rows) return;
-    const int len = (moving_rows + a.slices * kNarrowUnit - 1) / (a.slices * kNarrowUnit) * kNarrowUnit;
+    const int len = scalar((moving_rows + slices * kNarrowUnit - 1) / (slices * kNarrowUnit)) *
+                    kNarrowUnit;
     const int from = slice * len;
     const int rows = moving_rows - from < len ? (moving_rows > from ? moving_rows - from : 0) : len;
     const int units = (rows + kNarrowUnit - 1) / kNarrowUnit;
@@ -286,7 +290,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_narrow(NarrowArgs a) {
     }
     __builtin_amdgcn_s_waitcnt(0x0F70);   // (LDS is this workgroup's until all has come)
     if (!there) return;
-    float* to = a.sums + (slice * a.still_rows + n) * a.ld;
+    float* to = a.sums + (static_cast<int64_t>(slice) * still_rows + n) * a.ld;
     for (int w = 0; w < kWide; ++w)
         for (int q = 0; q < 4; ++q) {
             const int c = w * kSquare + 8 * q + 4 * half;

@@ -47,7 +47,17 @@ struct ProductArgs {
     int slices;                          // parts of k, each with sums of its own
     const int* count;                    // or nullptr: the number of rows that n (or k) stands for
     bool count_is_k;
+    int items;                           // or 0: cut by cut_of into this many, for that number
 };
+
+// Parts of k for a product of `tiles` tiles of 256 x 256, so that there are as many as `items`
+// of them in all.
+__host__ __device__ inline int cut_of(int64_t tiles, int items, int most) {
+    const int64_t n = items / (tiles > 1 ? tiles : 1);
+    return static_cast<int>(n < 1 ? 1 : n > most ? most : n);
+}
+constexpr int kMostSlices = 16;
+__host__ __device__ inline int64_t tiles_of(int64_t rows) { return (rows + 255) / 256; }
 
 // ---- one operand -------------------------------------------------------------
 
@@ -371,10 +381,12 @@ struct Items {
 // What the products are of, in 32 bits where these are enough (fewer than 2^31 items, rows
 // and columns): the loops below have few scalar registers to spare.
 struct Extent {
-    int m, n, k;
+    int m, n, k, slices;
     __device__ explicit Extent(const ProductArgs& a)
-        : m(static_cast<int>(a.m)), n(static_cast<int>(a.n)), k(static_cast<int>(a.k)) {
+        : m(static_cast<int>(a.m)), n(static_cast<int>(a.n)), k(static_cast<int>(a.k)),
+          slices(a.slices) {
         if (a.count != nullptr) (a.count_is_k ? k : n) = scalar(*a.count);
+        if (a.items != 0) slices = scalar(cut_of(tiles_of(m) * tiles_of(n), a.items, kMostSlices));
     }
 };
 
@@ -487,7 +499,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product(ProductArgs a, Epil
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wm = wave / WN * (TM / WM), wn = wave % WN * (TN / WN);
     const Extent x(a);
-    const Items items(x.m, x.n, x.k, TM, TN, a.slices, kStep);
+    const Items items(x.m, x.n, x.k, TM, TN, x.slices, kStep);
     int in_at = Items::first(), in_turns = 0;
     SideA sa;
     SideB sb;
@@ -628,7 +640,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_direct(ProductArgs 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wm = wave / WN * (TM / WM), wn = wave % WN * (TN / WN);
     const Extent x(a);
-    const Items items(x.m, x.n, x.k, TM, TN, a.slices, kStep);
+    const Items items(x.m, x.n, x.k, TM, TN, x.slices, kStep);
     typename SideA::Direct sa;
     typename SideB::Direct sb;
     sa.start(a.a, a.lda);

@@ -189,3 +189,15 @@ def test_graphs_replay_it_and_calls_repeat():
         torch.cuda.synchronize()
         hg.same_bits(hg.bits(got[0]), hg.bits(dx), f"dx {k}")
         hg.same_bits(hg.bits(got[1]), hg.bits(de), f"dembed {k}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,vocab,width", [(1100, 1500, 136), (1100, 1500, 64), (600, 300, 600)])
+@pytest.mark.parametrize("some", [1, 40, 270])
+def test_few_of_many_rows_have_a_target(rows, vocab, width, dtype, some):
+    """The products are cut for the rows that take part, whatever their number."""
+    rng = np.random.default_rng(some + width)
+    x, e, t = lg.inputs(rng, rows, vocab, width)
+    t[rng.permutation(rows)[some:]] = -1
+    a, _ = lg.weights(rng, rows, False)
+    lg.Case(x, e, t, dtype, 0, None, a).forward().backward().check_backward()
