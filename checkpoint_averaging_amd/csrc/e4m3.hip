@@ -273,7 +273,7 @@ template <typename Y> hipError_t few_tokens(const E4m3ProductArgs& a, hipStream_
 template <template <class, int, int, int> class Math, typename Y>
 hipError_t matmul_of(const E4m3ProductArgs& a, hipStream_t s) {
     typedef ProductTile<Y> E;
-    const ProductArgs p{a.w, a.ldw, a.x, a.ldx, a.rows, a.count, a.cols, 1, nullptr, false, 0};
+    const ProductArgs p{a.w, a.ldw, a.x, a.ldx, a.rows, a.count, a.cols, 1, nullptr, false, 0, 0};
     const E e{StoreTile<Y>(a.y, a.ldy), a.w_scales, a.x_scales, (a.cols + kBlock - 1) / kBlock};
     if (a.count <= kFewTokens) return few_tokens<Y>(a, s);
     const dim3 block(kTileThreads);

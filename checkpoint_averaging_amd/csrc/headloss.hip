@@ -469,7 +469,7 @@ template <typename T> constexpr int span_of() { return sizeof(T) == 2 ? kSpan : 
 struct Backward {
     int64_t piece, pieces;                // of the vocabulary; the last takes the rest
     int64_t ld_p, ld_x, ld_s;
-    int items, slices;                    // of the vocabulary for dx (of all rows: fewer have more)
+    int items, most, slices;              // of the vocabulary for dx (of all rows: fewer have more)
     int slices_e;                         // of the rows for dembed
     int64_t widest;                       // piece
     int64_t index, where, selected, terms, x, p, sums, sums_e, bytes;      // places in the workspace
@@ -500,12 +500,13 @@ Backward backward_plan(int64_t rows, int64_t vocab, int64_t width, int64_t esize
     b.ld_x = up(width, 8);
     b.ld_s = up(width, 4);
     // Products of few tiles are cut along k, so that every CU has some (333 rows x 73,760 x 2048
-    // in bf16: 2.60 ms whole, 0.62 so).
+    // in bf16: 2.60 ms whole, 0.62 in 16, 0.55 in 32).
     const int64_t m_tiles = tiles_of(width), tiles = m_tiles * tiles_of(rows);
     b.items = items_of(tiles);
-    b.slices = cut_of(tiles, b.items, kMostSlices);
+    b.most = most_of(b.piece);
+    b.slices = cut_of(tiles, b.items, b.most);
     const int64_t tiles_e = m_tiles * tiles_of(b.widest);
-    b.slices_e = cut_of(tiles_e, items_of(tiles_e), kMostSlices);
+    b.slices_e = cut_of(tiles_e, items_of(tiles_e), most_of(rows));
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t here = at;
@@ -518,7 +519,7 @@ Backward backward_plan(int64_t rows, int64_t vocab, int64_t width, int64_t esize
     b.terms = take(static_cast<int64_t>(sizeof(RowTerms)) * rows);
     b.x = take(rows * b.ld_x * esize);
     b.p = take(rows * b.ld_p * esize);
-    b.sums = take(slice_rows(rows, b.items, kMostSlices, m_tiles) * b.ld_s * 4);
+    b.sums = take(slice_rows(rows, b.items, b.most, m_tiles) * b.ld_s * 4);
     b.sums_e = b.slices_e == 1 ? at : take(b.slices_e * b.widest * b.ld_s * 4);
     b.bytes = at;
     return b;
@@ -528,7 +529,7 @@ Backward backward_plan(int64_t rows, int64_t vocab, int64_t width, int64_t esize
 // in the logits takes to be written and read twice.
 struct Narrow {
     int64_t ld_x, ld_s, piece;            // of the vocabulary, for dembed
-    int items, slices, slices_e;          // as above
+    int items, most, slices_e;            // as above
     int64_t index, where, selected, terms, x, sums, bytes;
 };
 
@@ -538,8 +539,8 @@ Narrow narrow_plan(int64_t rows, int64_t vocab, int64_t width) {
     b.ld_s = up(width, 4);
     b.piece = vocab < kNarrowPiece ? vocab : kNarrowPiece;
     b.items = items_of(tiles_of(rows));
-    b.slices = cut_of(tiles_of(rows), b.items, kNarrowSlices);
-    b.slices_e = cut_of(tiles_of(b.piece), items_of(tiles_of(b.piece)), kNarrowSlices);
+    b.most = most_of(vocab);
+    b.slices_e = cut_of(tiles_of(b.piece), items_of(tiles_of(b.piece)), most_of(rows));
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t here = at;
@@ -551,7 +552,7 @@ Narrow narrow_plan(int64_t rows, int64_t vocab, int64_t width) {
     b.selected = take(sizeof(Selected));
     b.terms = take(4 * kNarrowTerms * rows);
     b.x = take(2 * rows * b.ld_x);
-    const int64_t of_x = slice_rows(rows, b.items, kNarrowSlices, 1), of_e = b.slices_e * b.piece;
+    const int64_t of_x = slice_rows(rows, b.items, b.most, 1), of_e = b.slices_e * b.piece;
     b.sums = take((of_x > of_e ? of_x : of_e) * b.ld_s * 4);
     b.bytes = at;
     return b;
@@ -595,7 +596,7 @@ template <typename T> hipError_t forward(const HeadArgs& a, hipStream_t s) {
     } else {
         const StatsTile e{parts, a.rows, a.targets, at_target};
         const ProductArgs p{a.embed, a.lde, a.x, a.ldx, a.vocab, a.rows, a.width, 1, nullptr,
-                            false, 0};
+                            false, 0, 0};
         n_parts = static_cast<int>((a.vocab + span_of<T>() - 1) / span_of<T>());
         st = product_of<T, false, false>(p, e, s);
     }
@@ -645,12 +646,12 @@ hipError_t narrow_backward(const HeadBackwardArgs& a, hipStream_t s) {
     static_assert(kNarrowStill == 256, "tiles_of counts them");
     if (a.dx != nullptr) {
         const NarrowArgs k{x,       b.ld_x,           a.rows, embed,           a.lde, a.vocab, width,
-                           b.items, &selected->count, 0,      {terms, a.rows}, sums,  b.ld_s};
+                           b.items, b.most, &selected->count, 0, {terms, a.rows}, sums, b.ld_s};
         (a.dentropy != nullptr ? k_narrow<true, true> : k_narrow<true, false>)
-            <<<dim3(static_cast<unsigned>(slice_rows(a.rows, b.items, kNarrowSlices, 1) / 256)),
+            <<<dim3(static_cast<unsigned>(slice_rows(a.rows, b.items, b.most, 1) / 256)),
                dim3(kTileThreads), 0, s>>>(k);
         if ((st = hipGetLastError()) != hipSuccess) return st;
-        st = join_slices<bf16>({sums, b.ld_s, 0, b.items, kNarrowSlices, 1}, a.rows, a.width, where,
+        st = join_slices<bf16>({sums, b.ld_s, 0, b.items, b.most, 1}, a.rows, a.width, where,
                                selected, static_cast<bf16*>(a.dx), a.lddx, s);
         if (st != hipSuccess) return st;
     }
@@ -658,7 +659,7 @@ hipError_t narrow_backward(const HeadBackwardArgs& a, hipStream_t s) {
     for (int64_t v0 = 0; v0 < a.vocab; v0 += b.piece) {
         const int64_t n = a.vocab - v0 < b.piece ? a.vocab - v0 : b.piece;
         const NarrowArgs k{embed + v0 * a.lde, a.lde, n, x, b.ld_x, a.rows, width,
-                           b.slices_e, &selected->count, v0, {terms, a.rows}, sums, b.ld_s};
+                           b.slices_e, 0, &selected->count, v0, {terms, a.rows}, sums, b.ld_s};
         (a.dentropy != nullptr ? k_narrow<false, true> : k_narrow<false, false>)
             <<<dim3(static_cast<unsigned>(tiles_of(n) * b.slices_e)), dim3(kTileThreads), 0, s>>>(k);
         if ((st = hipGetLastError()) != hipSuccess) return st;
@@ -671,14 +672,14 @@ hipError_t narrow_backward(const HeadBackwardArgs& a, hipStream_t s) {
 
 template <typename T> hipError_t backward(const HeadBackwardArgs& a, hipStream_t s) {
     if (a.rows == 0) {
-        const ProductArgs none{nullptr, 0, nullptr, 0, a.width, a.vocab, 0, 1, nullptr, false, 0};
+        const ProductArgs none{nullptr, 0, nullptr, 0, a.width, a.vocab, 0, 1, nullptr, false, 0, 0};
         return product_of<T, true, true>(
             none, UnitTile<T>{static_cast<T*>(a.dembed), a.ldde, nullptr}, s);
     }
     if constexpr (sizeof(T) == 2)
         // (0.56 ms against the general form's 1.21 for 8191 tokens x 50304 x 128, 0.48 against
-        // 1.04 with a width of 16, 0.079 against 0.149 for 100 tokens; 0.077 against 0.067 for
-        // 100 x 1000, whose time is launches)
+        // 1.04 with a width of 16, 0.079 against 0.149 for 100 tokens, 0.040 against 0.067 for
+        // 100 x 1000)
         if (a.width <= kNarrow && direct(a.embed, a.lde, 2, a.width))
             return narrow_backward(a, s);
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
@@ -702,7 +703,7 @@ template <typename T> hipError_t backward(const HeadBackwardArgs& a, hipStream_t
         const int64_t v0 = i * b.piece;
         const int64_t n = i + 1 < b.pieces ? b.piece : a.vocab - v0;
         const T* embed = static_cast<const T*>(a.embed) + v0 * a.lde;
-        const ProductArgs lp{embed, a.lde, x, b.ld_x, n, a.rows, a.width, 1, count, false, 0};
+        const ProductArgs lp{embed, a.lde, x, b.ld_x, n, a.rows, a.width, 1, count, false, 0, 0};
         if (a.dentropy != nullptr) {
             const GradTile<T, true> e{terms, p, b.ld_p, v0};
             st = product_of<T, false, false>(lp, e, s);
@@ -713,13 +714,13 @@ template <typename T> hipError_t backward(const HeadBackwardArgs& a, hipStream_t
         if (st != hipSuccess) return st;
         if (a.dx != nullptr) {
             const ProductArgs dp{embed, a.lde, p, b.ld_p, a.width, a.rows, n, b.slices, count,
-                                 false, b.items};
+                                 false, b.items, b.most};
             const SumTile e{sums, b.ld_s, i == 0};
             if ((st = product_of<T, true, false>(dp, e, s, true)) != hipSuccess) return st;
         }
         if (a.dembed != nullptr) {
             T* to = static_cast<T*>(a.dembed) + v0 * a.ldde;
-            const ProductArgs ep{x, b.ld_x, p, b.ld_p, a.width, n, a.rows, b.slices_e, count, true, 0};
+            const ProductArgs ep{x, b.ld_x, p, b.ld_p, a.width, n, a.rows, b.slices_e, count, true, 0, 0};
             if (b.slices_e == 1) {
                 const UnitTile<T> e{to, a.ldde, selected};
                 st = product_of<T, true, true>(ep, e, s);
@@ -735,7 +736,7 @@ template <typename T> hipError_t backward(const HeadBackwardArgs& a, hipStream_t
     }
     if (a.dx == nullptr) return hipSuccess;
     return join_slices<T>(
-        {sums, b.ld_s, 0, b.items, kMostSlices, static_cast<int>(tiles_of(a.width))}, a.rows, a.width,
+        {sums, b.ld_s, 0, b.items, b.most, static_cast<int>(tiles_of(a.width))}, a.rows, a.width,
         where, selected, static_cast<T*>(a.dx), a.lddx, s);
 }
 

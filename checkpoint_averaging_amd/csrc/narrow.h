@@ -30,7 +30,7 @@ namespace dlk {
 constexpr int kNarrow = 128;             // elements of a row, with zeros from its width on
 constexpr int kNarrowStill = kTileWaves * kSquare, kNarrowUnit = 128;
 constexpr int kNarrowRing = 4, kNarrowBytes = kNarrowUnit * kNarrow * 2;
-constexpr int kNarrowTerms = 7, kNarrowSlices = 64;
+constexpr int kNarrowTerms = 7;
 
 // A row's terms, an array of `rows` for each: (m + log S) log2(e), -a, its target (or -1),
 // m (0 if that is -infinity), log S; and, with a gradient b of the entropies, -a - b H and
@@ -49,7 +49,8 @@ struct NarrowArgs {
     const bf16* moving;
     int64_t ld_moving, moving_rows;
     int width;
-    int slices;                           // of the moving rows; with tokens still: cut_of's items
+    int slices;                           // of the moving rows; with tokens still, cut_of's items
+    int most;                             // and most
     const int* count;                     // of the tokens
     int64_t first;                        // token id of the vocabulary's first row here
     NarrowTerms terms;
@@ -72,7 +73,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_narrow(NarrowArgs a) {
     const int lane = threadIdx.x % kWave, half = lane / 32;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int count = *a.count;
-    const int slices = scalar(TOKENS_STILL ? cut_of(tiles_of(count), a.slices, kNarrowSlices)
+    const int slices = scalar(TOKENS_STILL ? cut_of(tiles_of(count), a.slices, a.most)
                                            : a.slices);
     const int slice = scalar(static_cast<int>(blockIdx.x) % slices);
     const int still_rows = TOKENS_STILL ? count : static_cast<int>(a.still_rows);
