@@ -500,7 +500,7 @@ Backward backward_plan(int64_t rows, int64_t vocab, int64_t width, int64_t esize
     b.ld_x = up(width, 8);
     b.ld_s = up(width, 4);
     // Products of few tiles are cut along k, so that every CU has some (333 rows x 73,760 x 2048
-    // in bf16: 2.60 ms whole, 0.62 in 16, 0.55 in 32).
+    // in bf16: 2.60 ms whole, 0.59 in 16).
     const int64_t m_tiles = tiles_of(width), tiles = m_tiles * tiles_of(rows);
     b.items = items_of(tiles);
     b.most = most_of(b.piece);

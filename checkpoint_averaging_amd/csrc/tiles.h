@@ -234,7 +234,7 @@ template <class Via, bool ACROSS, int ROWS, bool FIRST, bool PAIRS, int STEP_BYT
             uint32_t bytes = bound;
             if constexpr (ACROSS) {
                 const int n = __builtin_elementwise_min(lines, kLines);
-                bytes = __builtin_elementwise_max((n - 1) * row_bytes + static_cast<int>(bound), 0);
+                bytes = n > 0 ? (n - 1) * row_bytes + bound : 0;
             }
             __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
                 const_cast<uint8_t*>(base), 0, bytes, 0x00020000);

@@ -312,3 +312,31 @@ def test_refusals_on_the_device():
         dh.dl_e4m3_matmul(w, ws, 200, 128, x, xs, 8, w.data_ptr(), y_dtype=dl.DL_BF16)
     with pytest.raises(dl.DLError):
         dh.dl_e4m3_quantize(y, 8, 200, x.data_ptr(), y.data_ptr(), TILE)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("count", [32, 33, 128, 129, 192, 193, 257])
+def test_product_about_its_forms(count, out):
+    """Counts at which another form is taken, with rows enough for the largest tiles."""
+    rng = np.random.default_rng(count)
+    w, ws, wv = operand(rng, 33_000, 112, TILE)
+    x, xs, xv = operand(rng, count, 112, BLOCK)
+    check_product(product(w, ws, x, xs, out), wv, xv, out)
+
+
+def test_product_straight_to_lds_past_32_bits():
+    """Large tiles of rows 4 MB apart: offsets past 2^32 bytes on both sides."""
+    rng = np.random.default_rng(3)
+    rows, cols, count, ld = 4300, 128, 2100, 1 << 22
+    w, ws, _ = operand(rng, rows, cols, TILE)
+    x, xs, _ = operand(rng, count, cols, BLOCK)
+
+    def far(t):
+        f = torch.empty((len(t) - 1) * ld + cols, dtype=torch.uint8, device=DEV)
+        f = f.as_strided((len(t), cols), (ld, 1))
+        f.copy_(t.view(torch.uint8))
+        return f.view(torch.float8_e4m3fn)
+
+    fw, fx = far(w), far(x)
+    for out in ("f32", "bf16"):
+        hg.same_bits(product(fw, ws, fx, xs, out), product(w, ws, x, xs, out), "far rows")

@@ -267,3 +267,10 @@ def test_loss_head_refuses(calls):
     with pytest.raises(ValueError):
         head.backward(torch.zeros(4, WIDTH), t, torch.zeros(4), torch.zeros(4, WIDTH))
     assert not calls
+
+
+@pytest.mark.parametrize("kind", [dh.DL_SCALE_TILE128, dh.DL_SCALE_BLOCK128, 5, -1])
+def test_4_bit_product_refuses_scales_of_128(kind):
+    w4 = dict(packed=_at(0), scales=_at(1), rows=4, cols=256, x=_at(2), count=2, y=_at(3),
+              x_scales=_at(4), ldx=256, ldy=4, x_dtype=dh.DL_E4M3, y_dtype=dl.DL_F32, stream=0)
+    _refused(dl.DL_E_INVAL, dh.dl_w4_matvec, x_scale_kind=kind, **w4)

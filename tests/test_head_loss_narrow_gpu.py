@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from checkpoint_averaging_amd import dlhead as dh
+from checkpoint_averaging_amd import dlmerge as dl
 from oracle import head as oh
 from tests import test_head_gpu as hg
 from tests import test_head_loss_gpu as lg
@@ -201,3 +202,44 @@ def test_few_of_many_rows_have_a_target(rows, vocab, width, dtype, some):
     t[rng.permutation(rows)[some:]] = -1
     a, _ = lg.weights(rng, rows, False)
     lg.Case(x, e, t, dtype, 0, None, a).forward().backward().check_backward()
+
+
+@pytest.mark.parametrize("dtype,width", [("bf16", 64), ("bf16", 264), ("f32", 136)])
+def test_rows_4_mb_apart(dtype, width):
+    """The embedding and its gradient in rows that go straight to LDS, at offsets past 2^32
+    bytes; the inputs too, as far as the calls take them from there."""
+    rows, vocab, size = 40, 1100, 4 if dtype == "f32" else 2
+    ld = (1 << 22) // size
+    rng = np.random.default_rng(width)
+    x, e, t = lg.inputs(rng, rows, vocab, width)
+    a, _ = lg.weights(rng, rows, False)
+    c = lg.Case(x, e, t, dtype, 0, None, a).forward().backward()
+    far = torch.empty((vocab + 1) * ld, dtype=hg.TORCH[dtype], device=DEV)
+    ev = far.as_strided((vocab, width), (ld, 1))
+    ev.copy_(c.e)
+    de = far.as_strided((vocab, width), (ld, 1), 4096)
+    lp, st, dx = torch.empty_like(c.logprobs), torch.empty_like(c.stats), torch.empty_like(c.dx)
+    ws = lg.workspace(rows, vocab, width, dtype, True)
+    dh.dl_head_logprobs(c.x, ev, rows, vocab, width, c.td, lp, stats=st, workspace=ws)
+    # (dembed's rows lie between embed's: the call sees two spans that overlap, and refuses)
+    with pytest.raises(dl.DLError):
+        dh.dl_head_logprobs_backward(c.x, ev, rows, vocab, width, c.td, st, c.ad, dx=dx, dembed=de,
+                                     workspace=ws)
+    dh.dl_head_logprobs_backward(c.x, ev, rows, vocab, width, c.td, st, c.ad, dx=dx, workspace=ws)
+    hg.same_bits(hg.bits(lp), hg.bits(c.logprobs), "logprobs")
+    hg.same_bits(hg.bits(dx), hg.bits(c.dx), "dx")
+    dh.dl_head_logprobs_backward(c.x, c.e, rows, vocab, width, c.td, st, c.ad, dembed=de,
+                                 workspace=ws)
+    hg.same_bits(hg.bits(de.contiguous()), hg.bits(c.de), "dembed")
+
+
+@pytest.mark.parametrize("width", [64, 264])
+def test_no_rows_at_all(width):
+    e = torch.randn(700, width, device=DEV).bfloat16()
+    de = torch.full((700, width), 3.0, dtype=torch.bfloat16, device=DEV)
+    none = torch.empty(0, device=DEV)
+    dh.dl_head_logprobs_backward(e[:0], e, 0, 700, width, torch.empty(0, dtype=torch.int64,
+                                                                      device=DEV),
+                                 none, none, dembed=de)
+    torch.cuda.synchronize()
+    assert not de.any()
