@@ -10,7 +10,7 @@
 // tokens x 73760 x 2048 in bf16: 0.54 ms, 1.14 PFLOP/s, of which 13 us join the parts; the
 // matrix cores' power bounds it (a loop of nothing but these instructions reaches 1.8).  In
 // fp32, six bf16 products for one: 3.3 ms, 187 TFLOP/s.  Up to 32 tokens read E once, straight
-// into registers (few.h): one token 69 us, 4.4 TB/s; 33 tokens in a tile of 256 take 103.
+// into registers (few.h): one token 69 us, 4.4 TB/s; 33 tokens in tiles of 128 take 84.
 //
 // Backward: the rows that have a part are gathered first, so that a product has as many
 // columns as there are of them (a masked-token loss has targets at its masked positions only);
@@ -464,7 +464,12 @@ int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 // Rows of the vocabulary that a wave leaves one part of.
 constexpr int kSpan = 128, kSpanSplit = 64;
 
-template <typename T> constexpr int span_of() { return sizeof(T) == 2 ? kSpan : kSpanSplit; }
+// Up to so many tokens go in tiles of their own.
+constexpr int kSomeTokens = 128;
+
+int span_of(int64_t rows, int64_t esize) {
+    return esize == 2 && rows > kSomeTokens ? kSpan : kSpanSplit;
+}
 
 struct Backward {
     int64_t piece, pieces;                // of the vocabulary; the last takes the rest
@@ -563,6 +568,23 @@ Narrow narrow_plan(int64_t rows, int64_t vocab, int64_t width) {
 template <typename T, bool SA, bool SB, class E>
 hipError_t product_of(const ProductArgs& a, const E& e, hipStream_t s, bool padded = false) {
     const dim3 block(kTileThreads);
+    // Tiles of 128 x 128, where half of a larger one or more would be empty and few tokens mean
+    // few tiles (forward, bf16 and fp32: 100 tokens x 2000 x 512 33 us against 40 and 60 against
+    // 86; 33 x 73,760 x 2048 84 against 105, 128 of them 299 against 311).  Not for products
+    // across the embedding, with its bytes to bring (dx of 20 x 73,760 x 2048 in fp32: 50 us
+    // more).
+    if constexpr (!SA && !SB) {
+        if (a.n <= kSomeTokens) {
+            typedef std::conditional_t<sizeof(T) == 2, ViaBf16, ViaSplit> Via;
+            const dim3 grid(product_grid(a.m, a.n, 128, 128, a.slices,
+                                         sizeof(T) == 2 ? 2 * kTileGroups : kTileGroups));
+            if constexpr (sizeof(T) == 2)
+                k_product<Via, SA, SB, 128, 128, 2, 4, E, Bf16Math><<<grid, block, 0, s>>>(a, e);
+            else
+                k_product<Via, SA, SB, 128, 128, 2, 4, E, SplitMath><<<grid, block, 0, s>>>(a, e);
+            return hipGetLastError();
+        }
+    }
     if constexpr (sizeof(T) == 2) {
         const dim3 grid(product_grid(a.m, a.n, 256, 256, a.slices, kTileGroups));
         if (direct(a.a, a.lda, 2, SA ? 0 : a.k) && direct(a.b, a.ldb, 2, SB || padded ? 0 : a.k))
@@ -597,7 +619,8 @@ template <typename T> hipError_t forward(const HeadArgs& a, hipStream_t s) {
         const StatsTile e{parts, a.rows, a.targets, at_target};
         const ProductArgs p{a.embed, a.lde, a.x, a.ldx, a.vocab, a.rows, a.width, 1, nullptr,
                             false, 0, 0};
-        n_parts = static_cast<int>((a.vocab + span_of<T>() - 1) / span_of<T>());
+        const int span = span_of(a.rows, sizeof(T));
+        n_parts = static_cast<int>((a.vocab + span - 1) / span);
         st = product_of<T, false, false>(p, e, s);
     }
     if (st != hipSuccess) return st;
@@ -744,7 +767,7 @@ template <typename T> hipError_t backward(const HeadBackwardArgs& a, hipStream_t
 
 int64_t head_workspace_bytes(int64_t rows, int64_t vocab, int64_t width, int dtype,
                              bool with_backward) {
-    const int64_t span = dtype == DL_BF16 ? kSpan : kSpanSplit;
+    const int64_t span = span_of(rows, dtype == DL_BF16 ? 2 : 4);
     const int64_t parts = rows <= kFewTokens ? kFewGroups : (vocab + span - 1) / span;
     const int64_t fwd =
         up(4 * rows, 256) + up(parts * rows * static_cast<int64_t>(sizeof(Part)), 256);

@@ -417,10 +417,10 @@ template <int N> struct Count {
 };
 
 // How a step's products are made: kSubs times, every row tile of A with all of B's.
-// A's pieces are read kAhead row tiles before their use, B's (into the next of kSlots) for
-// the next time round.
+// A's pieces are read kAhead row tiles (no more than a round's) before their use, B's (into the
+// next of kSlots) for the next time round.
 template <class Epilogue, int MT, int NT, int SUBS> struct Bf16Math {
-    static constexpr int kSubs = SUBS, kAhead = 3, kSlots = 2;
+    static constexpr int kSubs = SUBS, kAhead = MT > 3 ? 3 : 1, kSlots = 2;
     typedef bf16x8 A;
     struct B {
         bf16x8 v[NT];
@@ -497,7 +497,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product(ProductArgs a, Epil
     typedef Math<Epilogue, kMT, kNT, SideA::kStep * SideA::kHeld / 32> Made;
     constexpr int kStep = SideA::kStep, kGroups = Made::kSubs * kMT, kAhead = Made::kAhead;
     static_assert(kMT >= 1 && kNT >= 1 && kGroups % (kAhead + 1) == 0 && kGroups > kAhead &&
-                      Made::kSubs % Made::kSlots == 0, "");
+                      kAhead <= kMT && Made::kSubs % Made::kSlots == 0, "");
     __shared__ __attribute__((aligned(128))) uint8_t lds[2][SideA::kBytes + SideB::kBytes];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wm = wave / WN * (TM / WM), wn = wave % WN * (TN / WN);
@@ -637,7 +637,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_direct(ProductArgs 
     constexpr int kStep = SideA::kStep, kGroups = Made::kSubs * kMT, kAhead = Made::kAhead;
     constexpr int kLoads = SideA::kMine;                             // of a unit, each thread's
     static_assert(SideA::kBytes == kUnitBytes && SideB::kBytes == kUnitBytes, "");
-    static_assert(kGroups % (kAhead + 1) == 0 && kGroups > kAhead + 1 &&
+    static_assert(kGroups % (kAhead + 1) == 0 && kGroups > kAhead + 1 && kAhead <= kMT &&
                       Made::kSubs % Made::kSlots == 0, "");
     __shared__ __attribute__((aligned(128))) uint8_t lds[kUnits * kUnitBytes];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);

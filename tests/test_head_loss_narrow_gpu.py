@@ -243,3 +243,15 @@ def test_no_rows_at_all(width):
                                  none, none, dembed=de)
     torch.cuda.synchronize()
     assert not de.any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pad", [0, 1])
+@pytest.mark.parametrize("rows", [127, 128, 129])
+def test_numbers_of_tokens_about_the_general_forms(rows, pad, dtype):
+    rng = np.random.default_rng(rows)
+    x, e, t = lg.inputs(rng, rows, 900, 200)
+    t[::6] = -1
+    a, b = lg.weights(rng, rows, True)
+    c = lg.Case(x, e, t, dtype, pad, b, a).forward().check_forward()
+    c.backward(pad).check_backward()
