@@ -12,8 +12,8 @@
 // 32 moving rows in its column, which is what the second one takes of its own operand if the
 // rows are counted in that order.  d is rounded to bf16 for it, as the general form's is.
 //
-// 8191 tokens x 50304 x 128: dx 0.21 ms, dembed 0.28 (with an entropy's gradient 0.22 and
-// 0.29), 0.21 TFLOP each: 0.75 to 1 PFLOP/s, which the exponentials and conversions between
+// 8191 tokens x 50304 x 128: dx 0.21 ms, dembed 0.29 (with an entropy's gradient 0.24 and
+// 0.33), 0.21 TFLOP each: 0.64 to 1 PFLOP/s, which the exponentials and conversions between
 // the products bound (some 8 vector instructions an element beside its two matrix
 // instructions' share).  Through memory the gradient in the logits was 824 MB written and
 // twice read, and the two and its own product took 1.1 ms.
