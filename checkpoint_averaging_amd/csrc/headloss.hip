@@ -148,7 +148,8 @@ struct StatsFew {
     __device__ __forceinline__ void begin() { mine = Part{-__builtin_inff(), 0, 0}; }
     __device__ __forceinline__ void value(float l, int64_t row, int v) {
         if (targets != nullptr && targets[v] == row) at_target[v] = l;
-        mine.add(Part{l, 0, 0});
+        // (one of +infinity or NaN makes the sum NaN, one of -infinity has no part in it)
+        mine.add(Part{l, l == -__builtin_inff() ? 0.0f : l - l, 0});
     }
     __device__ __forceinline__ void end(float* lds, int count) {
         const int tokens = count <= 16 ? 16 : 32;

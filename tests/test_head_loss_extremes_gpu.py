@@ -1,0 +1,64 @@
+"""Log probabilities without logits, and their gradients, where logits leave binary32's
+range."""
+import numpy as np
+import pytest
+import torch
+
+from checkpoint_averaging_amd import dlhead as dh
+from tests import test_head_gpu as hg
+from tests import test_head_loss_gpu as lg
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+def forward(x, e, t):
+    rows, vocab, width = x.shape[0], e.shape[0], x.shape[1]
+    lp, h, st = (torch.full(s, 9.0, device=DEV) for s in ((rows,), (rows,), (rows, 2)))
+    need = dh.dl_head_workspace_bytes(rows, vocab, width, x.dtype)
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=DEV)
+    dh.dl_head_logprobs(x, e, rows, vocab, width, t, lp, entropy=h, stats=st, workspace=ws)
+    torch.cuda.synchronize()
+    return lp, h, st
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 16, 17, 32, 33, 200])
+def test_a_logit_past_the_range_is_nan(rows, dtype):
+    """A logit of +infinity from finite inputs: its row's results and gradients are NaN,
+    the other rows' are not."""
+    rng = np.random.default_rng(rows)
+    vocab, width = 500, 40
+    x, e, t = lg.inputs(rng, rows, vocab, width)
+    x[:, 3], e[:, 3] = 0, 0
+    bad = np.arange(0, rows, 5)
+    x[bad, 3], e[77, 3] = 2.0 ** 100, 2.0 ** 100
+    t[bad] = np.where(bad % 2 == 0, 77, 5)                       # the infinite one, or another
+    xd, ed = (torch.from_numpy(v).to(DEV).to(hg.TORCH[dtype]) for v in (x, e))
+    td = torch.from_numpy(t).to(DEV)
+    lp, h, st = forward(xd, ed, td)
+    got = [hg.host(lp), hg.host(h), hg.host(st)[:, 1]]
+    for v, name in zip(got, ("logprobs", "entropy", "log S")):
+        assert np.isnan(v[bad]).all(), name
+        assert np.isfinite(np.delete(v, bad)).all(), name
+    a = torch.ones(rows, device=DEV)
+    dx = torch.empty_like(xd)
+    ws = lg.workspace(rows, vocab, width, dtype, True)
+    for b in (None, a):
+        dh.dl_head_logprobs_backward(xd, ed, rows, vocab, width, td, st, a, dx=dx,
+                                     entropy=None if b is None else h, dentropy=b, workspace=ws)
+        got = hg.host(dx)
+        assert np.isnan(got[bad]).all()
+        # (2^100 is a finite element of every row's sum)
+        assert np.isfinite(np.delete(got, bad, 0)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 20, 40])
+def test_a_vocabulary_of_nothing_but_nan(rows, dtype):
+    x = torch.full((rows, 8), float("nan"), device=DEV).to(hg.TORCH[dtype])
+    for vocab in (1, 2):
+        e = torch.ones(vocab, 8, device=DEV).to(hg.TORCH[dtype])
+        lp, h, st = forward(x, e, torch.zeros(rows, dtype=torch.int64, device=DEV))
+        assert torch.isnan(lp).all() and torch.isnan(h).all() and torch.isnan(st[:, 1]).all()
