@@ -41,33 +41,41 @@ constexpr float kLog2e = 0x1.715476p+0f, kLn2 = 0x1.62e43p-1f;
 
 __device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
 
-// What a wave leaves of its span of the vocabulary for one token: the largest
-// logit m, the sum of exp(l - m) without one largest element's own 1, and the
-// sum of exp(l - m)(l - m).
-struct Part {
-    float m, rest, dot;
+// What is known of a span of the vocabulary for one token: the largest logit m, the
+// sum of exp(l - m) without one largest element's own 1, and the sum of
+// exp(l - m)(l - m).
+template <typename F> struct PartOf {
+    float m;
+    F rest, dot;
 
+    static __device__ __forceinline__ PartOf none() { return PartOf{-__builtin_inff(), 0, 0}; }
     // None of a span's tokens has a probability (nor is there a NaN).
     __device__ __forceinline__ bool nothing() const {
         return m == -__builtin_inff() && rest == rest;
     }
-    __device__ __forceinline__ void add(Part p) {
-        if (p.nothing()) return;
+    template <typename G> __device__ __forceinline__ void add(const PartOf<G>& q) {
+        if (q.nothing()) return;
+        PartOf p{q.m, q.rest, q.dot};
         if (nothing()) {
             *this = p;
             return;
         }
         if (p.m > m) {
-            const Part t = *this;
+            const PartOf t = *this;
             *this = p;
             p = t;
         }
         const float d = p.m - m, w = exp_of(d);
         rest += w * (1 + p.rest);
         // (w is 0 where d is -infinity)
-        dot += w > 0 || w != w ? w * (p.dot + d * (1 + p.rest)) : 0.0f;
+        dot += w > 0 || w != w ? w * (p.dot + d * (1 + p.rest)) : 0;
     }
 };
+// Of a wave's or workgroup's span, in memory; and of many of them, one after the other, in
+// binary64: equal terms round the same way at each addition, and 2^28 tokens' parts in one
+// chain of binary32 came out 4e-4 off.
+typedef PartOf<float> Part;
+typedef PartOf<double> Total;
 
 // ---- forward -----------------------------------------------------------------
 
@@ -143,9 +151,9 @@ struct StatsFew {
     int64_t rows;
     const int64_t* targets;               // or nullptr
     float* at_target;
-    Part mine;
+    Total mine;
 
-    __device__ __forceinline__ void begin() { mine = Part{-__builtin_inff(), 0, 0}; }
+    __device__ __forceinline__ void begin() { mine = Total::none(); }
     __device__ __forceinline__ void value(float l, int64_t row, int v) {
         if (targets != nullptr && targets[v] == row) at_target[v] = l;
         // (one of +infinity or NaN makes the sum NaN, one of -infinity has no part in it)
@@ -153,7 +161,8 @@ struct StatsFew {
     }
     __device__ __forceinline__ void end(float* lds, int count) {
         const int tokens = count <= 16 ? 16 : 32;
-        Part* all = reinterpret_cast<Part*>(lds);
+        static_assert(sizeof(Total) * kFewThreads <= kFewLds, "");
+        Total* all = reinterpret_cast<Total*>(lds);
         __syncthreads();
         all[threadIdx.x] = mine;
         for (int n = kFewThreads / 2; n >= tokens; n /= 2) {
@@ -163,7 +172,9 @@ struct StatsFew {
                 all[threadIdx.x] = mine;
             }
         }
-        if (static_cast<int>(threadIdx.x) < count) parts[blockIdx.x * rows + threadIdx.x] = mine;
+        if (static_cast<int>(threadIdx.x) < count)
+            parts[blockIdx.x * rows + threadIdx.x] =
+                Part{mine.m, static_cast<float>(mine.rest), static_cast<float>(mine.dot)};
     }
 };
 
@@ -173,16 +184,16 @@ constexpr int kJoinRows = 16, kJoinParts = 64;
 __global__ __launch_bounds__(kJoinRows * kJoinParts) void k_join(
     const Part* parts, int n_parts, int64_t rows, int64_t vocab, const int64_t* targets,
     const float* at_target, float* logprobs, float* entropy, float* stats) {
-    __shared__ Part lds[kJoinParts][kJoinRows];
+    __shared__ Total lds[kJoinParts][kJoinRows];
     const int r = threadIdx.x % kJoinRows, g = threadIdx.x / kJoinRows;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * kJoinRows + r;
     const int64_t safe = row < rows ? row : rows - 1;
-    constexpr Part kNone{-__builtin_inff(), 0, 0};
-    Part all = kNone;
+    Total all = Total::none();
     for (int p = g; p < n_parts; p += 4 * kJoinParts) {
         Part q[4];
         for (int k = 0; k < 4; ++k)
-            q[k] = p + k * kJoinParts < n_parts ? parts[(p + k * kJoinParts) * rows + safe] : kNone;
+            q[k] = p + k * kJoinParts < n_parts ? parts[(p + k * kJoinParts) * rows + safe]
+                                               : Part::none();
         for (int k = 0; k < 4; ++k) all.add(q[k]);
     }
     lds[g][r] = all;
@@ -195,13 +206,13 @@ __global__ __launch_bounds__(kJoinRows * kJoinParts) void k_join(
     }
     if (g != 0 || row >= rows) return;
     const bool nothing = all.nothing();
-    const float m = all.m, log_s = nothing ? 0.0f : log1pf(all.rest);
+    const float m = all.m, log_s = nothing ? 0.0f : log1pf(static_cast<float>(all.rest));
     if (stats != nullptr) {
         stats[2 * row] = m;
         stats[2 * row + 1] = log_s;
     }
     if (entropy != nullptr)
-        entropy[row] = nothing ? 0.0f : log_s - all.dot / (1 + all.rest);
+        entropy[row] = nothing ? 0.0f : static_cast<float>(log_s - all.dot / (1 + all.rest));
     if (logprobs != nullptr) {
         const int64_t t = targets[row];
         float lp = 0.0f;

@@ -1,5 +1,5 @@
 """Log probabilities without logits, and their gradients, where logits leave binary32's
-range."""
+range, and over a vocabulary of nearly the length that the call takes."""
 import numpy as np
 import pytest
 import torch
@@ -62,3 +62,26 @@ def test_a_vocabulary_of_nothing_but_nan(rows, dtype):
         e = torch.ones(vocab, 8, device=DEV).to(hg.TORCH[dtype])
         lp, h, st = forward(x, e, torch.zeros(rows, dtype=torch.int64, device=DEV))
         assert torch.isnan(lp).all() and torch.isnan(h).all() and torch.isnan(st[:, 1]).all()
+
+
+@pytest.mark.parametrize("rows", [1, 20, 33])
+def test_sums_over_a_long_vocabulary(rows):
+    """2^28 tokens, of which the first are above all others and these are equal: their sum is
+    off by no more than the 4e-5 that any vocabulary's may be, and so are log S and what it
+    goes into.  (Equal terms below the largest round the same way at each addition.)"""
+    vocab, tops, other = 1 << 28, 1 << 16, -0.75
+    e = torch.full((vocab, 1), other, dtype=torch.bfloat16, device=DEV)
+    e[:tops] = 0
+    x = torch.ones(rows, 1, dtype=torch.bfloat16, device=DEV)
+    t = torch.full((rows,), 5, dtype=torch.int64, device=DEV)
+    t[1::2] = vocab // 3
+    lp, h, st = (hg.host(v).astype(np.float64) for v in forward(x, e, t))
+    rest = (vocab - tops) * np.exp(other)
+    log_s = np.log(tops + rest)
+    # 2 u for the logarithm's last place, u for the subtraction
+    off = 4e-5 + 3 * hg.U * log_s
+    hg.within(st[:, 1], np.full(rows, log_s), off, "log S")
+    want = np.where(np.arange(rows) % 2 == 0, 0.0, other) - log_s
+    hg.within(lp, want, off, "logprobs")
+    # the entropy's second term is the mean of the distances, whose sum has S's error too
+    hg.within(h, np.full(rows, log_s - rest * other / (tops + rest)), 2 * off, "entropy")
