@@ -114,8 +114,6 @@ template <int STEPS> struct FewCodes {
 };
 
 constexpr int kFewThreads = 512, kFewWaves = kFewThreads / kWave;
-// Bytes of LDS that an epilogue's end has at least.
-constexpr int kFewLds = 2 * kFewWaves * 16 * 4 * static_cast<int>(sizeof(f32x4));
 
 // Src: one of the above; NT: tiles of 16 vectors; RT: tiles of 16 rows a wave.
 template <class Src, int NT, int RT, class Epilogue>

@@ -71,11 +71,14 @@ template <typename F> struct PartOf {
         dot += w > 0 || w != w ? w * (p.dot + d * (1 + p.rest)) : 0;
     }
 };
-// Of a wave's or workgroup's span, in memory; and of many of them, one after the other, in
-// binary64: equal terms round the same way at each addition, and 2^28 tokens' parts in one
-// chain of binary32 came out 4e-4 off.
+// Of a span; and of many, one after the other, in binary64: equal terms round the same way
+// at each addition, and 2^28 tokens' in one chain of binary32 came out 4e-4 off.
 typedef PartOf<float> Part;
 typedef PartOf<double> Total;
+
+__device__ __forceinline__ Part part_of(const Total& t) {
+    return Part{t.m, static_cast<float>(t.rest), static_cast<float>(t.dot)};
+}
 
 // ---- forward -----------------------------------------------------------------
 
@@ -161,40 +164,48 @@ struct StatsFew {
     }
     __device__ __forceinline__ void end(float* lds, int count) {
         const int tokens = count <= 16 ? 16 : 32;
-        static_assert(sizeof(Total) * kFewThreads <= kFewLds, "");
-        Total* all = reinterpret_cast<Total*>(lds);
+        Part* all = reinterpret_cast<Part*>(lds);
+        Part part = part_of(mine);
         __syncthreads();
-        all[threadIdx.x] = mine;
+        all[threadIdx.x] = part;
         for (int n = kFewThreads / 2; n >= tokens; n /= 2) {
             __syncthreads();
             if (static_cast<int>(threadIdx.x) < n) {
-                mine.add(all[threadIdx.x + n]);
-                all[threadIdx.x] = mine;
+                part.add(all[threadIdx.x + n]);
+                all[threadIdx.x] = part;
             }
         }
-        if (static_cast<int>(threadIdx.x) < count)
-            parts[blockIdx.x * rows + threadIdx.x] =
-                Part{mine.m, static_cast<float>(mine.rest), static_cast<float>(mine.dot)};
+        if (static_cast<int>(threadIdx.x) < count) parts[blockIdx.x * rows + threadIdx.x] = part;
     }
 };
 
-// The row's results from its spans' parts: 16 rows a workgroup, 64 threads each.
-constexpr int kJoinRows = 16, kJoinParts = 64;
+// The row's results from its spans' parts: 16 rows a workgroup, 64 threads each.  (All of a
+// thread's in binary64, rather than its runs of 256: 0.6 us more for one row of 256 parts.)
+constexpr int kJoinRows = 16, kJoinParts = 64, kJoinRun = 256;
 
 __global__ __launch_bounds__(kJoinRows * kJoinParts) void k_join(
     const Part* parts, int n_parts, int64_t rows, int64_t vocab, const int64_t* targets,
     const float* at_target, float* logprobs, float* entropy, float* stats) {
-    __shared__ Total lds[kJoinParts][kJoinRows];
+    __shared__ Part lds[kJoinParts][kJoinRows];
     const int r = threadIdx.x % kJoinRows, g = threadIdx.x / kJoinRows;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * kJoinRows + r;
     const int64_t safe = row < rows ? row : rows - 1;
-    Total all = Total::none();
-    for (int p = g; p < n_parts; p += 4 * kJoinParts) {
+    Part all = Part::none();
+    Total before = Total::none();         // what came before the last kJoinRun or fewer
+    for (int p = g, run = 0; p < n_parts; p += 4 * kJoinParts) {
         Part q[4];
         for (int k = 0; k < 4; ++k)
             q[k] = p + k * kJoinParts < n_parts ? parts[(p + k * kJoinParts) * rows + safe]
                                                : Part::none();
         for (int k = 0; k < 4; ++k) all.add(q[k]);
+        if ((run += 4) < kJoinRun) continue;
+        before.add(all);
+        all = Part::none();
+        run = 0;
+    }
+    if (!before.nothing()) {
+        before.add(all);
+        all = part_of(before);
     }
     lds[g][r] = all;
     for (int h = kJoinParts / 2; h > 0; h /= 2) {
@@ -206,13 +217,13 @@ __global__ __launch_bounds__(kJoinRows * kJoinParts) void k_join(
     }
     if (g != 0 || row >= rows) return;
     const bool nothing = all.nothing();
-    const float m = all.m, log_s = nothing ? 0.0f : log1pf(static_cast<float>(all.rest));
+    const float m = all.m, log_s = nothing ? 0.0f : log1pf(all.rest);
     if (stats != nullptr) {
         stats[2 * row] = m;
         stats[2 * row + 1] = log_s;
     }
     if (entropy != nullptr)
-        entropy[row] = nothing ? 0.0f : static_cast<float>(log_s - all.dot / (1 + all.rest));
+        entropy[row] = nothing ? 0.0f : log_s - all.dot / (1 + all.rest);
     if (logprobs != nullptr) {
         const int64_t t = targets[row];
         float lp = 0.0f;
