@@ -431,10 +431,19 @@ struct Slices {
     int number, items, most, m_tiles;
 };
 
+// What they leave out of the product: columns `from` to `to`, eight at most, of d, and as many
+// rows of e.
+template <typename T> struct Rest {
+    const T* d;
+    int64_t ldd;
+    const T* e;
+    int64_t lde, from, to;
+};
+
 template <typename T>
 __global__ __launch_bounds__(256) void k_join_slices(Slices a, int64_t rows, int width,
                                                      const int* where, const Selected* selected,
-                                                     T* out, int64_t ldo) {
+                                                     T* out, int64_t ldo, Rest<T> rest) {
     const float unit = selected->unit;
     const float* sums = a.sums;
     const int64_t lds = a.ld, apart = where != nullptr ? selected->count : rows;
@@ -453,6 +462,16 @@ __global__ __launch_bounds__(256) void k_join_slices(Slices a, int64_t rows, int
                 float w[8];
                 load8(sums + (s * apart + at) * lds, c, width, w);
                 for (int k = 0; k < 8; ++k) v[k] += w[k];
+            }
+            if (rest.from < rest.to) {
+                float d[8];
+                load8(rest.d + at * rest.ldd, rest.from, rest.to, d);
+                for (int j = 0; j < 8; ++j) {
+                    if (rest.from + j >= rest.to) break;
+                    float w[8];
+                    load8(rest.e + (rest.from + j) * rest.lde, c, width, w);
+                    for (int k = 0; k < 8; ++k) v[k] += d[j] * w[k];
+                }
             }
             for (int k = 0; k < 8; ++k) v[k] *= unit;
         }
@@ -586,10 +605,12 @@ Narrow narrow_plan(int64_t rows, int64_t vocab, int64_t width) {
     return b;
 }
 
-// bf16: 256 x 256 tiles; binary32, whose three planes fill the LDS: 256 x 128.  `padded`: b
-// holds zeros from its end along k up to a multiple of 8.
+// bf16: 256 x 256 tiles; binary32, whose three planes fill the LDS: 256 x 128.  `along_a`,
+// `along_b`: elements of the operands' last lines in memory that have to be whole pieces of 16
+// bytes to go straight to LDS; 0 for those of the workspace, which holds what follows.
 template <typename T, bool SA, bool SB, class E>
-hipError_t product_of(const ProductArgs& a, const E& e, hipStream_t s, bool padded = false) {
+hipError_t product_of(const ProductArgs& a, const E& e, hipStream_t s, int64_t along_a,
+                      int64_t along_b) {
     const dim3 block(kTileThreads);
     // Tiles of 128 x 128, where half of a larger one or more would be empty and few tokens mean
     // few tiles (forward, bf16 and fp32: 100 tokens x 2000 x 512 33 us against 40 and 60 against
@@ -610,7 +631,7 @@ hipError_t product_of(const ProductArgs& a, const E& e, hipStream_t s, bool padd
     }
     if constexpr (sizeof(T) == 2) {
         const dim3 grid(product_grid(a.m, a.n, 256, 256, a.slices, kTileGroups));
-        if (direct(a.a, a.lda, 2, SA ? 0 : a.k) && direct(a.b, a.ldb, 2, SB || padded ? 0 : a.k))
+        if (direct(a.a, a.lda, 2, along_a) && direct(a.b, a.ldb, 2, along_b))
             k_product_direct<ViaBf16, SA, SB, 256, 256, 2, 4, E, Bf16Math>
                 <<<grid, block, 0, s>>>(a, e);
         else
@@ -644,7 +665,7 @@ template <typename T> hipError_t forward(const HeadArgs& a, hipStream_t s) {
                             false, 0, 0};
         const int span = span_of(a.rows, sizeof(T));
         n_parts = static_cast<int>((a.vocab + span - 1) / span);
-        st = product_of<T, false, false>(p, e, s);
+        st = product_of<T, false, false>(p, e, s, a.width, a.width);
     }
     if (st != hipSuccess) return st;
     k_join<<<dim3(static_cast<unsigned>((a.rows + kJoinRows - 1) / kJoinRows)),
@@ -655,10 +676,11 @@ template <typename T> hipError_t forward(const HeadArgs& a, hipStream_t s) {
 
 template <typename T>
 hipError_t join_slices(const Slices& a, int64_t rows, int64_t width, const int* where,
-                       const Selected* selected, T* out, int64_t ldo, hipStream_t s) {
+                       const Selected* selected, T* out, int64_t ldo, hipStream_t s,
+                       const Rest<T>& rest = {}) {
     const int64_t blocks = (rows * ((width + 7) / 8) + 255) / 256;
     k_join_slices<T><<<dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s>>>(
-        a, rows, static_cast<int>(width), where, selected, out, ldo);
+        a, rows, static_cast<int>(width), where, selected, out, ldo, rest);
     return hipGetLastError();
 }
 
@@ -720,7 +742,7 @@ template <typename T> hipError_t backward(const HeadBackwardArgs& a, hipStream_t
     if (a.rows == 0) {
         const ProductArgs none{nullptr, 0, nullptr, 0, a.width, a.vocab, 0, 1, nullptr, false, 0, 0};
         return product_of<T, true, true>(
-            none, UnitTile<T>{static_cast<T*>(a.dembed), a.ldde, nullptr}, s);
+            none, UnitTile<T>{static_cast<T*>(a.dembed), a.ldde, nullptr}, s, 0, 0);
     }
     if constexpr (sizeof(T) == 2)
         // (0.56 ms against the general form's 1.21 for 8191 tokens x 50304 x 128, 0.48 against
@@ -745,6 +767,7 @@ template <typename T> hipError_t backward(const HeadBackwardArgs& a, hipStream_t
                        p,         b.ld_p,     b.widest};
     hipError_t st = collect<T>(a, g, index, where, selected, s);
     if (st != hipSuccess) return st;
+    Rest<T> rest{};
     for (int64_t i = 0; i < b.pieces; ++i) {
         const int64_t v0 = i * b.piece;
         const int64_t n = i + 1 < b.pieces ? b.piece : a.vocab - v0;
@@ -752,27 +775,36 @@ template <typename T> hipError_t backward(const HeadBackwardArgs& a, hipStream_t
         const ProductArgs lp{embed, a.lde, x, b.ld_x, n, a.rows, a.width, 1, count, false, 0, 0};
         if (a.dentropy != nullptr) {
             const GradTile<T, true> e{terms, p, b.ld_p, v0};
-            st = product_of<T, false, false>(lp, e, s);
+            st = product_of<T, false, false>(lp, e, s, a.width, a.width);
         } else {
             const GradTile<T, false> e{terms, p, b.ld_p, v0};
-            st = product_of<T, false, false>(lp, e, s);
+            st = product_of<T, false, false>(lp, e, s, a.width, a.width);
         }
         if (st != hipSuccess) return st;
         if (a.dx != nullptr) {
-            const ProductArgs dp{embed, a.lde, p, b.ld_p, a.width, a.rows, n, b.slices, count,
+            // (p's rows end in zeros up to whole pieces; a row of the embedding that ends inside a
+            // piece is read on into the next one, but the last of all has none: up to eight rows
+            // are left for the join)
+            int64_t end = n;
+            if (sizeof(T) == 2 && i + 1 == b.pieces && a.width % 8 != 0 &&
+                direct(embed, a.lde, 2, 0)) {
+                end = (n - 1) / 8 * 8;
+                rest = Rest<T>{p, b.ld_p, embed, a.lde, end, n};
+            }
+            const ProductArgs dp{embed, a.lde, p, b.ld_p, a.width, a.rows, end, b.slices, count,
                                  false, b.items, b.most};
             const SumTile e{sums, b.ld_s, i == 0};
-            if ((st = product_of<T, true, false>(dp, e, s, true)) != hipSuccess) return st;
+            if ((st = product_of<T, true, false>(dp, e, s, 0, 0)) != hipSuccess) return st;
         }
         if (a.dembed != nullptr) {
             T* to = static_cast<T*>(a.dembed) + v0 * a.ldde;
             const ProductArgs ep{x, b.ld_x, p, b.ld_p, a.width, n, a.rows, b.slices_e, count, true, 0, 0};
             if (b.slices_e == 1) {
                 const UnitTile<T> e{to, a.ldde, selected};
-                st = product_of<T, true, true>(ep, e, s);
+                st = product_of<T, true, true>(ep, e, s, 0, 0);
             } else {
                 const SumTile e{sums_e, b.ld_s, true};
-                st = product_of<T, true, true>(ep, e, s);
+                st = product_of<T, true, true>(ep, e, s, 0, 0);
                 if (st == hipSuccess)
                     st = join_slices<T>({sums_e, b.ld_s, b.slices_e, 0, 0, 0}, n, a.width, nullptr,
                                         selected, to, a.ldde, s);
@@ -783,7 +815,7 @@ template <typename T> hipError_t backward(const HeadBackwardArgs& a, hipStream_t
     if (a.dx == nullptr) return hipSuccess;
     return join_slices<T>(
         {sums, b.ld_s, 0, b.items, b.most, static_cast<int>(tiles_of(a.width))}, a.rows, a.width,
-        where, selected, static_cast<T*>(a.dx), a.lddx, s);
+        where, selected, static_cast<T*>(a.dx), a.lddx, s, rest);
 }
 
 }  // namespace

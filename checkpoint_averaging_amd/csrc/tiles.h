@@ -761,7 +761,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_direct(ProductArgs 
 // 2048 tokens x 73,760 x 2048 in bf16: 0.62 and 0.90.)
 //
 // Whether an operand can go straight to LDS: rows at multiples of 16 bytes, offsets within a
-// tile in 31 bits, and `along` k whole pieces.
+// tile in 31 bits, and whole pieces of `along` elements (0: whatever a line's last piece holds
+// past its end may be read).
 inline bool direct(const void* p, int64_t ld, int64_t esize, int64_t along) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * esize % 16 == 0 &&
            along * esize % 16 == 0 && ld * esize < int64_t(1) << 23;
