@@ -249,6 +249,7 @@ class LossHead:
         need = max(dh.dl_head_workspace_bytes(r, self.vocab, self.width, embed.dtype, True)
                    for r in range(1, max_rows + 1))
         self._ws = new(max(need, 256), dtype=torch.uint8)
+        self._scored = None              # (rows, address of their sums) that the buffers are of
         need = dh.dl_rmsnorm_workspace_bytes(max_rows, self.width)      # (fewer rows need no more)
         self._norm_ws = new(max(need, 256), dtype=torch.uint8)
 
@@ -270,11 +271,14 @@ class LossHead:
         residual), in fp32 or bf16; sum_, if given, receives x + residual (backward()
         wants it)."""
         rows = self._rows(x, "x")
+        self._scored = None
         dh.dl_rmsnorm(x, rows, self.width, self.weight, self._h, eps=self.eps, residual=residual,
                       sum_=sum_, inv_rms=self._inv)
         logprobs = None if targets is None else self._logprobs[:rows]
         dh.dl_head_logprobs(self._h, self.embed, rows, self.vocab, self.width, targets, logprobs,
                             entropy=self._entropy, stats=self._stats, workspace=self._ws)
+        left = x if residual is None else sum_
+        self._scored = rows, None if left is None else left.data_ptr()
         return Loss(logprobs, self._entropy[:rows], self._stats[:rows])
 
     def backward(self, sum_: torch.Tensor, targets: torch.Tensor, dlogprobs: torch.Tensor,
@@ -285,10 +289,17 @@ class LossHead:
         """The gradients of sum(dlogprobs * logprobs) + sum(dentropy * entropy) (and of
         what gave dsum), after the score() of these targets that left sum_ (or took it
         as x): dx in the stream, dembed, dweight, each written.  The stream has to be of
-        the embedding's type."""
+        the embedding's type.  The norm's output and the statistics are that score()'s, so
+        no other may come between: sum_ has to be the last one's tensor.  (The host's order
+        is what is checked: a graph that holds a score() brings its own backward().)"""
         rows = self._rows(sum_, "sum")
         if sum_.dtype != self.embed.dtype:
             raise ValueError(f"sum: {sum_.dtype}, and the embedding {self.embed.dtype}")
+        if self._scored is None:
+            raise RuntimeError("score() first")
+        scored, at = self._scored
+        if rows != scored or (rows > 0 and at is not None and sum_.data_ptr() != at):
+            raise ValueError(f"sum: not what the last score(), of {scored} rows, left or took")
         dh.dl_head_logprobs_backward(self._h, self.embed, rows, self.vocab, self.width, targets,
                                      self._stats, dlogprobs, dx=self._dh, dembed=dembed,
                                      entropy=None if dentropy is None else self._entropy,
