@@ -1,0 +1,47 @@
+"""Calls of a few tokens over long matrices, as decoding makes them: several turns of rows
+with every wave's columns in use, vectors that are loaded again for each chunk of columns,
+and each number of row and vector tiles; against binary64.  And layouts in 8 bits of more
+tiles than the grid has workgroups."""
+import numpy as np
+import pytest
+
+from tests import test_e4m3_gpu as eg
+from tests import test_head_loss_gpu as lg
+
+pytestmark = pytest.mark.gpu
+
+COUNTS = [1, 16, 17, 32]
+
+
+@pytest.mark.parametrize("rows,cols", [(20_000, 2048), (9000, 5632), (30_011, 2041), (5000, 2304)])
+def test_products_in_8_bits(rows, cols):
+    rng = np.random.default_rng(rows)
+    w, ws, wv = eg.operand(rng, rows, cols, eg.TILE)
+    for count in COUNTS:
+        x, xs, xv = eg.operand(rng, count, cols, eg.BLOCK)
+        for out in ("f32", "bf16"):
+            eg.check_product(eg.product(w, ws, x, xs, out), wv, xv, out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("width", [2048, 2047, 2304, 4500])
+def test_log_probabilities(width, dtype):
+    rng = np.random.default_rng(width)
+    vocab = 20_000 if width < 4000 else 9000
+    x, e, t = lg.inputs(rng, 32, vocab, width)
+    t[5::7] = -1
+    # (the last rows of the vocabulary, too, are some tokens' targets)
+    t[:3] = [vocab - 1, vocab - 2, 0]
+    for count in COUNTS:
+        lg.Case(x[:count], e, t[:count], dtype).forward().check_forward()
+
+
+def test_layout_of_more_tiles_than_workgroups():
+    """16,407 tiles for 16,384 workgroups, neighbours and those 16,384 apart of different
+    magnitude."""
+    rng = np.random.default_rng(6)
+    rows, cols = 2, 2_100_000
+    size = np.repeat(np.exp2(rng.integers(-20, 20, cols // 128 + 1)), 128)[:cols]
+    x = (rng.standard_normal((rows, cols)) * size).astype(np.float32)
+    eg.check_quantize(x, eg.TILE)
+    eg.check_quantize(x, eg.TILE, "bf16")
