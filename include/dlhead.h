@@ -304,13 +304,14 @@ int dl_e4m3_quantize(const void *x, int64_t ldx, int dtype, int64_t rows, int64_
  *   w         rows x cols codes, rows ldw bytes apart;  w_scales its scales.
  *   x         count x cols codes, rows ldx bytes apart;  x_scales its scales.
  *   y         count x rows of y_dtype.  DL_F32: products are exact and summed in
- *             binary32 (block scales are applied in bf16, exact for values of at
- *             least 2^-133; products and partial sums below 2^-126 may count as 0).
+ *             binary32 (products and partial sums below 2^-126 may count as 0).
  *             DL_BF16: the matrix cores' own 8-bit products, which drop low bits
  *             of small addends beside large ones (at most 2^-13 of the sum of
- *             magnitudes of 128 products, some 2e-5 of a typical result), then
- *             bf16's rounding.
+ *             magnitudes of 128 products, some 2e-5 of a typical result), or for
+ *             up to 32 vectors exact ones; then bf16's rounding.
  *
+ * Block scales may be applied in bf16, exact for values of at least 2^-133; an
+ * element that stands for 2^128 or more may count as infinite.
  * Any code and scale byte is accepted.  rows = 0 and count = 0 are no-ops;
  * 1 <= cols, all at most 2^30, rows x count at most 2^43.
  */

@@ -4,8 +4,11 @@ and each number of row and vector tiles; against binary64.  And layouts in 8 bit
 tiles than the grid has workgroups."""
 import numpy as np
 import pytest
+import torch
 
+from oracle import head as oh
 from tests import test_e4m3_gpu as eg
+from tests import test_head_gpu as hg
 from tests import test_head_loss_gpu as lg
 
 pytestmark = pytest.mark.gpu
@@ -45,3 +48,18 @@ def test_layout_of_more_tiles_than_workgroups():
     x = (rng.standard_normal((rows, cols)) * size).astype(np.float32)
     eg.check_quantize(x, eg.TILE)
     eg.check_quantize(x, eg.TILE, "bf16")
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,count", [(64, 4), (64, 20), (64, 40), (6000, 1200)])
+def test_scales_at_the_ends_of_the_range(rows, count, out):
+    """Elements of 448 2^119 and of 2^-133, the largest and the smallest that block scales in
+    bf16 hold, are exact in every form: one product each, whole in bf16."""
+    for code, byte, other in ((0x7E, 246, 27), (0x01, 3, 227), (0x7E, 0, 247)):
+        w, x = (np.zeros((n, 128), np.uint8) for n in (rows, count))
+        w[:, 7], x[:, 7] = code, 0x38                            # 0x38: 1
+        ws = torch.full((eg.groups(eg.TILE, rows), 1), byte, dtype=torch.uint8, device=eg.DEV)
+        xs = torch.full((count, 1), other, dtype=torch.uint8, device=eg.DEV)
+        dev = lambda v: torch.from_numpy(v).to(eg.DEV).view(torch.float8_e4m3fn)  # noqa: E731
+        want = oh.e4m3_value(np.array([code], np.uint8))[0] * 2.0 ** (byte - 127 + other - 127)
+        hg.same_bits(eg.product(dev(w), ws, dev(x), xs, out), np.full((count, rows), want), out)
