@@ -343,13 +343,13 @@ template <typename T> __global__ __launch_bounds__(256) void k_gather(GatherArgs
                 a.terms[j] = r;
             } else {
                 const float m = r.m == -__builtin_inff() ? 0.0f : r.m;
-                a.narrow[j] = (m + r.log_s) * kLog2e;
-                a.narrow[a.rows + j] = -r.a;
-                a.narrow[2 * a.rows + j] = __int_as_float(r.target);
-                a.narrow[3 * a.rows + j] = m;
-                a.narrow[4 * a.rows + j] = r.log_s;
-                a.narrow[5 * a.rows + j] = -r.a - r.b * r.entropy;
-                a.narrow[6 * a.rows + j] = -r.b * kLn2;
+                const float base = (m + r.log_s) * kLog2e, other = -r.b * kLn2;
+                // (what log2(p) of the largest logit lacks)
+                const float lack = -r.log_s * kLog2e - __builtin_fmaf(m, kLog2e, -base);
+                const float of_h = other * lack - r.b * r.entropy;
+                const float terms[kNarrowTerms] = {
+                    base, -r.a, __int_as_float(r.target), m, r.log_s, of_h - r.a, other, of_h};
+                for (int k = 0; k < kNarrowTerms; ++k) a.narrow[k * a.rows + j] = terms[k];
             }
         }
     }
@@ -375,7 +375,9 @@ template <typename T, bool ENTROPY> struct GradTile {
             // (a row of masked tokens only: their log probabilities are the logits)
             const float from = r.m == -__builtin_inff() ? 0.0f : r.m;
             auto gradient = [&](float l, bool target) {
-                const float lp = (l - from) - r.log_s, x = exp_of(lp);
+                float lp = (l - from) - r.log_s;
+                if ((ENTROPY || target) && lp > kCertain) lp = -r.log_s;
+                const float x = exp_of(lp);
                 const float h = ENTROPY && x > 0 ? r.b * x * (lp + r.entropy) : 0.0f;
                 // (1 - p of the target keeps its digits)
                 return x != x ? x : -r.a * (target ? expm1f(lp) : x) - h;
@@ -705,6 +707,7 @@ hipError_t narrow_backward(const HeadBackwardArgs& a, hipStream_t s) {
     bf16* x = reinterpret_cast<bf16*>(ws + b.x);
     float* sums = reinterpret_cast<float*>(ws + b.sums);
     const int width = static_cast<int>(a.width);
+    const bool few = a.rows <= kFewTokens;
     const GatherArgs g{a.x,     a.ldx,     a.rows,      a.vocab,    width, a.targets,
                        a.stats, a.entropy, a.dlogprobs, a.dentropy, index, selected,
                        x,       b.ld_x,    nullptr,     terms,      nullptr, 0, 0};
@@ -715,7 +718,8 @@ hipError_t narrow_backward(const HeadBackwardArgs& a, hipStream_t s) {
     if (a.dx != nullptr) {
         const NarrowArgs k{x,       b.ld_x,           a.rows, embed,           a.lde, a.vocab, width,
                            b.items, b.most, &selected->count, 0, {terms, a.rows}, sums, b.ld_s};
-        (a.dentropy != nullptr ? k_narrow<true, true> : k_narrow<true, false>)
+        (a.dentropy == nullptr ? k_narrow<true, false>
+         : few                ? k_narrow<true, true, true> : k_narrow<true, true>)
             <<<dim3(static_cast<unsigned>(slice_rows(a.rows, b.items, b.most, 1) / 256)),
                dim3(kTileThreads), 0, s>>>(k);
         if ((st = hipGetLastError()) != hipSuccess) return st;
@@ -728,7 +732,8 @@ hipError_t narrow_backward(const HeadBackwardArgs& a, hipStream_t s) {
         const int64_t n = a.vocab - v0 < b.piece ? a.vocab - v0 : b.piece;
         const NarrowArgs k{embed + v0 * a.lde, a.lde, n, x, b.ld_x, a.rows, width,
                            b.slices_e, 0, &selected->count, v0, {terms, a.rows}, sums, b.ld_s};
-        (a.dentropy != nullptr ? k_narrow<false, true> : k_narrow<false, false>)
+        (a.dentropy == nullptr ? k_narrow<false, false>
+         : few                ? k_narrow<false, true, true> : k_narrow<false, true>)
             <<<dim3(static_cast<unsigned>(tiles_of(n) * b.slices_e)), dim3(kTileThreads), 0, s>>>(k);
         if ((st = hipGetLastError()) != hipSuccess) return st;
         st = join_slices<bf16>({sums, b.ld_s, b.slices_e, 0, 0, 0}, n, a.width, nullptr, selected,

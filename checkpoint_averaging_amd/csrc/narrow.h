@@ -30,11 +30,22 @@ namespace dlk {
 constexpr int kNarrow = 128;             // elements of a row, with zeros from its width on
 constexpr int kNarrowStill = kTileWaves * kSquare, kNarrowUnit = 128;
 constexpr int kNarrowRing = 4, kNarrowBytes = kNarrowUnit * kNarrow * 2;
-constexpr int kNarrowTerms = 7;
+constexpr int kNarrowTerms = 8;
+
+// A token whose log probability comes out above this has the row's largest logit, m: its log
+// probability is -log S.  (Formed from a logit that is summed in another order than the
+// forward pass's, it would lose all digits of a 1 - p, or of a log p + H, that are below the
+// logit's last place.)
+constexpr float kCertain = -0.25f;
 
 // A row's terms, an array of `rows` for each: (m + log S) log2(e), -a, its target (or -1),
-// m (0 if that is -infinity), log S; and, with a gradient b of the entropies, -a - b H and
-// -b log(2): d = p (one + other log2(p)) + a delta_t.
+// m (0 if that is -infinity), log S; and, with a gradient b of the entropies, -a - b H,
+// -b log(2) and -b H: d = p (one + other log2(p)) + a delta_t.
+//
+// The first is one binary32 number, so log2(p) = l log2(e) less it is off by up to three
+// roundings of the logit's own size (the general form subtracts m first), the same for all of
+// a row.  p moves by as much, relatively; from log p + H it is taken out: -b H has what is
+// missing in log2(p) added, times -b log(2).
 struct NarrowTerms {
     const float* of;
     int64_t rows;
@@ -63,7 +74,8 @@ struct NarrowArgs {
 // rows, meet all banks.
 __device__ __forceinline__ int narrow_key(int row) { return (row & 3) << 2 | (row >> 2 & 3); }
 
-template <bool TOKENS_STILL, bool ENTROPY>
+// FEW: the forward pass was a few tokens', whose logits are summed in another order.
+template <bool TOKENS_STILL, bool ENTROPY, bool FEW = false>
 __global__ __launch_bounds__(kTileThreads, 2) void k_narrow(NarrowArgs a) {
     constexpr float kLog2e = 0x1.715476p+0f;
     constexpr int kSubs = kNarrow / 16, kWide = kNarrow / kSquare, kMine = kNarrowBytes / 16 / kTileThreads;
@@ -120,7 +132,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_narrow(NarrowArgs a) {
                 const_cast<float*>(term_of), 0, have * 4, 0x00020000);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(t, (lds_any*)to, 4, term_offset, 0, 0, 0);
             t = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(term_of + 4 * a.terms.rows), 0,
-                                                  wave < (ENTROPY ? 6 : 2) ? have * 4 : 0, 0x00020000);
+                                                  wave < (ENTROPY ? 8 : 2) ? have * 4 : 0, 0x00020000);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(t, (lds_any*)(to + 4 * kNarrowUnit), 4,
                                                      term_offset, 0, 0, 0);
             term_of += kNarrowUnit;
@@ -137,7 +149,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_narrow(NarrowArgs a) {
             v = *reinterpret_cast<const u32x4*>(a.still + n * a.ld_still + k);
         still[s] = __builtin_bit_cast(bf16x8, v);
     }
-    float base2 = 0, mine = 0, top = 0, log_s = 0, one = 0, other = 0;
+    float base2 = 0, mine = 0, top = 0, log_s = 0, one = 0, other = 0, of_h = 0;
     int target = -1;
     if constexpr (TOKENS_STILL) {
         if (there) {
@@ -149,6 +161,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_narrow(NarrowArgs a) {
             if constexpr (ENTROPY) {
                 one = a.terms.get(5, n);
                 other = a.terms.get(6, n);
+                of_h = a.terms.get(7, n);
             }
         }
     }
@@ -198,6 +211,23 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_narrow(NarrowArgs a) {
                 const int row0 = pair * 64 + t * 32;          // of the unit
                 // element i is of row row0 + 8 (i / 4) + 4 half + i % 4
                 float v[16];
+                // (looked for there only: 58 us for 53 of dx, and 43 for 40 of dembed, for 20
+                // tokens x 50,304 x 128; 8 to 12 in 100 more for 8191)
+                if constexpr (FEW) {
+                    float e[16], most = kCertain * kLog2e;
+                    for (int i = 0; i < 16; ++i) {
+                        const int r = row0 + 8 * (i / 4) + 4 * half + i % 4;
+                        e[i] = power(s[t][i], TOKENS_STILL ? base2 : lds_terms[slot][0][r]);
+                        // (rows past the end are zeros, which are not looked for)
+                        if (TOKENS_STILL ? there : u * kNarrowUnit + r < rows) most = fmaxf(most, e[i]);
+                    }
+                    if (__any(most > kCertain * kLog2e))
+                        for (int i = 0; i < 16; ++i) {
+                            const int r = row0 + 8 * (i / 4) + 4 * half + i % 4;
+                            const float m = TOKENS_STILL ? top : lds_terms[slot][3][r];
+                            s[t][i] = e[i] > kCertain * kLog2e ? m : s[t][i];
+                        }
+                }
                 if constexpr (TOKENS_STILL) {
                     for (int i = 0; i < 16; ++i) {
                         const float e = power(s[t][i], base2);
@@ -208,11 +238,12 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_narrow(NarrowArgs a) {
                     if (__any(at >= 0 && at < 32)) {
                         for (int i = 0; i < 16; ++i)
                             if (at == 8 * (i / 4) + 4 * half + i % 4) {
-                                const float less = expm1f((s[t][i] - top) - log_s);
+                                const float lp = (s[t][i] - top) - log_s;
+                                const float less = expm1f(lp > kCertain ? -log_s : lp);
                                 if constexpr (ENTROPY) {
                                     const float e = power(s[t][i], base2);
                                     v[i] = mine * less + __builtin_amdgcn_exp2f(e) *
-                                                             weight(e, one - mine, other);
+                                                             weight(e, of_h, other);
                                 } else {
                                     v[i] = less;
                                 }
@@ -253,12 +284,11 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_narrow(NarrowArgs a) {
                             for (int i = 0; i < 16; ++i) {
                                 const int r = row0 + 8 * (i / 4) + 4 * half + i % 4;
                                 if (!(certain >> i & 1)) continue;
-                                v[i] = terms[1][r] *
-                                       expm1f((s[t][i] - terms[3][r]) - terms[4][r]);
+                                v[i] = terms[1][r] * expm1f(-terms[4][r]);
                                 if constexpr (ENTROPY) {
                                     const float e = power(s[t][i], terms[0][r]);
                                     v[i] += __builtin_amdgcn_exp2f(e) *
-                                            weight(e, terms[5][r] - terms[1][r], terms[6][r]);
+                                            weight(e, terms[7][r], terms[6][r]);
                                 }
                             }
                         }
