@@ -63,3 +63,11 @@ def test_scales_at_the_ends_of_the_range(rows, count, out):
         dev = lambda v: torch.from_numpy(v).to(eg.DEV).view(torch.float8_e4m3fn)  # noqa: E731
         want = oh.e4m3_value(np.array([code], np.uint8))[0] * 2.0 ** (byte - 127 + other - 127)
         hg.same_bits(eg.product(dev(w), ws, dev(x), xs, out), np.full((count, rows), want), out)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_a_short_matrix_times_many_vectors(out):
+    rng = np.random.default_rng(7)
+    w, ws, wv = eg.operand(rng, 70, 136, eg.TILE)
+    x, xs, xv = eg.operand(rng, 200_003, 136, eg.BLOCK)
+    eg.check_product(eg.product(w, ws, x, xs, out), wv, xv, out)

@@ -86,3 +86,28 @@ def test_sums_over_a_long_vocabulary(vocab, rows):
     hg.within(lp, want, off, "logprobs")
     # the entropy's second term is the mean of the distances, whose sum has S's error too
     hg.within(h, np.full(rows, log_s - rest * other / (tops + rest)), 2 * off, "entropy")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [2, 20, 40])
+def test_the_widest_rows(rows, dtype):
+    rng = np.random.default_rng(rows)
+    x, e, t = lg.inputs(rng, rows, 300, dh.DL_MAX_NORM_COLS)
+    t[1::5] = -1
+    a, b = lg.weights(rng, rows, True)
+    lg.Case(x, e, t, dtype, 0, b, a).forward().check_forward().backward().check_backward()
+
+
+@pytest.mark.parametrize("dtype,width", [("bf16", 24), ("bf16", 136), ("f32", 24)])
+@pytest.mark.parametrize("part", [0.01, 0.9])
+def test_many_rows(part, width, dtype):
+    """More rows than the products' slices and the gradients' walkers take at once, of which
+    few or most have a target."""
+    rng = np.random.default_rng(width)
+    rows, vocab = 300_001, 70
+    x, e, t = lg.inputs(rng, rows, vocab, width)
+    t[rng.random(rows) > part] = -1
+    a, _ = lg.weights(rng, rows, False)
+    c = lg.Case(x, e, t, dtype, 0, None, a).forward().check_forward()
+    c.backward().check_backward()
+    assert not hg.host(c.dx)[t < 0].any()
