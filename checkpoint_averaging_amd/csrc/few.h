@@ -8,9 +8,9 @@
 // take other rows) and keep the vectors' parts in registers, as the matrix
 // instruction (16 rows x 16 vectors x 32 columns) wants them; past kw * STEPS * 32
 // columns they are loaded again for every chunk of them.  The next rows are under way
-// while these are multiplied.  Four neighbouring lanes load 64 bytes of a row.  The
-// waves' sums meet in LDS, where one thread a result adds them and hands it to the
-// epilogue.
+// while these are multiplied.  One load has 64 bytes of each of 16 rows, by four lanes
+// 16 apart (of binary32 every other 16 of 128).  The waves' sums meet in LDS, where one
+// thread a result adds them and hands it to the epilogue.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -14,10 +14,11 @@
 //
 // Backward: the rows that have a part are gathered first, so that a product has as many
 // columns as there are of them (a masked-token loss has targets at its masked positions only);
-// then the logits again, piece by piece of the vocabulary (128 MB of d at a time: with 72 the
-// products' last tiles cost 0.6 in 100 more, with 48 17 in 100; with 256 3 in 100 more here,
-// and 8 less at a width of 128), d in memory, and its two products.  2048 rows x 73760 x 2048
-// in bf16: 2.23 ms for 1.86 TFLOP.  Rows of at most 128 numbers keep d in registers
+// then the logits again, piece by piece of the vocabulary, d in memory, and its two products.
+// 2048 rows, all with a target, x 73760 x 2048 in bf16: 1.92 ms for 1.86 TFLOP.  A piece is
+// 128 MB of d: here 96 x 8 tiles, three whole turns of the 256 workgroups (with 72 MB 0.6 in
+// 100 more, with 48 17, with 256 3; other sizes fall between turns with any of them, and a
+// width of 128 took 8 in 100 less with 256).  Rows of at most 128 numbers keep d in registers
 // (narrow.h).
 #include <hip/hip_runtime.h>
 #include <stdint.h>

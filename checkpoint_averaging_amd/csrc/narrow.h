@@ -12,8 +12,8 @@
 // 32 moving rows in its column, which is what the second one takes of its own operand if the
 // rows are counted in that order.  d is rounded to bf16 for it, as the general form's is.
 //
-// 8191 tokens x 50304 x 128: dx 0.21 ms, dembed 0.29 (with an entropy's gradient 0.24 and
-// 0.33), 0.21 TFLOP each: 0.64 to 1 PFLOP/s, which the exponentials and conversions between
+// 8191 tokens x 50304 x 128: dx 0.21 ms, dembed 0.29 (with an entropy's gradient 0.23 and
+// 0.28), 0.21 TFLOP each: 0.64 to 1 PFLOP/s, which the exponentials and conversions between
 // the products bound (some 8 vector instructions an element beside its two matrix
 // instructions' share).  Through memory the gradient in the logits was 824 MB written and
 // twice read, and the two and its own product took 1.1 ms.
@@ -219,7 +219,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_narrow(NarrowArgs a) {
                         const int r = row0 + 8 * (i / 4) + 4 * half + i % 4;
                         e[i] = power(s[t][i], TOKENS_STILL ? base2 : lds_terms[slot][0][r]);
                         // (rows past the end are zeros, which are not looked for)
-                        if (TOKENS_STILL ? there : u * kNarrowUnit + r < rows) most = fmaxf(most, e[i]);
+                        if (TOKENS_STILL ? there : u * kNarrowUnit + r < rows)
+                            most = fmaxf(most, e[i]);
                     }
                     if (__any(most > kCertain * kLog2e))
                         for (int i = 0; i < 16; ++i) {

@@ -757,8 +757,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_product_direct(ProductArgs 
     __builtin_amdgcn_s_waitcnt(0x0F70);
 }
 
-// (8192^3 of codes with a bf16 result, straight against through registers: 0.51 and 1.17 ms;
-// 2048 tokens x 73,760 x 2048 in bf16: 0.62 and 0.90.)
+// (8192^3 of codes with a bf16 result, straight against through registers: 0.47 and 1.10 ms, or
+// 1.00 with one operand of odd rows; 2048 tokens x 73,760 x 2048 in bf16: 0.53 and 0.74.)
 //
 // Whether an operand can go straight to LDS: rows at multiples of 16 bytes, offsets within a
 // tile in 31 bits, and whole pieces of `along` elements (0: whatever a line's last piece holds

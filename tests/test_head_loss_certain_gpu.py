@@ -50,7 +50,8 @@ def test_each_row_keeps_its_digits(width, entropy, rows, dtype):
         # it; what of that is taken out of log p + H again has four roundings of its own (the
         # lack, its product, the sum with b H, and of both in the kernel).
         if dtype == "bf16" and width <= 128:
-            off = off + 12 * hg.U ** 2 * (np.abs(b) * (np.abs(c.m) + c.log_s))[:, None] * np.exp(c.lp)
+            size = np.abs(b) * (np.abs(c.m) + c.log_s)
+            off = off + 12 * hg.U ** 2 * size[:, None] * np.exp(c.lp)
     # (both parts of d may be rounded before they are added)
     off = off + hg.HALF[dtype] * np.abs(d) + 4 * hg.U * mag
     terms = (6 if dtype == "f32" else 1) * max(vocab, rows) + 40
