@@ -708,7 +708,7 @@ hipError_t narrow_backward(const HeadBackwardArgs& a, hipStream_t s) {
     bf16* x = reinterpret_cast<bf16*>(ws + b.x);
     float* sums = reinterpret_cast<float*>(ws + b.sums);
     const int width = static_cast<int>(a.width);
-    const bool few = a.rows <= kFewTokens;
+    const bool few = a.rows <= kFewTokens, h = a.dentropy != nullptr;
     const GatherArgs g{a.x,     a.ldx,     a.rows,      a.vocab,    width, a.targets,
                        a.stats, a.entropy, a.dlogprobs, a.dentropy, index, selected,
                        x,       b.ld_x,    nullptr,     terms,      nullptr, 0, 0};
@@ -719,8 +719,13 @@ hipError_t narrow_backward(const HeadBackwardArgs& a, hipStream_t s) {
     if (a.dx != nullptr) {
         const NarrowArgs k{x,       b.ld_x,           a.rows, embed,           a.lde, a.vocab, width,
                            b.items, b.most, &selected->count, 0, {terms, a.rows}, sums, b.ld_s};
-        (a.dentropy == nullptr ? k_narrow<true, false>
-         : few                ? k_narrow<true, true, true> : k_narrow<true, true>)
+        const auto to_lds = [&](auto straight) {
+            constexpr bool kStraight = decltype(straight)::value;
+            return !h ? k_narrow<true, false, false, kStraight>
+                   : few ? k_narrow<true, true, true, kStraight>
+                         : k_narrow<true, true, false, kStraight>;
+        };
+        (direct(embed, a.lde, 2, a.width) ? to_lds(std::true_type{}) : to_lds(std::false_type{}))
             <<<dim3(static_cast<unsigned>(slice_rows(a.rows, b.items, b.most, 1) / 256)),
                dim3(kTileThreads), 0, s>>>(k);
         if ((st = hipGetLastError()) != hipSuccess) return st;
@@ -733,8 +738,8 @@ hipError_t narrow_backward(const HeadBackwardArgs& a, hipStream_t s) {
         const int64_t n = a.vocab - v0 < b.piece ? a.vocab - v0 : b.piece;
         const NarrowArgs k{embed + v0 * a.lde, a.lde, n, x, b.ld_x, a.rows, width,
                            b.slices_e, 0, &selected->count, v0, {terms, a.rows}, sums, b.ld_s};
-        (a.dentropy == nullptr ? k_narrow<false, false>
-         : few                ? k_narrow<false, true, true> : k_narrow<false, true>)
+        (!h ? k_narrow<false, false, false, true>
+         : few ? k_narrow<false, true, true, true> : k_narrow<false, true, false, true>)
             <<<dim3(static_cast<unsigned>(tiles_of(n) * b.slices_e)), dim3(kTileThreads), 0, s>>>(k);
         if ((st = hipGetLastError()) != hipSuccess) return st;
         st = join_slices<bf16>({sums, b.ld_s, b.slices_e, 0, 0, 0}, n, a.width, nullptr, selected,
@@ -754,8 +759,7 @@ template <typename T> hipError_t backward(const HeadBackwardArgs& a, hipStream_t
         // (0.56 ms against the general form's 1.21 for 8191 tokens x 50304 x 128, 0.48 against
         // 1.04 with a width of 16, 0.079 against 0.149 for 100 tokens, 0.040 against 0.067 for
         // 100 x 1000)
-        if (a.width <= kNarrow && direct(a.embed, a.lde, 2, a.width))
-            return narrow_backward(a, s);
+        if (a.width <= kNarrow && a.width % 8 == 0) return narrow_backward(a, s);
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     const Backward b = backward_plan(a.rows, a.vocab, a.width, sizeof(T));
     int* index = reinterpret_cast<int*>(ws + b.index);
@@ -790,10 +794,9 @@ template <typename T> hipError_t backward(const HeadBackwardArgs& a, hipStream_t
         if (a.dx != nullptr) {
             // (p's rows end in zeros up to whole pieces; a row of the embedding that ends inside a
             // piece is read on into the next one, but the last of all has none: up to eight rows
-            // are left for the join)
+            // are left for the join, where nothing is read so too, for the same results)
             int64_t end = n;
-            if (sizeof(T) == 2 && i + 1 == b.pieces && a.width % 8 != 0 &&
-                direct(embed, a.lde, 2, 0)) {
+            if (sizeof(T) == 2 && i + 1 == b.pieces && a.width % 8 != 0) {
                 end = (n - 1) / 8 * 8;
                 rest = Rest<T>{p, b.ld_p, embed, a.lde, end, n};
             }

@@ -75,7 +75,9 @@ struct NarrowArgs {
 __device__ __forceinline__ int narrow_key(int row) { return (row & 3) << 2 | (row >> 2 & 3); }
 
 // FEW: the forward pass was a few tokens', whose logits are summed in another order.
-template <bool TOKENS_STILL, bool ENTROPY, bool FEW = false>
+// STRAIGHT: the moving rows go to LDS straight; otherwise, at any alignment, through
+// registers, with the same results (dx of 8191 tokens x 50304 x 128: 255 us for 216).
+template <bool TOKENS_STILL, bool ENTROPY, bool FEW, bool STRAIGHT>
 __global__ __launch_bounds__(kTileThreads, 2) void k_narrow(NarrowArgs a) {
     constexpr float kLog2e = 0x1.715476p+0f;
     constexpr int kSubs = kNarrow / 16, kWide = kNarrow / kSquare, kMine = kNarrowBytes / 16 / kTileThreads;
@@ -102,30 +104,45 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_narrow(NarrowArgs a) {
     const bool there = n < still_rows;
 
     // ---- the way of the moving rows to LDS: rows that are not there are zeros
-    const int row_bytes = static_cast<int>(a.ld_moving * 2);
+    const int64_t row_bytes = a.ld_moving * 2;
     const int line = threadIdx.x / 16, piece = threadIdx.x % 16 ^ narrow_key(line);
     uint32_t offset[kMine];
     for (int j = 0; j < kMine; ++j)
         offset[j] = piece * 8 < a.width
-                        ? static_cast<uint32_t>(line + j * 32) * row_bytes + piece * 16
+                        ? (line + j * 32) * static_cast<uint32_t>(row_bytes) + piece * 16
                         : 0xFFFFFFF0u;
     const uint8_t* base = reinterpret_cast<const uint8_t*>(a.moving) +
-                          static_cast<int64_t>(from) * row_bytes;
+                          from * row_bytes;
     const float* term_base = a.terms.of + from;
     const uint32_t term_offset = static_cast<uint32_t>(threadIdx.x % kNarrowUnit) * 4;
     // (a wave's places are of half of a term)
     const float* term_of = term_base + wave / 2 * a.terms.rows;
     int left = rows;                      // not sent for yet
     auto fetch = [&](int slot) {
+        if constexpr (!STRAIGHT) {
+            static_assert(TOKENS_STILL, "their terms' way is straight");
+            u32x4 v[kMine];
+            for (int j = 0; j < kMine; ++j) {
+                v[j] = u32x4{};
+                if (line + j * 32 < left && piece * 8 < a.width)
+                    v[j] = *reinterpret_cast<const Raw<bf16>::any*>(
+                        base + (line + j * 32) * row_bytes + piece * 16);
+            }
+            for (int j = 0; j < kMine; ++j)
+                *reinterpret_cast<u32x4*>(lds[slot] + (j * kTileThreads + threadIdx.x) * 16) = v[j];
+            base += kNarrowUnit * row_bytes;
+            left -= kNarrowUnit;
+            return;
+        }
         typedef __attribute__((address_space(3))) void lds_any;
         const int have = __builtin_elementwise_max(__builtin_elementwise_min(left, kNarrowUnit), 0);
         __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<uint8_t*>(base), 0, static_cast<uint32_t>(have) * row_bytes, 0x00020000);
+            const_cast<uint8_t*>(base), 0, static_cast<uint32_t>(have * row_bytes), 0x00020000);
         for (int j = 0; j < kMine; ++j)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 r, (lds_any*)(lds[slot] + wave * (kWave * 16) + j * (kTileThreads * 16)), 16,
                 offset[j], 0, 0, 0);
-        base += static_cast<int64_t>(kNarrowUnit) * row_bytes;
+        base += kNarrowUnit * row_bytes;
         if constexpr (!TOKENS_STILL) {
             float* to = &lds_terms[slot][0][0] + wave * kWave;
             __amdgpu_buffer_rsrc_t t = __builtin_amdgcn_make_buffer_rsrc(
@@ -146,7 +163,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_narrow(NarrowArgs a) {
         const int k = s * 16 + half * 8;
         u32x4 v{};
         if (there && k < a.width)
-            v = *reinterpret_cast<const u32x4*>(a.still + n * a.ld_still + k);
+            v = *reinterpret_cast<const Raw<bf16>::any*>(a.still + n * a.ld_still + k);
         still[s] = __builtin_bit_cast(bf16x8, v);
     }
     float base2 = 0, mine = 0, top = 0, log_s = 0, one = 0, other = 0, of_h = 0;
@@ -239,8 +256,9 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_narrow(NarrowArgs a) {
                     if (__any(at >= 0 && at < 32)) {
                         for (int i = 0; i < 16; ++i)
                             if (at == 8 * (i / 4) + 4 * half + i % 4) {
+                                // (with ENTROPY a certain token's logit is m itself here)
                                 const float lp = (s[t][i] - top) - log_s;
-                                const float less = expm1f(lp > kCertain ? -log_s : lp);
+                                const float less = expm1f(!ENTROPY && lp > kCertain ? -log_s : lp);
                                 if constexpr (ENTROPY) {
                                     const float e = power(s[t][i], base2);
                                     v[i] = mine * less + __builtin_amdgcn_exp2f(e) *
